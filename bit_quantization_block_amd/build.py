@@ -71,6 +71,7 @@ def build(out: str = LIB, defines=(), build_dir: str | None = None, jobs: int = 
               for dt in range(3) for odt in range(3)]
     units += [("lq_fast.hip", f"lq_fast_{dt}.o", [f"-DLQ_FAST_DT={dt}"]) for dt in range(2)]
     units += [("lq_lc.hip", "lq_lc.o", []), ("lq_h16.hip", "lq_h16.o", [])]
+    units += [(f"{u}.hip", f"{u}.o", []) for u in ("lq_linear", "lq_mx4", "lq_grad", "lq_swiglu")]
     ceiling = ("lq_ceiling.hip", "lq_ceiling.o", [])
     cmds = []
     for src, obj, extra in units + [ceiling]:

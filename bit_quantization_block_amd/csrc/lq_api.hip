@@ -712,7 +712,7 @@ const char* lq_status_string(int status) {
     case LQ_ERR_ALIGN: return "a device pointer is not 16-byte aligned";
     case LQ_ERR_WORKSPACE: return "workspace missing or too small";
     case LQ_ERR_HIP: return "HIP launch failed";
-    case LQ_ERR_UNSUPPORTED: return "block size not built (use 16, 32, 64, 128 or 256)";
+    case LQ_ERR_UNSUPPORTED: return "not built (blocks: 16, 32, 64, 128 or 256; see lq.h for the linear layer's types)";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,196 @@
+// lq_linear.h — device-side pieces shared by the low-bit linear layer's kernels
+// (lq_mx4.hip, lq_grad.hip, lq_swiglu.hip) and the launchers that lq_linear.hip
+// calls.
+//
+// Two stored forms of a rows x cols matrix, both in blocks of 32 along a row
+// with one UE8M0 scale each, the smallest 2^e with Qmax * 2^e >= max|block|:
+//   MX4 operand    E2M1 codes, rows padded with zeros to 256 elements (128
+//                  bytes), scale rows padded to 16 bytes: a row's codes and
+//                  scales can be read 16 bytes at a time whatever cols is
+//   8-bit checkpoint  INT8 or E4M3 codes, rows padded with zeros to 32
+//                  elements; one scale byte per block
+// For cols a multiple of 512 (MX4) or 32 (checkpoint) they are byte for byte
+// what lq_quantize writes for E2M1 / INT8 / E4M3, PER_BLOCK 32, UE8M0.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "lq.h"
+#include "lq_device.h"
+
+namespace lql {
+
+constexpr int kBlock = 32;
+
+__host__ __device__ inline int64_t mx4_pitch(int64_t cols) { return (cols + 255) / 256 * 128; }        // bytes of a code row
+__host__ __device__ inline int64_t mx4_scale_pitch(int64_t cols) { return (cols + 511) / 512 * 16; }   // bytes of a scale row
+__host__ __device__ inline int64_t ckpt_pitch(int64_t cols) { return (cols + 31) / 32 * 32; }
+__host__ __device__ inline int64_t ckpt_scale_pitch(int64_t cols) { return (cols + 31) / 32; }
+
+// ------------------------------------------------------------ floats in memory
+template <int DT> struct El;
+template <> struct El<LQ_F32> { typedef float T; static constexpr int bytes = 4; };
+template <> struct El<LQ_BF16> { typedef uint16_t T; static constexpr int bytes = 2; };
+template <> struct El<LQ_F16> { typedef uint16_t T; static constexpr int bytes = 2; };
+
+template <int DT>
+__device__ __forceinline__ float widen(typename El<DT>::T b) {
+  if constexpr (DT == LQ_F32) return b;
+  else if constexpr (DT == LQ_BF16) return __uint_as_float((uint32_t)b << 16);
+  else return (float)__builtin_bit_cast(_Float16, b);
+}
+// Round to the stored type, to nearest even (bf16 through the compiler's own
+// conversion, one instruction on gfx950).
+template <int DT>
+__device__ __forceinline__ typename El<DT>::T narrow(float f) {
+  if constexpr (DT == LQ_F32) return f;
+  else if constexpr (DT == LQ_BF16) return __builtin_bit_cast(uint16_t, (__bf16)f);
+  else return __builtin_bit_cast(uint16_t, (_Float16)f);
+}
+
+// Eight consecutive elements of a row, the first `valid` of which exist; the
+// rest are zero. Rows need not start at a multiple of 16 bytes (the caller's
+// row stride is any number of elements): the vector loads carry the element's
+// alignment, which gfx950's global memory instructions take as they are.
+template <int DT>
+__device__ __forceinline__ void load8(const void* row, int64_t col, int valid, float v[8]) {
+  typedef typename El<DT>::T T;
+  const T* p = (const T*)row + col;
+  T t[8];
+  if (valid >= 8) {
+    __builtin_memcpy(t, p, sizeof(t));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) t[i] = i < valid ? p[i] : (T)0;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = widen<DT>(t[i]);
+}
+template <int DT>
+__device__ __forceinline__ void store8(void* row, int64_t col, int valid, const float v[8]) {
+  typedef typename El<DT>::T T;
+  T* p = (T*)row + col;
+  T t[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) t[i] = narrow<DT>(v[i]);
+  if (valid >= 8) {
+    __builtin_memcpy(p, t, sizeof(t));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      if (i < valid) p[i] = t[i];
+  }
+}
+
+// ------------------------------------------------------------ block scales
+// A scale byte from the bits of max|block|. Qmax = 2^(qexp-1) * (1 + f): the
+// exponent field of amax, one more if amax's significand is above Qmax's,
+// less Qmax's own exponent; clamped at 2^-127. A block that holds an infinity
+// or a NaN (whose bits, without the sign, are the largest) gets the NaN scale
+// 0xFF, and what is computed from it is NaN: a spoiled activation shows.
+template <int F> struct Sig;   // significand field of Qmax
+template <> struct Sig<LQ_E2M1> { static constexpr uint32_t bits = 0x400000u; };   // 1.5
+template <> struct Sig<LQ_INT8> { static constexpr uint32_t bits = 0x7E0000u; };   // 127 / 64
+template <> struct Sig<LQ_E4M3> { static constexpr uint32_t bits = 0x600000u; };   // 1.75
+constexpr uint32_t kInfBits = 0x7F800000u;
+template <int F>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+  const int e = (int)((amax_bits + (0x7FFFFFu - Sig<F>::bits)) >> 23) + 1 - lqd::Fmt<F>::qexp;
+  return amax_bits >= kInfBits ? 255u : (uint32_t)(e < 0 ? 0 : e);
+}
+// 2^-e of a finite scale byte (e = byte - 127), exact; 0 for the NaN scale,
+// whose block's codes are all zero.
+__device__ __forceinline__ float scale_recip(uint32_t byte) {
+  return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+// The scale's value: 2^(byte-127), subnormal for byte 0, NaN for 0xFF (both
+// are the exponent field with the top fraction bit set).
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float((byte << 23) | ((byte == 0u || byte == 255u) ? 0x00400000u : 0u));
+}
+
+// max over the four lanes of a quad, in all four
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);
+  v = v > o ? v : o;
+  o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);
+  return v > o ? v : o;
+}
+__device__ __forceinline__ uint32_t amax8_bits(const float v[8]) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    a = a > b ? a : b;
+  }
+  return a;
+}
+
+// Eight elements of one block as codes; r the scale's reciprocal, 0 for the
+// NaN scale (an infinite or NaN element times 0 is NaN, so the codes are
+// cleared explicitly).
+__device__ __forceinline__ uint32_t encode_e2m1(const float v[8], float r) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) q[i] = v[i] * r;
+  return r == 0.0f ? 0u : lqd::fp4_pack8(q);
+}
+template <int F>
+__device__ __forceinline__ uint2 encode8(const float v[8], float r) {
+  uint2 w;
+  if constexpr (F == LQ_INT8) {
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) c[i] = (uint32_t)(int)__builtin_rintf(lqd::clampf(v[i] * r, -127.0f, 127.0f));
+    w.x = (c[0] & 0xFFu) | ((c[1] & 0xFFu) << 8) | ((c[2] & 0xFFu) << 16) | (c[3] << 24);
+    w.y = (c[4] & 0xFFu) | ((c[5] & 0xFFu) << 8) | ((c[6] & 0xFFu) << 16) | (c[7] << 24);
+  } else {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) q[i] = lqd::clampf(v[i] * r, -448.0f, 448.0f);
+    w.x = lqd::fp8_pack4<LQ_E4M3>(q[0], q[1], q[2], q[3]);
+    w.y = lqd::fp8_pack4<LQ_E4M3>(q[4], q[5], q[6], q[7]);
+  }
+  if (r == 0.0f) w = make_uint2(0u, 0u);
+  return w;
+}
+// The values of four 8-bit codes times the scale.
+template <int F>
+__device__ __forceinline__ void decode4(uint32_t w, float s, float o[4]) {
+  if constexpr (F == LQ_INT8) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) o[i] = (float)(int8_t)(w >> (8 * i)) * s;
+  } else {
+    lqd::fp8_unpack4<LQ_E4M3>(w, o);
+#pragma unroll
+    for (int i = 0; i < 4; i++) o[i] *= s;
+  }
+}
+
+// Workgroups of four waves for `units` one-wave units of a streaming kernel;
+// beyond 2^20 the waves take several each (and the launch's thread count stays
+// within 32 bits).
+inline unsigned stream_grid(int64_t units) {
+  const int64_t wgs = (units + 3) / 4;
+  return (unsigned)(wgs < (1 << 20) ? wgs : (1 << 20));
+}
+
+// ------------------------------------------------------------ launchers
+// (lq_mx4.hip, lq_grad.hip, lq_swiglu.hip; arguments checked by lq_linear.hip)
+hipError_t launch_mx4_quantize(int in_dtype, int ckpt_format, const void* x, int64_t m, int64_t k, int64_t ldx,
+                               void* codes, void* scales, void* ckpt_codes, void* ckpt_scales, hipStream_t s);
+hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
+                              int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s);
+hipError_t launch_mx4_dgrad(const void* dy, int64_t m, int64_t n, int64_t lddy, const void* w_codes,
+                            const void* w_scales, int64_t k, int out_dtype, void* dx, int64_t lddx, hipStream_t s);
+hipError_t launch_ckpt8_wgrad(int format, const void* dy, int64_t m, int64_t n, int64_t lddy, const void* x_codes,
+                              const void* x_scales, int64_t k, const float* dw_in, float* dw, int64_t lddw,
+                              hipStream_t s);
+hipError_t launch_swiglu(int dtype, int format, const void* gate, const void* up, int64_t rows, int64_t cols,
+                         int64_t ld, void* h, int64_t ldh, void* gc, void* gs, void* uc, void* us, hipStream_t s);
+hipError_t launch_swiglu_backward(int dtype, int format, const void* dh, int64_t rows, int64_t cols, int64_t lddh,
+                                  const void* gc, const void* gs, const void* uc, const void* us, void* dgate,
+                                  void* dup, int64_t ld, hipStream_t s);
+
+}  // namespace lql

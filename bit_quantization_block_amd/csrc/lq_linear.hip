@@ -1,0 +1,179 @@
+// lq_linear.hip — C ABI of the low-bit linear layer (declared in include/lq.h):
+// argument checks and workspace sizes. Every check runs before the first
+// launch, so a call that fails writes nothing.
+#include <stddef.h>
+#include <stdint.h>
+
+#include "lq_linear.h"
+
+using namespace lql;
+
+namespace {
+
+bool aligned(const void* p) { return ((uintptr_t)p & 15u) == 0u; }
+template <class... P>
+bool all_aligned(P... p) {
+  return (aligned(p) && ...);
+}
+bool is_dtype(int d) { return d == LQ_F32 || d == LQ_BF16 || d == LQ_F16; }
+bool is_ckpt_format(int f) { return f == LQ_INT8 || f == LQ_E4M3; }
+// One side of a matrix; products of two sides and a stride stay within 64 bits.
+bool is_side(int64_t v) { return v >= 0 && v <= 0x7FFFFFFF; }
+bool is_stride(int64_t ld, int64_t cols) { return ld >= cols && ld <= (int64_t)1 << 31; }
+
+int status_of(hipError_t e) { return e == hipSuccess ? LQ_OK : LQ_ERR_HIP; }
+
+int check_linear(const lq_linear_desc* d) {
+  if (!d) return LQ_ERR_NULL;
+  if (!is_dtype(d->in_dtype) || !is_dtype(d->out_dtype) || d->reserved != 0) return LQ_ERR_BAD_DESC;
+  if (d->ckpt_format < LQ_INT8 || d->ckpt_format > LQ_E3M2) return LQ_ERR_BAD_DESC;
+  if (!is_ckpt_format(d->ckpt_format)) return LQ_ERR_UNSUPPORTED;
+  if (!is_side(d->m) || !is_side(d->n) || !is_side(d->k)) return LQ_ERR_SHAPE;
+  return LQ_OK;
+}
+
+// The forward call's copy of x as an MX4 operand: codes, then scales, each
+// from a multiple of 256 bytes.
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+size_t operand_codes(const lq_linear_desc* d) { return round256((size_t)(d->m * mx4_pitch(d->k))); }
+size_t operand_bytes(const lq_linear_desc* d) {
+  return operand_codes(d) + round256((size_t)(d->m * mx4_scale_pitch(d->k)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lq_mx4_codes_bytes(int64_t rows, int64_t cols) {
+  return is_side(rows) && is_side(cols) ? (size_t)(rows * mx4_pitch(cols)) : 0;
+}
+size_t lq_mx4_scales_bytes(int64_t rows, int64_t cols) {
+  return is_side(rows) && is_side(cols) ? (size_t)(rows * mx4_scale_pitch(cols)) : 0;
+}
+size_t lq_ckpt8_codes_bytes(int64_t rows, int64_t cols) {
+  return is_side(rows) && is_side(cols) ? (size_t)(rows * ckpt_pitch(cols)) : 0;
+}
+size_t lq_ckpt8_scales_bytes(int64_t rows, int64_t cols) {
+  return is_side(rows) && is_side(cols) ? (size_t)(rows * ckpt_scale_pitch(cols)) : 0;
+}
+
+size_t lq_linear_workspace_bytes(const lq_linear_desc* d) {
+  if (check_linear(d)) return 0;
+  const size_t b = operand_bytes(d);
+  return b ? b : 256;
+}
+
+int lq_mx4_quantize(const lq_linear_desc* d, const void* x, void* codes, void* scales, void* ckpt_codes,
+                    void* ckpt_scales, void* stream) {
+  const int rc = check_linear(d);
+  if (rc) return rc;
+  if (!is_stride(d->ld_in, d->k)) return LQ_ERR_SHAPE;
+  if (!codes != !scales || !ckpt_codes != !ckpt_scales) return LQ_ERR_NULL;
+  if (d->m == 0 || d->k == 0) return LQ_OK;
+  if (!x || (!codes && !ckpt_codes)) return LQ_ERR_NULL;
+  if (!all_aligned(x, codes, scales, ckpt_codes, ckpt_scales)) return LQ_ERR_ALIGN;
+  return status_of(launch_mx4_quantize(d->in_dtype, d->ckpt_format, x, d->m, d->k, d->ld_in, codes, scales, ckpt_codes,
+                                       ckpt_scales, (hipStream_t)stream));
+}
+
+int lq_mx4_product(const lq_linear_desc* d, const void* x_codes, const void* x_scales, const void* w_codes,
+                   const void* w_scales, void* y, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_linear(d);
+  if (rc) return rc;
+  if (!is_stride(d->ld_out, d->n)) return LQ_ERR_SHAPE;
+  if (d->m == 0 || d->n == 0) return LQ_OK;
+  if (!y || (d->k > 0 && (!x_codes || !x_scales || !w_codes || !w_scales))) return LQ_ERR_NULL;
+  if (!all_aligned(x_codes, x_scales, w_codes, w_scales, (const void*)y, (const void*)ws)) return LQ_ERR_ALIGN;
+  if (!ws || ws_bytes < lq_linear_workspace_bytes(d)) return LQ_ERR_WORKSPACE;
+  return status_of(launch_mx4_product(x_codes, x_scales, w_codes, w_scales, d->m, d->n, d->k, d->out_dtype, y,
+                                      d->ld_out, (hipStream_t)stream));
+}
+
+int lq_mx4_linear(const lq_linear_desc* d, const void* x, const void* w_codes, const void* w_scales, void* y,
+                  void* ckpt_codes, void* ckpt_scales, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_linear(d);
+  if (rc) return rc;
+  if (!is_stride(d->ld_in, d->k) || !is_stride(d->ld_out, d->n)) return LQ_ERR_SHAPE;
+  if (!ckpt_codes != !ckpt_scales) return LQ_ERR_NULL;
+  if (d->m == 0) return LQ_OK;
+  if ((d->n > 0 && !y) || (d->k > 0 && (!x || (d->n > 0 && (!w_codes || !w_scales))))) return LQ_ERR_NULL;
+  if (!all_aligned(x, w_codes, w_scales, (const void*)y, (const void*)ckpt_codes, (const void*)ckpt_scales,
+                   (const void*)ws))
+    return LQ_ERR_ALIGN;
+  if (!ws || ws_bytes < lq_linear_workspace_bytes(d)) return LQ_ERR_WORKSPACE;
+  uint8_t *codes = (uint8_t*)ws, *scales = (uint8_t*)ws + operand_codes(d);
+  if (d->k > 0) {
+    const hipError_t e = launch_mx4_quantize(d->in_dtype, d->ckpt_format, x, d->m, d->k, d->ld_in, codes, scales,
+                                             ckpt_codes, ckpt_scales, (hipStream_t)stream);
+    if (e != hipSuccess) return LQ_ERR_HIP;
+  }
+  if (d->n == 0) return LQ_OK;
+  return status_of(launch_mx4_product(codes, scales, w_codes, w_scales, d->m, d->n, d->k, d->out_dtype, y, d->ld_out,
+                                      (hipStream_t)stream));
+}
+
+int lq_mx4_dgrad(const lq_linear_desc* d, const void* dy, const void* w_codes, const void* w_scales, void* dx,
+                 void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_linear(d);
+  if (rc) return rc;
+  if (d->in_dtype != LQ_BF16) return LQ_ERR_UNSUPPORTED;
+  if (!is_stride(d->ld_in, d->n) || !is_stride(d->ld_out, d->k)) return LQ_ERR_SHAPE;
+  if (d->m == 0 || d->k == 0) return LQ_OK;
+  if (!dx || (d->n > 0 && (!dy || !w_codes || !w_scales))) return LQ_ERR_NULL;
+  if (!all_aligned(dy, w_codes, w_scales, (const void*)dx, (const void*)ws)) return LQ_ERR_ALIGN;
+  if (!ws || ws_bytes < lq_linear_workspace_bytes(d)) return LQ_ERR_WORKSPACE;
+  return status_of(launch_mx4_dgrad(dy, d->m, d->n, d->ld_in, w_codes, w_scales, d->k, d->out_dtype, dx, d->ld_out,
+                                    (hipStream_t)stream));
+}
+
+int lq_ckpt8_wgrad(const lq_linear_desc* d, const void* dy, const void* ckpt_codes, const void* ckpt_scales,
+                   const void* dw_in, void* dw, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_linear(d);
+  if (rc) return rc;
+  if (d->in_dtype != LQ_BF16 || d->out_dtype != LQ_F32) return LQ_ERR_UNSUPPORTED;
+  if (!is_stride(d->ld_in, d->n) || !is_stride(d->ld_out, d->k)) return LQ_ERR_SHAPE;
+  if (d->n == 0 || d->k == 0) return LQ_OK;
+  if (!dw || (d->m > 0 && (!dy || !ckpt_codes || !ckpt_scales))) return LQ_ERR_NULL;
+  if (!all_aligned(dy, ckpt_codes, ckpt_scales, dw_in, (const void*)dw, (const void*)ws)) return LQ_ERR_ALIGN;
+  if (!ws || ws_bytes < lq_linear_workspace_bytes(d)) return LQ_ERR_WORKSPACE;
+  return status_of(launch_ckpt8_wgrad(d->ckpt_format, dy, d->m, d->n, d->ld_in, ckpt_codes, ckpt_scales, d->k,
+                                      (const float*)dw_in, (float*)dw, d->ld_out, (hipStream_t)stream));
+}
+
+static int check_swiglu(const lq_swiglu_desc* d) {
+  if (!d) return LQ_ERR_NULL;
+  if (!is_dtype(d->dtype) || d->ckpt_format < LQ_INT8 || d->ckpt_format > LQ_E3M2) return LQ_ERR_BAD_DESC;
+  if (!is_ckpt_format(d->ckpt_format)) return LQ_ERR_UNSUPPORTED;
+  if (!is_side(d->rows) || !is_side(d->cols) || !is_stride(d->ld, d->cols) || !is_stride(d->ld_h, d->cols))
+    return LQ_ERR_SHAPE;
+  return LQ_OK;
+}
+
+int lq_swiglu_ckpt8(const lq_swiglu_desc* d, const void* gate, const void* up, void* h, void* gate_codes,
+                    void* gate_scales, void* up_codes, void* up_scales, void* stream) {
+  const int rc = check_swiglu(d);
+  if (rc) return rc;
+  const bool keep = gate_codes != nullptr;
+  if (!gate_scales == keep || !up_codes == keep || !up_scales == keep) return LQ_ERR_NULL;
+  if (d->rows == 0 || d->cols == 0) return LQ_OK;
+  if (!gate || !up || (!h && !keep)) return LQ_ERR_NULL;
+  if (!all_aligned(gate, up, (const void*)h, (const void*)gate_codes, (const void*)gate_scales, (const void*)up_codes,
+                   (const void*)up_scales))
+    return LQ_ERR_ALIGN;
+  return status_of(launch_swiglu(d->dtype, d->ckpt_format, gate, up, d->rows, d->cols, d->ld, h, d->ld_h, gate_codes,
+                                 gate_scales, up_codes, up_scales, (hipStream_t)stream));
+}
+
+int lq_swiglu_ckpt8_backward(const lq_swiglu_desc* d, const void* dh, const void* gate_codes, const void* gate_scales,
+                             const void* up_codes, const void* up_scales, void* dgate, void* dup, void* stream) {
+  const int rc = check_swiglu(d);
+  if (rc) return rc;
+  if (d->rows == 0 || d->cols == 0) return LQ_OK;
+  if (!dh || !gate_codes || !gate_scales || !up_codes || !up_scales || !dgate || !dup) return LQ_ERR_NULL;
+  if (!all_aligned(dh, gate_codes, gate_scales, up_codes, up_scales, (const void*)dgate, (const void*)dup))
+    return LQ_ERR_ALIGN;
+  return status_of(launch_swiglu_backward(d->dtype, d->ckpt_format, dh, d->rows, d->cols, d->ld_h, gate_codes,
+                                          gate_scales, up_codes, up_scales, dgate, dup, d->ld, (hipStream_t)stream));
+}
+
+}  // extern "C"

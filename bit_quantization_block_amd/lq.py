@@ -26,7 +26,10 @@ DTYPE = {"f32": 0, "bf16": 1, "f16": 2}
 
 EXPORTS = ("lq_quantize", "lq_dequantize", "lq_fake_quant_qsnr", "lq_hadamard_quant", "lq_workspace_bytes",
            "lq_codes_bytes", "lq_scales_bytes", "lq_zeros_bytes", "lq_workspace_init", "lq_sweep_tally",
-           "lq_call_kernels", "lq_set_grid_limit", "lq_status_string", "lq_fake_quant_qsnr_static")
+           "lq_call_kernels", "lq_set_grid_limit", "lq_status_string", "lq_fake_quant_qsnr_static",
+           "lq_mx4_codes_bytes", "lq_mx4_scales_bytes", "lq_ckpt8_codes_bytes", "lq_ckpt8_scales_bytes",
+           "lq_linear_workspace_bytes", "lq_mx4_quantize", "lq_mx4_product", "lq_mx4_linear", "lq_mx4_dgrad",
+           "lq_ckpt8_wgrad", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward")
 # output bits of lq_call_kernels
 OUT = {"codes": 1, "scales": 2, "zeros": 4, "y": 8, "res": 16}
 
@@ -46,6 +49,16 @@ class Desc(ctypes.Structure):
 class Result(ctypes.Structure):
     _fields_ = [("err2", ctypes.c_double), ("sig2", ctypes.c_double), ("qsnr_db", ctypes.c_double),
                 ("nonfinite", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_dtype", "out_dtype", "ckpt_format", "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("m", "n", "k", "ld_in", "ld_out")]
+
+
+class SwigluDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("ckpt_format", ctypes.c_int32)] + \
+               [(n, ctypes.c_int64) for n in ("rows", "cols", "ld", "ld_h")]
 
 
 _lib = None
@@ -80,6 +93,22 @@ def load(path: str | None = None):
                                  ctypes.POINTER(ctypes.c_int32)]
     L.lq_call_kernels.argtypes = [dp, i64, i64, ctypes.c_uint32, ctypes.c_int, ctypes.c_char_p, sz]
     L.lq_call_kernels.restype = ctypes.c_int
+    for f in ("lq_mx4_codes_bytes", "lq_mx4_scales_bytes", "lq_ckpt8_codes_bytes", "lq_ckpt8_scales_bytes"):
+        getattr(L, f).argtypes = [i64, i64]
+        getattr(L, f).restype = sz
+    lp, sp = ctypes.POINTER(LinearDesc), ctypes.POINTER(SwigluDesc)
+    L.lq_linear_workspace_bytes.argtypes = [lp]
+    L.lq_linear_workspace_bytes.restype = sz
+    L.lq_mx4_quantize.argtypes = [lp, vp, vp, vp, vp, vp, vp]
+    L.lq_mx4_product.argtypes = [lp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.lq_mx4_linear.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.lq_mx4_dgrad.argtypes = [lp, vp, vp, vp, vp, vp, sz, vp]
+    L.lq_ckpt8_wgrad.argtypes = [lp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.lq_swiglu_ckpt8.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.lq_swiglu_ckpt8_backward.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp]
+    for f in ("lq_mx4_quantize", "lq_mx4_product", "lq_mx4_linear", "lq_mx4_dgrad", "lq_ckpt8_wgrad",
+              "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward"):
+        getattr(L, f).restype = ctypes.c_int
     L.lq_status_string.argtypes = [ctypes.c_int]
     L.lq_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -291,6 +320,217 @@ class Runner:
             raw = self.y[:self.rows * self.cols * ob].cpu().numpy()
             out["y"] = raw.view(np.uint32 if ob == 4 else np.uint16).reshape(self.rows, self.cols)
         return out
+
+
+# ------------------------------------------------------------------ the low-bit linear layer
+_TORCH_DTYPE = {"f32": "float32", "bf16": "bfloat16", "f16": "float16"}
+
+
+def _torch_dtype(name):
+    import torch
+
+    return getattr(torch, _TORCH_DTYPE[name])
+
+
+def _dtype_name(t) -> str:
+    for name, full in _TORCH_DTYPE.items():
+        if str(t.dtype) == "torch." + full:
+            return name
+    raise TypeError(f"no lq dtype for {t.dtype}")
+
+
+def _matrix(t, rows, cols, dtype, what):
+    """A 2-D device tensor of this shape and dtype whose rows are contiguous; its row stride."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} is {t.dtype}, expected {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} is not on the GPU")
+    st = t.stride()
+    if cols > 1 and st[1] != 1:
+        raise ValueError(f"{what}'s rows must be contiguous (strides {st})")
+    if rows > 1 and st[0] < cols:
+        raise ValueError(f"{what}'s rows overlap (strides {st})")
+    return st[0] if rows > 1 else max(st[0], cols)
+
+
+class Ckpt8:
+    """An activation [rows, cols] kept in 8 bits for the backward pass: INT8
+    or E4M3 codes (`fmt`), a power-of-two scale per 32 columns. A forward call
+    writes it, or save()."""
+
+    def __init__(self, rows: int, cols: int, fmt: str = "int8", device="cuda", lib=None):
+        import torch
+
+        self.lib = lib or load()
+        self.rows, self.cols, self.fmt = rows, cols, fmt
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.codes = torch.empty(max(16, self.lib.lq_ckpt8_codes_bytes(rows, cols)), **u8)
+        self.scales = torch.empty(max(16, self.lib.lq_ckpt8_scales_bytes(rows, cols)), **u8)
+
+    def save(self, x, stream=None):
+        ld = _matrix(x, self.rows, self.cols, x.dtype, "x")
+        d = LinearDesc(DTYPE[_dtype_name(x)], 0, FORMAT[self.fmt], 0, self.rows, 0, self.cols, ld, 0)
+        _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(x), None, None, _ptr(self.codes),
+                                                           _ptr(self.scales), _stream(stream)))
+
+
+class Mx4Linear:
+    """A linear layer y = x W^T with W held in 4 bits (MXFP4), and its
+    gradients. `w` [n, k] is quantised once; `rows` is the most rows of x or
+    dy a call may have, for which the workspace and the results' buffers are
+    allocated once (a call's result is a view of the layer's buffer, which the
+    layer's next call of that kind overwrites, unless the caller passes its
+    own as `out`). `dtype`: of x; `out`: of y and dx; dy is bfloat16 and dw
+    float32."""
+
+    def __init__(self, w, rows: int, dtype: str = "bf16", out: str = "bf16", lib=None):
+        import torch
+
+        self.torch = torch
+        self.lib = lib or load()
+        self.n, self.k = w.shape
+        self.rows, self.dtype, self.out = rows, dtype, out
+        self.device = w.device
+        u8 = dict(dtype=torch.uint8, device=w.device)
+        self.codes = torch.empty(max(16, self.lib.lq_mx4_codes_bytes(self.n, self.k)), **u8)
+        self.scales = torch.empty(max(16, self.lib.lq_mx4_scales_bytes(self.n, self.k)), **u8)
+        ld = _matrix(w, self.n, self.k, w.dtype, "w")
+        d = LinearDesc(DTYPE[_dtype_name(w)], 0, 0, 0, self.n, 0, self.k, ld, 0)
+        _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(w), _ptr(self.codes),
+                                                           _ptr(self.scales), None, None, _stream(None)))
+        self._w = (self.codes.data_ptr(), self.scales.data_ptr())
+        self._descs = {}
+        self._buffers = {}
+        self.ws, self._old_ws = None, []
+
+    def _desc(self, kind, m, ld_in, ld_out, in_dtype, out_dtype, fmt):
+        key = (kind, m, ld_in, ld_out, fmt)
+        d = self._descs.get(key)
+        if d is None:
+            if m > self.rows:
+                raise ValueError(f"{m} rows in a layer planned for {self.rows}")
+            d = LinearDesc(DTYPE[in_dtype], DTYPE[out_dtype], FORMAT[fmt], 0, m, self.n, self.k, ld_in, ld_out)
+            need = self.lib.lq_linear_workspace_bytes(ctypes.byref(d))
+            if need == 0:
+                raise LQError(kind, self.lib.lq_mx4_quantize(ctypes.byref(d), None, None, None, None, None, None))
+            if self.ws is None or self.ws.numel() < need:
+                # a smaller one stays alive: a captured graph may hold its address
+                self._old_ws.append(self.ws)
+                self.ws = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
+            if len(self._descs) > 256:
+                self._descs.clear()
+            self._descs[key] = d
+        return d
+
+    def _result(self, kind, rows, cols, dtype, out):
+        """The result's tensor and row stride: the caller's, or a view of the layer's buffer."""
+        if out is not None:
+            return out, _matrix(out, rows, cols, _torch_dtype(dtype), "out")
+        b = self._buffers.get(kind)
+        if b is None:
+            most = self.n if kind == "dw" else self.rows
+            b = self._buffers[kind] = self.torch.empty(most, cols, dtype=_torch_dtype(dtype), device=self.device)
+        return (b if b.shape[0] == rows else b[:rows]), cols
+
+    def forward(self, x, ckpt: Ckpt8 | None = None, out=None, stream=None):
+        """y = Q4(x) W^T; `ckpt` also receives x in 8 bits."""
+        m = x.shape[0]
+        ld = _matrix(x, m, self.k, _torch_dtype(self.dtype), "x")
+        self._check_ckpt(ckpt, m)
+        y, ldy = self._result("y", m, self.n, self.out, out)
+        d = self._desc("lq_mx4_linear", m, ld, ldy, self.dtype, self.out, ckpt.fmt if ckpt else "int8")
+        _check("lq_mx4_linear", self.lib.lq_mx4_linear(
+            ctypes.byref(d), x.data_ptr(), *self._w, y.data_ptr(), ckpt.codes.data_ptr() if ckpt else None,
+            ckpt.scales.data_ptr() if ckpt else None, self.ws.data_ptr(), self.ws.numel(), _stream(stream)))
+        return y
+
+    def dgrad(self, dy, out=None, stream=None):
+        """dx = dy W."""
+        m = dy.shape[0]
+        ld = _matrix(dy, m, self.n, self.torch.bfloat16, "dy")
+        dx, ldx = self._result("dx", m, self.k, self.out, out)
+        d = self._desc("lq_mx4_dgrad", m, ld, ldx, "bf16", self.out, "int8")
+        _check("lq_mx4_dgrad", self.lib.lq_mx4_dgrad(ctypes.byref(d), dy.data_ptr(), *self._w, dx.data_ptr(),
+                                                     self.ws.data_ptr(), self.ws.numel(), _stream(stream)))
+        return dx
+
+    def wgrad(self, dy, ckpt: Ckpt8, dw_in=None, out=None, stream=None):
+        """dw = dw_in + dy^T x8, x8 the checkpoint that forward wrote; `out` may be dw_in."""
+        m = dy.shape[0]
+        ld = _matrix(dy, m, self.n, self.torch.bfloat16, "dy")
+        self._check_ckpt(ckpt, m)
+        dw, lddw = self._result("dw", self.n, self.k, "f32", out)
+        if dw_in is not None and _matrix(dw_in, self.n, self.k, self.torch.float32, "dw_in") != lddw:
+            raise ValueError("dw_in and the result differ in their row strides")
+        d = self._desc("lq_ckpt8_wgrad", m, ld, lddw, "bf16", "f32", ckpt.fmt)
+        _check("lq_ckpt8_wgrad", self.lib.lq_ckpt8_wgrad(
+            ctypes.byref(d), dy.data_ptr(), ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), _ptr(dw_in), dw.data_ptr(),
+            self.ws.data_ptr(), self.ws.numel(), _stream(stream)))
+        return dw
+
+    def _check_ckpt(self, ckpt, m):
+        if ckpt is not None and (ckpt.rows != m or ckpt.cols != self.k):
+            raise ValueError(f"the checkpoint is {ckpt.rows} x {ckpt.cols}, the call's x {m} x {self.k}")
+
+
+class SwigluCkpt8:
+    """h = silu(gate) up over [rows, cols], keeping gate and up in 8 bits, and
+    its backward pass from those. Results are the object's own buffers unless
+    the caller passes its own."""
+
+    def __init__(self, rows: int, cols: int, dtype: str = "bf16", fmt: str = "int8", device="cuda", lib=None):
+        import torch
+
+        self.torch = torch
+        self.lib = lib or load()
+        self.rows, self.cols, self.dtype, self.fmt = rows, cols, dtype, fmt
+        self._t = _torch_dtype(dtype)
+        self.gate = Ckpt8(rows, cols, fmt, device, lib)
+        self.up = Ckpt8(rows, cols, fmt, device, lib)
+        self._kept = (self.gate.codes.data_ptr(), self.gate.scales.data_ptr(), self.up.codes.data_ptr(),
+                      self.up.scales.data_ptr())
+        self._device = device
+        self._descs = {}
+        self._buffers = {}
+
+    def _desc(self, ld, ld_h):
+        d = self._descs.get((ld, ld_h))
+        if d is None:
+            d = self._descs[(ld, ld_h)] = SwigluDesc(DTYPE[self.dtype], FORMAT[self.fmt], self.rows, self.cols, ld,
+                                                     ld_h)
+        return d
+
+    def _result(self, kind, out):
+        if out is not None:
+            return out, _matrix(out, self.rows, self.cols, self._t, "out")
+        b = self._buffers.get(kind)
+        if b is None:
+            b = self._buffers[kind] = self.torch.empty(self.rows, self.cols, dtype=self._t, device=self._device)
+        return b, self.cols
+
+    def forward(self, gate, up, out=None, stream=None):
+        ld = _matrix(gate, self.rows, self.cols, self._t, "gate")
+        if _matrix(up, self.rows, self.cols, self._t, "up") != ld:
+            raise ValueError("gate and up differ in their row strides")
+        h, ldh = self._result("h", out)
+        _check("lq_swiglu_ckpt8", self.lib.lq_swiglu_ckpt8(
+            ctypes.byref(self._desc(ld, ldh)), gate.data_ptr(), up.data_ptr(), h.data_ptr(), *self._kept,
+            _stream(stream)))
+        return h
+
+    def backward(self, dh, out=None, stream=None):
+        """(dgate, dup); `out`: a pair of tensors for them."""
+        ldh = _matrix(dh, self.rows, self.cols, self._t, "dh")
+        dg, ld = self._result("dgate", out[0] if out else None)
+        du, ld2 = self._result("dup", out[1] if out else None)
+        if ld != ld2:
+            raise ValueError("dgate and dup differ in their row strides")
+        _check("lq_swiglu_ckpt8_backward", self.lib.lq_swiglu_ckpt8_backward(
+            ctypes.byref(self._desc(ld, ldh)), dh.data_ptr(), *self._kept, dg.data_ptr(), du.data_ptr(),
+            _stream(stream)))
+        return dg, du
 
 
 # ------------------------------------------------------------------ ceilings

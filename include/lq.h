@@ -118,7 +118,7 @@ extern "C" {
 #define LQ_ERR_ALIGN (-4)       /* a device pointer is not 16-byte aligned */
 #define LQ_ERR_WORKSPACE (-5)   /* workspace missing or smaller than lq_workspace_bytes() */
 #define LQ_ERR_HIP (-6)         /* a HIP launch failed */
-#define LQ_ERR_UNSUPPORTED (-7) /* defined by the method but not built (block size) */
+#define LQ_ERR_UNSUPPORTED (-7) /* defined by the method but not built (block size; a type or format of the linear layer) */
 
 /* element formats */
 typedef enum { LQ_INT8 = 0, LQ_INT4 = 1, LQ_E4M3 = 2, LQ_E5M2 = 3, LQ_E2M1 = 4, LQ_E2M3 = 5, LQ_E3M2 = 6 } lq_format;
@@ -230,7 +230,7 @@ LQ_API size_t lq_zeros_bytes(const lq_desc* desc, int64_t rows, int64_t cols);
  * `stream` with a fill kernel (no memset node); ws_bytes is rounded down to 4. */
 LQ_API int lq_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
-/* Caps the grid of every later launch in this process at max_workgroups
+/* Caps the grid of every later quantize, dequantize or fake-quant launch in this process at max_workgroups
  * 256-thread workgroups (the per-block kernels with 1024-thread workgroups
  * take a quarter of that, at least one); 0 restores the default (32 per CU).
  * Results do not depend on it: a tuning and testing knob that trades
@@ -277,6 +277,103 @@ LQ_API int lq_sweep_tally(const double* qsnr, int64_t n_tensors, double tie_db, 
  * match profiler records to calls. */
 LQ_API int lq_call_kernels(const lq_desc* desc, int64_t rows, int64_t cols, uint32_t outputs, int unrotate_y,
                            char* names, size_t bytes);
+
+/* ---------------------------------------------------------------------------
+ * Low-bit linear layers: products with 4-bit microscaled weights, and 8-bit
+ * activation checkpoints for the backward pass.
+ *
+ * A layer y = x W^T has W [n, k] held in 4 bits. Forward, x [m, k] is quantised
+ * to 4 bits too and the two are multiplied by the matrix cores; x can be kept
+ * for the backward pass in 8 bits (a checkpoint), written in the same read of
+ * x. Backward, dx = dy W (the quantiser of x passes the gradient through), and
+ * dw = dw_in + dy^T x8 from the checkpoint's values x8. Between two projections
+ * of a gated MLP, h = silu(gate) up keeps gate and up as checkpoints and its
+ * backward pass reads only those and dh.
+ *
+ * Exact numerics: scales are the UE8M0 rule above in blocks of 32 along k, the
+ * last block of a row short if k is no multiple of 32. Codes are the rules
+ * above (E2M1; INT8 in [-127,127], half to even; E4M3). A block that holds an
+ * infinity or a NaN gets the NaN scale 0xFF and zero codes, and every result
+ * computed from it is NaN. The products take the quantised values as they are (E2M1, INT8 and
+ * E4M3 values times a power of two are exact in bfloat16) and add in binary32;
+ * results are rounded once, to nearest even, to the output type. A repeated
+ * call gives the same bits. silu(g) = g / (1 + exp(-g)), its derivative
+ * s (1 + g (1 - s)) with s = 1 / (1 + exp(-g)), in binary32.
+ *
+ * Layouts (all row-major; ld_*: elements between the starts of two rows of a
+ * caller's matrix, at least its row length, no alignment asked for):
+ *   MX4 operand [rows, cols] (x or W): codes, two per byte as above, rows of
+ *           128 * ceil(cols / 256) bytes; scales, rows of 16 * ceil(cols / 512)
+ *           bytes. Elements and blocks past cols hold zeros. With cols a
+ *           multiple of 512 these are lq_quantize's bytes for E2M1, PER_BLOCK
+ *           32, UE8M0.
+ *   checkpoint [rows, cols]: codes, one byte each, rows of 32 * ceil(cols / 32);
+ *           scales, rows of ceil(cols / 32). With cols a multiple of 32 these
+ *           are lq_quantize's bytes for INT8 or E4M3, PER_BLOCK 32, UE8M0, and
+ *           lq_dequantize reads them.
+ *
+ * Sides are 0 .. 2^31-1. Empty sides are no error: an empty contraction gives
+ * zeros (or dw_in). Pointers, ownership, streams and errors as above; buffers
+ * of one call must not overlap, except that dw may be dw_in. Every call but the
+ * quantisers and the activation needs a workspace of
+ * lq_linear_workspace_bytes(), 16-byte aligned, not initialised, not shared
+ * by calls that overlap in time. */
+typedef struct {
+  int32_t in_dtype;    /* lq_dtype of x (forward) or of dy (gradients: LQ_BF16, else LQ_ERR_UNSUPPORTED) */
+  int32_t out_dtype;   /* lq_dtype of y or dx; of dw: LQ_F32, else LQ_ERR_UNSUPPORTED */
+  int32_t ckpt_format; /* the checkpoint's elements: LQ_INT8 or LQ_E4M3 */
+  int32_t reserved;    /* 0 */
+  int64_t m, n, k;     /* rows of x and y; columns of y, rows of W; columns of x and W */
+  int64_t ld_in;       /* row stride of x (forward) or dy (gradients) */
+  int64_t ld_out;      /* row stride of y, dx, or dw and dw_in */
+} lq_linear_desc;
+
+/* Sizes in bytes of a stored matrix (0 for a side out of range). */
+LQ_API size_t lq_mx4_codes_bytes(int64_t rows, int64_t cols);
+LQ_API size_t lq_mx4_scales_bytes(int64_t rows, int64_t cols);
+LQ_API size_t lq_ckpt8_codes_bytes(int64_t rows, int64_t cols);
+LQ_API size_t lq_ckpt8_scales_bytes(int64_t rows, int64_t cols);
+/* Workspace that each of the calls below needs with this descriptor (0 on a bad one). */
+LQ_API size_t lq_linear_workspace_bytes(const lq_linear_desc* desc);
+
+/* x [m, k] as an MX4 operand and/or as an 8-bit checkpoint (either pair may be
+ * NULL), in one read of x. Weights are quantised with it too (m = n rows). n,
+ * out_dtype and ld_out are not used. */
+LQ_API int lq_mx4_quantize(const lq_linear_desc* desc, const void* x, void* codes, void* scales, void* ckpt_codes,
+                           void* ckpt_scales, void* stream);
+
+/* y [m, n] = x W^T from two MX4 operands. in_dtype, ckpt_format and ld_in are not used. */
+LQ_API int lq_mx4_product(const lq_linear_desc* desc, const void* x_codes, const void* x_scales, const void* w_codes,
+                          const void* w_scales, void* y, void* ws, size_t ws_bytes, void* stream);
+
+/* y [m, n] = Q4(x) W^T, keeping x [m, k] as a checkpoint unless ckpt_codes and ckpt_scales are NULL. */
+LQ_API int lq_mx4_linear(const lq_linear_desc* desc, const void* x, const void* w_codes, const void* w_scales, void* y,
+                         void* ckpt_codes, void* ckpt_scales, void* ws, size_t ws_bytes, void* stream);
+
+/* dx [m, k] = dy W, dy [m, n]. */
+LQ_API int lq_mx4_dgrad(const lq_linear_desc* desc, const void* dy, const void* w_codes, const void* w_scales,
+                        void* dx, void* ws, size_t ws_bytes, void* stream);
+
+/* dw [n, k] = dw_in + dy^T x8, dy [m, n], x8 [m, k] a checkpoint; dw_in (fp32, the stride of dw) NULL for zeros. */
+LQ_API int lq_ckpt8_wgrad(const lq_linear_desc* desc, const void* dy, const void* ckpt_codes, const void* ckpt_scales,
+                          const void* dw_in, void* dw, void* ws, size_t ws_bytes, void* stream);
+
+typedef struct {
+  int32_t dtype;       /* lq_dtype of every matrix */
+  int32_t ckpt_format; /* LQ_INT8 or LQ_E4M3 */
+  int64_t rows, cols;
+  int64_t ld;          /* row stride of gate and up, and of dgate and dup */
+  int64_t ld_h;        /* row stride of h and dh */
+} lq_swiglu_desc;
+
+/* h = silu(gate) up (NULL to skip it), keeping gate and up as checkpoints (all four NULL to keep nothing). */
+LQ_API int lq_swiglu_ckpt8(const lq_swiglu_desc* desc, const void* gate, const void* up, void* h, void* gate_codes,
+                           void* gate_scales, void* up_codes, void* up_scales, void* stream);
+
+/* dgate and dup from dh and the checkpoints. */
+LQ_API int lq_swiglu_ckpt8_backward(const lq_swiglu_desc* desc, const void* dh, const void* gate_codes,
+                                    const void* gate_scales, const void* up_codes, const void* up_scales, void* dgate,
+                                    void* dup, void* stream);
 
 /* Text for a status code (static storage). */
 LQ_API const char* lq_status_string(int status);

@@ -1,0 +1,482 @@
+"""The low-bit linear layer on the GPU against its 64-bit reference
+(tests/linear_ref.py): codes and scales bit for bit; products within binary32
+accumulation plus one output rounding; odd sizes, strides, empty sides, spoiled
+blocks, offsets past 32 bits, streams and captured graphs."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from bit_quantization_block_amd import lq
+from tests import linear_ref as R
+from tests.gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+T = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def matrix(rows, cols, dtype, pad=0, seed=0, scale=1.0):
+    """(device view with `pad` elements after each row, its values in float64)."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * scale
+    x *= 2.0 ** torch.randint(-3, 4, (rows, 1), generator=g)
+    t = torch.full((rows, cols + pad), 77.0, dtype=T[dtype])
+    t[:, :cols] = x.to(T[dtype])
+    d = t.cuda()
+    return d[:, :cols], t[:, :cols].double().numpy()
+
+
+def accumulation(a, b):
+    """Bound on adding k exact products a[i] b[i] in binary32 in any order, a
+    truncation of up to one unit (2^-23) of the running magnitude at each step."""
+    k = a.shape[1]
+    return (k + 8) * 2.0 ** -23 * (np.abs(a) @ np.abs(b))
+
+
+def close(got, want, acc, out, what):
+    got = got.double().cpu().numpy()
+    bound = acc + R.out_error(np.abs(want) + acc, out)
+    bad = ~(np.abs(got - want) <= bound)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {np.nanmax(np.abs(got - want) / bound)} of the bound"
+
+
+SHAPES = [  # m, n, k, pad
+    (1, 1, 1, 0), (1, 64, 256, 0), (1, 4099, 1000, 0), (2, 33, 31, 1), (3, 130, 512, 3), (7, 257, 544, 0),
+    (15, 48, 4096, 0), (16, 512, 2048, 8), (17, 96, 768, 0), (31, 32, 33, 5), (33, 1001, 257, 1), (64, 256, 64, 0),
+    (100, 300, 1056, 2), (127, 255, 511, 1), (128, 128, 1024, 0), (129, 513, 96, 7), (257, 260, 1280, 0),
+    (515, 385, 1000, 3), (700, 1024, 520, 0)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (3, 31, 1), (5, 32, 0), (2, 33, 7), (4, 255, 0), (3, 512, 0),
+                                           (7, 1000, 3), (130, 2049, 1)])
+def test_quantise(dtype, fmt, rows, cols, pad):
+    say(f"[gpu] mx4 quantise {dtype} {fmt} {rows}x{cols}+{pad}")
+    x, xv = matrix(rows, cols, dtype, pad, seed=rows + cols)
+    x[0, 0] = 0.0
+    if cols > 64:
+        x[rows - 1, 32:64] = 0.0                     # a block of zeros
+        x[0, 64:cols].mul_(2.0 ** -12)
+    xv = x.double().cpu().numpy()
+    L = lq.load()
+    d = lq.LinearDesc(lq.DTYPE[dtype], 0, lq.FORMAT[fmt], 0, rows, 0, cols, cols + pad, 0)
+    sizes = [L.lq_mx4_codes_bytes(rows, cols), L.lq_mx4_scales_bytes(rows, cols), L.lq_ckpt8_codes_bytes(rows, cols),
+             L.lq_ckpt8_scales_bytes(rows, cols)]
+    bufs = [torch.full((s + 64,), 0xA5, dtype=torch.uint8, device="cuda") for s in sizes]
+    lq._check("q", L.lq_mx4_quantize(ctypes.byref(d), x.data_ptr(), *[b.data_ptr() for b in bufs], lq._stream(None)))
+    host = [b.cpu().numpy() for b in bufs]
+    for h, s in zip(host, sizes):
+        assert (h[s:] == 0xA5).all()                 # nothing past the end
+    nb = -(-cols // 32)
+    c4, s4, _ = R.quantise(xv, "e2m1")
+    got = host[0][:sizes[0]].reshape(rows, -1)
+    assert np.array_equal(got[:, :nb * 16], R.pack4(c4)) and (got[:, nb * 16:] == 0).all()
+    got = host[1][:sizes[1]].reshape(rows, -1)
+    assert np.array_equal(got[:, :nb], s4) and (got[:, nb:] == 0).all()
+    c8, s8, _ = R.quantise(xv, fmt)
+    assert np.array_equal(host[2][:sizes[2]].reshape(rows, -1), c8)
+    assert np.array_equal(host[3][:sizes[3]].reshape(rows, -1), s8)
+
+
+def test_quantise_equals_lq_quantize():
+    x, _ = matrix(96, 1024, "bf16", 0, seed=5)
+    w = lq.Mx4Linear(x, rows=1)
+    keep = {f: lq.Ckpt8(96, 1024, f) for f in ("int8", "e4m3")}
+    for f, c in keep.items():
+        c.save(x)
+    for f, codes, scales in (("e2m1", w.codes, w.scales), ("int8", keep["int8"].codes, keep["int8"].scales),
+                             ("e4m3", keep["e4m3"].codes, keep["e4m3"].scales)):
+        r = lq.Runner({"fmt": f, "gran": "block", "block": 32, "scale": "ue8m0", "out": "f32"}, 96, 1024, "bf16")
+        r.quantize(x)
+        assert torch.equal(r.codes, codes) and torch.equal(r.scales, scales)
+
+
+def test_extremes_of_the_scale():
+    """Blocks at the ends of binary32's range, and tiny ones whose scale is clamped."""
+    x = torch.zeros(6, 64)
+    x[0, :32] = torch.linspace(-3.4e38, 3.4e38, 32)
+    x[1, :32] = torch.linspace(-1e-38, 1e-38, 32)
+    x[2, 0] = 1e-45
+    x[3, :] = -0.0
+    x[4, 5], x[4, 40] = 6 * 2.0 ** -127, 127 * 2.0 ** -127
+    x[5, 1] = 448 * 2.0 ** 100
+    for f in ("int8", "e4m3"):
+        c = lq.Ckpt8(6, 64, f)
+        c.save(x.cuda())
+        codes, sb, _ = R.quantise(x.numpy(), f)
+        assert np.array_equal(c.codes.cpu().numpy().reshape(6, 64), codes)
+        assert np.array_equal(c.scales[:12].cpu().numpy().reshape(6, 2), sb)
+    w = lq.Mx4Linear(x.cuda(), rows=1)
+    codes, sb, _ = R.quantise(x.numpy(), "e2m1")
+    assert np.array_equal(w.codes.cpu().numpy().reshape(6, 128)[:, :32], R.pack4(codes))
+    assert np.array_equal(w.scales.cpu().numpy().reshape(6, 16)[:, :2], sb)
+
+
+def test_largest_finite_values():
+    x = torch.zeros(3, 32)
+    x[0] = torch.linspace(-1.0, 1.0, 32) * 3.4e38
+    x[1, 7] = torch.finfo(torch.float32).max
+    x[2, 3] = -1.5 * 2.0 ** 127
+    w = lq.Mx4Linear(x.cuda(), rows=1)
+    codes, sb, _ = R.quantise(x.numpy(), "e2m1")
+    assert np.array_equal(w.codes.cpu().numpy().reshape(3, 128)[:, :16], R.pack4(codes))
+    assert np.array_equal(w.scales.cpu().numpy().reshape(3, 16)[:, :1], sb)
+
+
+@pytest.mark.parametrize("m,n,k,pad", SHAPES)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32"), ("f16", "f16")])
+def test_linear(m, n, k, pad, dtype, out):
+    say(f"[gpu] mx4 linear {dtype}->{out} {m}x{n}x{k}+{pad}")
+    x, xv = matrix(m, k, dtype, pad, seed=m)
+    w, wv = matrix(n, k, "bf16", pad, seed=n + 1, scale=0.05)
+    layer = lq.Mx4Linear(w, rows=m, dtype=dtype, out=out)
+    ckpt = lq.Ckpt8(m, k, "int8")
+    y = torch.full((m, n + pad), 55.0, dtype=T[out], device="cuda")
+    got = layer.forward(x, ckpt=ckpt, out=y[:, :n])
+    x4, w4 = R.quantise(xv, "e2m1")[2], R.quantise(wv, "e2m1")[2]
+    close(got, x4 @ w4.T, accumulation(x4, w4.T), out, "y")
+    assert (y[:, n:] == 55.0).all()                  # nothing between the rows
+    c8, s8, _ = R.quantise(xv, "int8")
+    assert np.array_equal(ckpt.codes.cpu().numpy()[:c8.size].reshape(c8.shape), c8)
+    assert np.array_equal(ckpt.scales.cpu().numpy()[:s8.size].reshape(s8.shape), s8)
+    # the same product from operands quantised once, and without a checkpoint
+    assert torch.equal(layer.forward(x), got)
+    xo = lq.Mx4Linear(x, rows=1)
+    d = lq.LinearDesc(0, lq.DTYPE[out], 0, 0, m, n, k, 0, n)
+    y2 = torch.empty(m, n, dtype=T[out], device="cuda")
+    L = lq.load()
+    ws = torch.empty(L.lq_linear_workspace_bytes(ctypes.byref(d)), dtype=torch.uint8, device="cuda")
+    lq._check("p", L.lq_mx4_product(ctypes.byref(d), xo.codes.data_ptr(), xo.scales.data_ptr(), layer.codes.data_ptr(),
+                                    layer.scales.data_ptr(), y2.data_ptr(), ws.data_ptr(), ws.numel(), lq._stream(None)))
+    x4w4 = x4 @ w4.T
+    close(y2, x4w4, accumulation(x4, w4.T), out, "product")
+
+
+@pytest.mark.parametrize("m,n,k,pad", SHAPES)
+@pytest.mark.parametrize("out", ["bf16", "f32", "f16"])
+def test_dgrad(m, n, k, pad, out):
+    say(f"[gpu] mx4 dgrad ->{out} {m}x{n}x{k}+{pad}")
+    dy, dyv = matrix(m, n, "bf16", pad, seed=m, scale=0.1)
+    w, wv = matrix(n, k, "bf16", pad, seed=n + 1, scale=0.05)
+    layer = lq.Mx4Linear(w, rows=m, out=out)
+    dx = torch.full((m, k + pad), 55.0, dtype=T[out], device="cuda")
+    got = layer.dgrad(dy, out=dx[:, :k])
+    w4 = R.quantise(wv, "e2m1")[2]
+    close(got, dyv @ w4, accumulation(dyv, w4), out, "dx")
+    assert (dx[:, k:] == 55.0).all()
+
+
+@pytest.mark.parametrize("m,n,k,pad", SHAPES)
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_wgrad(m, n, k, pad, fmt):
+    say(f"[gpu] ckpt8 wgrad {fmt} {m}x{n}x{k}+{pad}")
+    dy, dyv = matrix(m, n, "bf16", pad, seed=m, scale=0.1)
+    x, xv = matrix(m, k, "f32", pad, seed=k)
+    layer = lq.Mx4Linear(torch.zeros(n, k, device="cuda"), rows=m)
+    kept = lq.Ckpt8(m, k, fmt)
+    kept.save(x)
+    x8 = R.quantise(xv, fmt)[2]
+    want, acc = dyv.T @ x8, accumulation(np.ascontiguousarray(dyv.T), x8)
+    got = layer.wgrad(dy, kept).clone()
+    close(got, want, acc, "f32", "dw")
+    # added to what is there, in place and out of place, with rows apart
+    base, bv = matrix(n, k, "f32", pad, seed=9)
+    out = torch.full((n, k + pad), 55.0, device="cuda")
+    layer.wgrad(dy, kept, dw_in=base, out=out[:, :k])
+    close(out[:, :k], want + bv, acc + 2.0 ** -24 * (np.abs(bv) + np.abs(want)), "f32", "dw + dw_in")
+    assert (out[:, k:] == 55.0).all()
+    layer.wgrad(dy, kept, dw_in=base, out=base)
+    assert torch.equal(base, out[:, :k])
+
+
+ACT = [(1, 1, 0), (2, 31, 1), (3, 33, 0), (5, 100, 5), (16, 512, 0), (7, 1001, 3), (64, 4096, 8), (129, 2050, 0)]
+
+
+@pytest.mark.parametrize("rows,cols,pad", ACT)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_swiglu(rows, cols, pad, dtype, fmt):
+    say(f"[gpu] swiglu {dtype} {fmt} {rows}x{cols}+{pad}")
+    g, gv = matrix(rows, cols, dtype, pad, seed=1, scale=2.0)
+    u, uv = matrix(rows, cols, dtype, pad, seed=2)
+    dh, dhv = matrix(rows, cols, dtype, pad, seed=3)
+    act = lq.SwigluCkpt8(rows, cols, dtype, fmt)
+    h = torch.full((rows, cols + pad), 55.0, dtype=T[dtype], device="cuda")
+    act.forward(g, u, out=h[:, :cols])
+    # exp, 1 + e, the quotient and two products, each within 2^-23 relative; outputs below the normal range
+    # of binary32 (exp overflows past g = -88) lie within 2^-120 of zero
+    rel = 16 * 2.0 ** -24
+    want = R.swiglu(gv, uv)
+    close(h[:, :cols], want, rel * np.abs(want) + 2.0 ** -120, dtype, "h")
+    assert (h[:, cols:] == 55.0).all()
+    g8, u8 = R.quantise(gv, fmt), R.quantise(uv, fmt)
+    for kept, ref in ((act.gate, g8), (act.up, u8)):
+        assert np.array_equal(kept.codes.cpu().numpy()[:ref[0].size].reshape(ref[0].shape), ref[0])
+        assert np.array_equal(kept.scales.cpu().numpy()[:ref[1].size].reshape(ref[1].shape), ref[1])
+    out = [torch.full((rows, cols + pad), 55.0, dtype=T[dtype], device="cuda") for _ in range(2)]
+    act.backward(dh, out=[t[:, :cols] for t in out])
+    dg, du = R.swiglu_grad(g8[2], u8[2], dhv)
+    s = R.silu_parts(g8[2])
+    # 1 + g (1 - s) adds terms of magnitude 1 and |g|: its error is absolute
+    close(out[0][:, :cols], dg, rel * np.abs(dhv * u8[2] * s) * (1 + np.abs(g8[2])) + 2.0 ** -120, dtype, "dgate")
+    close(out[1][:, :cols], du, rel * np.abs(du) + 2.0 ** -120, dtype, "dup")
+    assert all((t[:, cols:] == 55.0).all() for t in out)
+
+
+def test_swiglu_gradient_against_differences():
+    """The GPU's own forward, differenced, against its backward: gate and up are multiples of 1/16 that an
+    INT8 checkpoint holds exactly. Central difference of step 1/64: error step^2/6 |h'''| <= 4.1e-5 * 0.6
+    (|silu'''| < 0.6) * |u|, plus rounding 2^-22 |h| / (2 step)."""
+    gen = torch.Generator().manual_seed(4)
+    g = (torch.randint(-60, 61, (8, 256), generator=gen).float() / 16).cuda()
+    u = (torch.randint(-60, 61, (8, 256), generator=gen).float() / 16).cuda()
+    one = torch.ones_like(g)
+    act = lq.SwigluCkpt8(8, 256, "f32", "int8")
+    act.forward(g, u)
+    dg, du = (t.clone() for t in act.backward(one))
+    probe = lq.SwigluCkpt8(8, 256, "f32", "int8")
+    e = 1 / 64
+    for num, an, slack in (((probe.forward(g + e, u).clone() - probe.forward(g - e, u)) / (2 * e), dg, 4.1e-5 * 0.6 * 4),
+                           ((probe.forward(g, u + e).clone() - probe.forward(g, u - e)) / (2 * e), du, 0.0)):
+        assert (num - an).abs().max().item() <= slack + 2.0 ** -22 * 16 * 32 + 1e-6
+
+
+def test_linear_gradients_against_differences():
+    """f(x, W) = sum(dy * (x8 W^T)) is linear in either: the gradients reproduce differences along random
+    directions, all in the layer's own quantised values (64-bit sums on the host)."""
+    m, n, k = 40, 72, 96
+    w, wv = matrix(n, k, "bf16", seed=1, scale=0.05)
+    x, xv = matrix(m, k, "f32", seed=2)
+    dy, dyv = matrix(m, n, "bf16", seed=3)
+    layer = lq.Mx4Linear(w, rows=m, out="f32")
+    kept = lq.Ckpt8(m, k, "int8")
+    kept.save(x)
+    w4, x8 = R.quantise(wv, "e2m1")[2], R.quantise(xv, "int8")[2]
+    dx, dw = layer.dgrad(dy).double().cpu().numpy(), layer.wgrad(dy, kept).double().cpu().numpy()
+    rng = np.random.default_rng(0)
+    f = lambda a, b: (dyv * (a @ b.T)).sum()
+    for _ in range(4):
+        px, pw = rng.normal(size=(m, k)), rng.normal(size=(n, k))
+        tx = (np.abs(px) * accumulation(dyv, w4)).sum() + 2.0 ** -24 * np.abs(dx * px).sum()
+        tw = (np.abs(pw) * accumulation(np.ascontiguousarray(dyv.T), x8)).sum() + 2.0 ** -24 * np.abs(dw * pw).sum()
+        assert abs((f(x8 + px, w4) - f(x8 - px, w4)) / 2 - (dx * px).sum()) <= tx + 1e-9
+        assert abs((f(x8, w4 + pw) - f(x8, w4 - pw)) / 2 - (dw * pw).sum()) <= tw + 1e-9
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_spoiled_blocks_show(bad):
+    """A non-finite element makes NaN of all that its block enters, and of nothing else."""
+    m, n, k = 40, 70, 160
+    for dtype in ("bf16", "f32"):
+        x, xv = matrix(m, k, dtype, seed=1)
+        x[3, 33] = bad
+        x[20, k - 1] = bad
+        xv = x.double().cpu().numpy()
+        w, wv = matrix(n, k, "bf16", seed=2)
+        w[5, 64] = bad
+        wv = w.double().cpu().numpy()
+        for rows in (m, 4, 1):
+            layer = lq.Mx4Linear(w, rows=rows, dtype=dtype, out="f32")
+            kept = lq.Ckpt8(rows, k, "int8")
+            lo = 3 if rows == 1 else 0
+            y = layer.forward(x[lo:lo + rows].clone(), ckpt=kept).cpu()
+            want = torch.zeros(rows, n, dtype=torch.bool)
+            want[:, 5] = True
+            if rows == 1:
+                want[0] = True
+            else:
+                want[3] = True
+                if rows > 20:
+                    want[20] = True
+            assert torch.equal(torch.isnan(y), want), (dtype, rows)
+            assert torch.isfinite(y[~want]).all()
+            dy, _ = matrix(rows, n, "bf16", seed=3)
+            dx = layer.dgrad(dy).cpu()
+            assert torch.isnan(dx[:, 64:96]).all() and torch.isfinite(dx[:, :64]).all() and torch.isfinite(dx[:, 96:]).all()
+            dw = layer.wgrad(dy, kept).cpu()
+            cols = torch.zeros(k, dtype=torch.bool)
+            cols[32:64] = True
+            if rows > 20:
+                cols[128:] = True
+            assert torch.isnan(dw[:, cols]).all() and torch.isfinite(dw[:, ~cols]).all()
+    for fmt in ("int8", "e4m3"):
+        g, _ = matrix(4, 100, "f32", seed=1)
+        u, _ = matrix(4, 100, "f32", seed=2)
+        u[1, 40] = bad
+        act = lq.SwigluCkpt8(4, 100, "f32", fmt)
+        h = act.forward(g, u).cpu()
+        assert not torch.isfinite(h[1, 40]) and torch.isfinite(h).sum() == h.numel() - 1
+        dg, du = (t.cpu() for t in act.backward(torch.ones_like(g)))
+        assert torch.isnan(dg[1, 32:64]).all() and torch.isnan(dg).sum() == 32 and torch.isfinite(du).all()
+
+
+def test_nonfinite_gradients_pass_through():
+    """An infinity or a NaN in dy reaches what it multiplies."""
+    m, n, k = 33, 40, 64
+    dy, _ = matrix(m, n, "bf16", seed=1)
+    dy[2, 3] = float("nan")
+    w, _ = matrix(n, k, "bf16", seed=2)
+    layer = lq.Mx4Linear(w, rows=m, out="f32")
+    dx = layer.dgrad(dy)
+    assert torch.isnan(dx[2]).all() and torch.isfinite(dx[3:]).all() and torch.isfinite(dx[:2]).all()
+    kept = lq.Ckpt8(m, k, "int8")
+    kept.save(torch.randn(m, k, device="cuda"))
+    dw = layer.wgrad(dy, kept)
+    assert torch.isnan(dw[3]).all() and torch.isfinite(dw[4:]).all() and torch.isfinite(dw[:3]).all()
+
+
+def test_empty_sides():
+    layer = lq.Mx4Linear(torch.randn(40, 64, device="cuda"), rows=8, dtype="f32", out="f32")
+    assert layer.forward(torch.empty(0, 64, device="cuda")).shape == (0, 40)
+    assert layer.dgrad(torch.empty(0, 40, device="cuda", dtype=torch.bfloat16)).shape == (0, 64)
+    none = lq.Ckpt8(0, 64)
+    none.save(torch.empty(0, 64, device="cuda"))
+    no_rows = torch.empty(0, 40, device="cuda", dtype=torch.bfloat16)
+    out = torch.full((40, 64), 7.0, device="cuda")
+    assert (layer.wgrad(no_rows, none, out=out) == 0).all()
+    base = torch.randn(40, 64, device="cuda")
+    assert torch.equal(layer.wgrad(no_rows, none, dw_in=base, out=out), base)
+    flat = lq.Mx4Linear(torch.empty(40, 0, device="cuda"), rows=8, dtype="f32", out="f32")
+    y = torch.full((8, 40), 7.0, device="cuda")
+    assert (flat.forward(torch.empty(8, 0, device="cuda"), out=y) == 0).all()
+    thin = lq.Mx4Linear(torch.empty(0, 64, device="cuda"), rows=8, out="f32")
+    dx = torch.full((8, 64), 7.0, device="cuda")
+    assert (thin.dgrad(torch.empty(8, 0, device="cuda", dtype=torch.bfloat16), out=dx) == 0).all()
+    act = lq.SwigluCkpt8(0, 64)
+    e = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
+    assert act.forward(e, e).shape == (0, 64)
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^32 elements: the last rows equal a small call's."""
+    m, k = 70016, 65536
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(16, k, device="cuda").to(torch.bfloat16)
+    x[-16:] = tail
+    kept, small = lq.Ckpt8(m, k), lq.Ckpt8(16, k)
+    say("[gpu] checkpoint of 70016 x 65536")
+    kept.save(x)
+    small.save(tail)
+    assert torch.equal(kept.codes[-16 * k:], small.codes)
+    assert torch.equal(kept.scales[-16 * k // 32:], small.scales)
+    del kept, small
+    w = torch.randn(8, k, device="cuda")
+    layer, few = lq.Mx4Linear(w, rows=m), lq.Mx4Linear(w, rows=300)
+    say("[gpu] linear of 70016 x 8 x 65536")
+    # (the last 300 rows of a call go through the same tiles as a call of 300 that starts on a tile's edge)
+    y = layer.forward(x)
+    part = few.forward(x[-300:])
+    close(y[-300:], part.double().cpu().numpy(), np.zeros((300, 8)), "bf16", "y of the last rows")
+    del layer, y
+    say("[gpu] swiglu of 70016 x 65536")
+    act = lq.SwigluCkpt8(m, k)
+    h = act.forward(x, x)
+    ref = lq.SwigluCkpt8(16, k)
+    assert torch.equal(h[-16:], ref.forward(tail, tail))
+    dg, du = act.backward(x)
+    rg, ru = ref.backward(tail)
+    assert torch.equal(dg[-16:], rg) and torch.equal(du[-16:], ru)
+    del act, h, dg, du, x
+    say("[gpu] wide products of 66000 x 66000 x 32")
+    n = 66000
+    w = torch.randn(n, 32, device="cuda")
+    wide, few = lq.Mx4Linear(w, rows=n, dtype="f32"), lq.Mx4Linear(w[-64:].contiguous(), rows=64, dtype="f32")
+    xs = torch.randn(n, 32, device="cuda")
+    y = wide.forward(xs)
+    assert torch.equal(y[-64:, -64:], few.forward(xs[-64:]))
+    dx = wide.dgrad(y)
+    w4 = R.quantise(w.cpu().numpy(), "e2m1")[2]
+    yv = y[-2:].double().cpu().numpy()
+    close(dx[-2:], yv @ w4, accumulation(yv, w4), "bf16", "dx of the last rows")
+    kept = lq.Ckpt8(n, 32)
+    kept.save(xs)
+    dw = wide.wgrad(y, kept)
+    x8 = R.quantise(xs.cpu().numpy(), "int8")[2]
+    cols = np.ascontiguousarray(y[:, -2:].double().cpu().numpy().T)
+    close(dw[-2:], cols @ x8, accumulation(cols, x8), "f32", "dw of the last rows")
+
+
+def _step(layer, act, x, dy, kept, acc):
+    y = layer.forward(x, ckpt=kept)
+    h = act.forward(y, y)
+    dg, du = act.backward(dy)
+    dx = layer.dgrad(dg)
+    dw = layer.wgrad(du, kept, dw_in=acc)
+    return [y, h, dg, du, dx, dw, kept.codes, kept.scales]
+
+
+@pytest.mark.parametrize("m", [1, 9, 200])
+def test_streams_and_graphs(m):
+    """The same bits on another stream, and from a captured graph replayed between eager work."""
+    n, k = 320, 512
+    x, _ = matrix(m, k, "bf16", seed=1)
+    w, _ = matrix(n, k, "bf16", seed=2)
+    dy, _ = matrix(m, n, "bf16", seed=3)
+    acc = torch.randn(n, k, device="cuda")
+
+    def objects():
+        return lq.Mx4Linear(w, rows=m), lq.SwigluCkpt8(m, n), lq.Ckpt8(m, k)
+
+    layer, act, kept = objects()
+    want = [t.clone() for t in _step(layer, act, x, dy, kept, acc)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    l2, a2, k2 = objects()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = _step(l2, a2, x, dy, k2, acc)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    l3, a3, k3 = objects()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        _step(l3, a3, x, dy, k3, acc)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _step(l3, a3, x, dy, k3, acc)
+    for i in range(4):
+        for t in got:
+            t.zero_()
+        torch.randn(1000, 1000, device="cuda").sum()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+        _step(layer, act, x, dy, kept, acc)
+
+
+def test_repeats_give_the_same_bits():
+    m, n, k = 300, 500, 700
+    x, _ = matrix(m, k, "bf16", seed=1)
+    w, _ = matrix(n, k, "bf16", seed=2)
+    dy, _ = matrix(m, n, "bf16", seed=3)
+    layer, act, kept = lq.Mx4Linear(w, rows=m), lq.SwigluCkpt8(m, n), lq.Ckpt8(m, k)
+    acc = torch.randn(n, k, device="cuda")
+    want = [t.clone() for t in _step(layer, act, x, dy, kept, acc)]
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(_step(layer, act, x, dy, kept, acc), want))
+
+
+def test_refusals_of_the_classes():
+    layer = lq.Mx4Linear(torch.randn(40, 64, device="cuda"), rows=8)
+    bf = dict(device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        layer.forward(torch.zeros(9, 64, **bf))            # more rows than planned
+    with pytest.raises(ValueError):
+        layer.forward(torch.zeros(8, 65, **bf))
+    with pytest.raises(TypeError):
+        layer.forward(torch.zeros(8, 64, device="cuda"))
+    with pytest.raises(ValueError):
+        layer.forward(torch.zeros(64, 8, **bf).t())        # rows not contiguous
+    with pytest.raises(lq.LQError):
+        layer.forward(torch.zeros(8, 65, **bf)[:, 1:])     # not 16-byte aligned
+    with pytest.raises(ValueError):
+        layer.forward(torch.zeros(8, 64, **bf), ckpt=lq.Ckpt8(7, 64))
+    with pytest.raises(TypeError):
+        layer.dgrad(torch.zeros(8, 40, device="cuda"))
+    with pytest.raises(ValueError):
+        lq.SwigluCkpt8(4, 64).forward(torch.zeros(4, 64, **bf), torch.zeros(4, 72, **bf)[:, :64])
+    with pytest.raises(lq.LQError):
+        lq.Ckpt8(4, 64, "e5m2").save(torch.zeros(4, 64, device="cuda"))
