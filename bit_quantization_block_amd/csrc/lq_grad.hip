@@ -32,7 +32,6 @@ __global__ __launch_bounds__(256) void k_mx4_dgrad(const uint16_t* dy, int64_t m
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t across = (k + 63) / 64;
   const int64_t row0 = blockIdx.x / across * 64, col0 = blockIdx.x % across * 64;
-  const int64_t p = mx4_pitch(k), sp = mx4_scale_pitch(k);
   v16f acc;
 #pragma unroll
   for (int i = 0; i < 16; i++) acc[i] = 0.0f;
@@ -43,10 +42,10 @@ __global__ __launch_bounds__(256) void k_mx4_dgrad(const uint16_t* dy, int64_t m
       const int64_t col = col0 + e % 64, jw = j0 + e / 64;
       uint16_t b = 0;
       if (col < k && jw < n) {
-        const uint32_t c = w[jw * p + col / 2] >> (4 * (col & 1)) & 15u;
+        const uint32_t c = w[mx4_code_at(n, jw, col)] >> (4 * (col & 1)) & 15u;
         float v[8];
         lqd::fp4_unpack8(c, v);
-        b = narrow<LQ_BF16>(v[0] * scale_value(ws[jw * sp + col / 32]));
+        b = narrow<LQ_BF16>(v[0] * scale_value(ws[mx4_scale_at(n, jw, col)]));
       }
       t.b[e % 64][e / 64] = b;
     }

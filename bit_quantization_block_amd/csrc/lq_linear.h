@@ -4,13 +4,19 @@
 //
 // Two stored forms of a rows x cols matrix, both in blocks of 32 along a row
 // with one UE8M0 scale each, the smallest 2^e with Qmax * 2^e >= max|block|:
-//   MX4 operand    E2M1 codes, rows padded with zeros to 256 elements (128
-//                  bytes), scale rows padded to 16 bytes: a row's codes and
-//                  scales can be read 16 bytes at a time whatever cols is
+//   MX4 operand    E2M1 codes in groups of 128 columns, group by group, a
+//                  group's 64 bytes of every row one after the other; scales
+//                  likewise, 4 bytes a row (rows padded to a multiple of 4).
+//                  Elements past cols are zeros. The rows of a tile then have
+//                  each step's codes and scales in one stretch of whole cache
+//                  lines (with each row in one stretch instead, a step's 64
+//                  bytes a row cost the memory pipe as much as 128, and its
+//                  scales more than its codes).
 //   8-bit checkpoint  INT8 or E4M3 codes, rows padded with zeros to 32
 //                  elements; one scale byte per block
-// For cols a multiple of 512 (MX4) or 32 (checkpoint) they are byte for byte
-// what lq_quantize writes for E2M1 / INT8 / E4M3, PER_BLOCK 32, UE8M0.
+// For cols a multiple of 32 the checkpoint is byte for byte what lq_quantize
+// writes for INT8 / E4M3, PER_BLOCK 32, UE8M0; the MX4 operand holds the codes
+// and scales that it writes for E2M1, in another order.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -23,8 +29,15 @@ namespace lql {
 
 constexpr int kBlock = 32;
 
-__host__ __device__ inline int64_t mx4_pitch(int64_t cols) { return (cols + 255) / 256 * 128; }        // bytes of a code row
-__host__ __device__ inline int64_t mx4_scale_pitch(int64_t cols) { return (cols + 511) / 512 * 16; }   // bytes of a scale row
+__host__ __device__ inline int64_t mx4_groups(int64_t cols) { return (cols + 127) / 128; }
+__host__ __device__ inline int64_t mx4_scale_rows(int64_t rows) { return (rows + 3) / 4 * 4; }
+// Places of the byte that holds a row's element col, and of the scale of its block.
+__host__ __device__ inline int64_t mx4_code_at(int64_t rows, int64_t row, int64_t col) {
+  return ((col >> 7) * rows + row) * 64 + (col >> 1 & 63);
+}
+__host__ __device__ inline int64_t mx4_scale_at(int64_t rows, int64_t row, int64_t col) {
+  return ((col >> 7) * mx4_scale_rows(rows) + row) * 4 + (col >> 5 & 3);
+}
 __host__ __device__ inline int64_t ckpt_pitch(int64_t cols) { return (cols + 31) / 32 * 32; }
 __host__ __device__ inline int64_t ckpt_scale_pitch(int64_t cols) { return (cols + 31) / 32; }
 
@@ -180,6 +193,7 @@ inline unsigned stream_grid(int64_t units) {
 // (lq_mx4.hip, lq_grad.hip, lq_swiglu.hip; arguments checked by lq_linear.hip)
 hipError_t launch_mx4_quantize(int in_dtype, int ckpt_format, const void* x, int64_t m, int64_t k, int64_t ldx,
                                void* codes, void* scales, void* ckpt_codes, void* ckpt_scales, hipStream_t s);
+hipError_t launch_constant(int64_t rows, int64_t cols, int dtype, const void* in, void* y, int64_t ldy, hipStream_t s);
 hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
                               int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s);
 hipError_t launch_mx4_dgrad(const void* dy, int64_t m, int64_t n, int64_t lddy, const void* w_codes,

@@ -35,9 +35,9 @@ int check_linear(const lq_linear_desc* d) {
 // The forward call's copy of x as an MX4 operand: codes, then scales, each
 // from a multiple of 256 bytes.
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
-size_t operand_codes(const lq_linear_desc* d) { return round256((size_t)(d->m * mx4_pitch(d->k))); }
+size_t operand_codes(const lq_linear_desc* d) { return round256((size_t)(d->m * mx4_groups(d->k) * 64)); }
 size_t operand_bytes(const lq_linear_desc* d) {
-  return operand_codes(d) + round256((size_t)(d->m * mx4_scale_pitch(d->k)));
+  return operand_codes(d) + round256((size_t)(mx4_scale_rows(d->m) * mx4_groups(d->k) * 4));
 }
 
 }  // namespace
@@ -45,10 +45,10 @@ size_t operand_bytes(const lq_linear_desc* d) {
 extern "C" {
 
 size_t lq_mx4_codes_bytes(int64_t rows, int64_t cols) {
-  return is_side(rows) && is_side(cols) ? (size_t)(rows * mx4_pitch(cols)) : 0;
+  return is_side(rows) && is_side(cols) ? (size_t)(rows * mx4_groups(cols) * 64) : 0;
 }
 size_t lq_mx4_scales_bytes(int64_t rows, int64_t cols) {
-  return is_side(rows) && is_side(cols) ? (size_t)(rows * mx4_scale_pitch(cols)) : 0;
+  return is_side(rows) && is_side(cols) ? (size_t)(mx4_scale_rows(rows) * mx4_groups(cols) * 4) : 0;
 }
 size_t lq_ckpt8_codes_bytes(int64_t rows, int64_t cols) {
   return is_side(rows) && is_side(cols) ? (size_t)(rows * ckpt_pitch(cols)) : 0;

@@ -1,4 +1,7 @@
 // lq_mx4.hip — 4-bit microscaled quantisation and product.
+#include <atomic>
+#include <type_traits>
+
 #include "lq_linear.h"
 
 namespace lql {
@@ -9,68 +12,366 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 // ---------------------------------------------------------------- quantise
-// One wave per 512 columns of a row; a lane holds 8 consecutive elements, so
-// every load and store instruction of a wave covers one stretch of whole
-// lines, and a block of 32 is the four lanes of a quad. One read of x gives
-// the 4-bit operand and the 8-bit checkpoint.
+// One wave per 4 rows x 128 columns; a lane holds 8 consecutive elements, so a
+// block of 32 is the four lanes of a quad, and the wave's codes are 256 bytes
+// in one stretch. One read of x gives the 4-bit operand and the 8-bit
+// checkpoint.
 template <int DT, int F>
 __global__ __launch_bounds__(256) void k_mx4_quantize(const void* x, int64_t m, int64_t k, int64_t ldx,
                                                       uint8_t* codes, uint8_t* scales, uint8_t* ck, uint8_t* cks) {
-  const int64_t segs = (k + 511) / 512;
-  for (int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); unit < m * segs; unit += (int64_t)gridDim.x * 4) {
-  const int64_t row = unit / segs;
+  const int64_t bands = (m + 3) / 4, units = bands * mx4_groups(k);
   const int lane = threadIdx.x & 63;
-  const int64_t col = (unit % segs) * 512 + lane * 8;
-  const int valid = col >= k ? 0 : (k - col >= 8 ? 8 : (int)(k - col));
-  float v[8];
-  load8<DT>((const typename El<DT>::T*)x + row * ldx, col, valid, v);
-  const uint32_t amax = quad_max(amax8_bits(v));
-  if (codes) {
-    const uint32_t sb = scale_byte<LQ_E2M1>(amax);
-    const uint32_t w = encode_e2m1(v, scale_recip(sb));
-    if (col < (k + 255) / 256 * 256) *(uint32_t*)(codes + row * mx4_pitch(k) + col / 2) = w;
-    if ((lane & 3) == 0) scales[row * mx4_scale_pitch(k) + col / 32] = (uint8_t)sb;
-  }
-  if (ck && col < ckpt_pitch(k)) {
-    const uint32_t sb = scale_byte<F>(amax);
-    const uint2 w = encode8<F>(v, scale_recip(sb));
-    *(uint2*)(ck + row * ckpt_pitch(k) + col) = w;
-    if ((lane & 3) == 0) cks[row * ckpt_scale_pitch(k) + col / 32] = (uint8_t)sb;
-  }
+  for (int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); unit < units; unit += (int64_t)gridDim.x * 4) {
+    const int64_t row = unit % bands * 4 + (lane >> 4), col = unit / bands * 128 + (lane & 15) * 8;
+    const int valid = row >= m || col >= k ? 0 : (k - col >= 8 ? 8 : (int)(k - col));
+    float v[8];
+    load8<DT>((const typename El<DT>::T*)x + row * ldx, col, valid, v);
+    const uint32_t amax = quad_max(amax8_bits(v));
+    if (row >= m) continue;
+    if (codes) {
+      const uint32_t sb = scale_byte<LQ_E2M1>(amax);
+      *(uint32_t*)(codes + mx4_code_at(m, row, col)) = encode_e2m1(v, scale_recip(sb));
+      if ((lane & 3) == 0) scales[mx4_scale_at(m, row, col)] = (uint8_t)sb;
+    }
+    if (ck && col < ckpt_pitch(k)) {
+      const uint32_t sb = scale_byte<F>(amax);
+      *(uint2*)(ck + row * ckpt_pitch(k) + col) = encode8<F>(v, scale_recip(sb));
+      if ((lane & 3) == 0) cks[row * ckpt_scale_pitch(k) + col / 32] = (uint8_t)sb;
+    }
   }
 }
 
 // ---------------------------------------------------------------- product
-// One wave per 32 x 32 tile of y, operands straight from memory.
-template <int OUT>
-__global__ __launch_bounds__(256) void k_mx4_product(const uint8_t* a, const uint8_t* as, const uint8_t* w,
-                                                     const uint8_t* ws, int64_t m, int64_t n, int64_t k, void* y,
-                                                     int64_t ldy) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t across = (n + 63) / 64;
-  const int64_t row0 = blockIdx.x / across * 64 + (wave >> 1) * 32, col0 = blockIdx.x % across * 64 + (wave & 1) * 32;
-  const int r = lane & 31, h = lane >> 5;
-  const int64_t ar = row0 + r < m ? row0 + r : m - 1, wr = col0 + r < n ? col0 + r : n - 1;
-  const int64_t p = mx4_pitch(k), sp = mx4_scale_pitch(k);
-  v16f acc;
+// y = x W^T on the matrix cores: v_mfma_scale_f32_32x32x64_f8f6f4 takes 32
+// E2M1 codes and a scale byte per lane, so a lane's operand is exactly one
+// stored block and nothing is converted. The contraction's order is free as
+// long as both operands agree: within a step of 128, half h of a wave takes
+// blocks 2h and 2h+1, whose scales are two neighbouring bytes.
+//
+// A workgroup of 2 x 2 waves makes (64 FM) x (64 FN) tiles, 32 FM x 32 FN per
+// wave, one after the other. Codes and scales go from memory to LDS without
+// passing through registers, a step of 128 of the contraction (64 bytes a row)
+// at a time into a ring of four stages, three of them in flight; the transfers
+// run on across the end of a tile, so the next tile starts with its first steps
+// in LDS, and a tile's results leave through a part of LDS of their own.
+constexpr int kStages = 4;
+// A row's four 16-byte units are stored in the order u ^ (row / 4 & 3): the 16
+// lanes that the LDS serves at a time (0-3, 12-15, 20-27 and so on) then read
+// 16 different units of 256 bytes.
+__device__ __forceinline__ int swizzled(int row, int unit) { return (unit ^ (row >> 2 & 3)) * 16; }
+
+// A stretch of memory for buffer loads: what lies past its end reads as zero.
+__device__ __forceinline__ v4i stretch(const uint8_t* p, uint32_t bytes) {
+  const uint64_t b = (uint64_t)(uintptr_t)p;
+  const v4i d = {(int)__builtin_amdgcn_readfirstlane((uint32_t)b), (int)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)),
+                 (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000};
+  return d;
+}
+// 16 bytes per lane from the stretch's byte `offset` on to LDS address lds + 16 * lane.
+__device__ __forceinline__ void to_lds(v4i from, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+               "v"(offset), "s"(from)
+               : "memory");
+}
+// Waits until all but the wave's N newest transfers (and stores) are done and
+// its LDS reads have returned, then for the workgroup.
+template <int N>
+__device__ __forceinline__ void drain_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <int FM, int FN>
+struct ProductLds {
+  static constexpr int kOut = FM * FN >= 16 ? 4096 : 2048;   // bytes a wave turns results through
+  __attribute__((aligned(128))) uint8_t x[kStages][64 * FM][64];
+  __attribute__((aligned(128))) uint8_t w[kStages][64 * FN][64];
+  __attribute__((aligned(128))) uint8_t s[kStages][2][256][4];   // scales of x, of W
+  __attribute__((aligned(128))) uint8_t out[4][kOut];
+};
+
+// Tile i of an XCD's share. Consecutive workgroups go round-robin to the 8
+// XCDs, each with an L2 of its own: an XCD takes a contiguous run of the tiles,
+// ordered in bands of 4 rows of tiles, so that the 32 tiles it works on at a
+// time share 4 row blocks of x and 8 of W.
+__device__ __forceinline__ void tile_at(uint32_t t, uint32_t tm, uint32_t tn, uint32_t& row, uint32_t& col) {
+  const uint32_t band = t / (4 * tn), first = band * 4, high = tm - first < 4 ? tm - first : 4, in = t - band * 4 * tn;
+  row = __builtin_amdgcn_readfirstlane(first + in % high);
+  col = __builtin_amdgcn_readfirstlane(in / high);
+}
+
+template <int OUT, int FM, int FN>
+__global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
+                                                        int64_t m, int64_t n, int64_t k, void* y, int64_t ldy,
+                                                        uint32_t tm, uint32_t tn) {
+  typedef typename El<OUT>::T T;
+  constexpr int BM = 64 * FM, BN = 64 * FN;
+  __shared__ ProductLds<FM, FN> lds;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
+
+  // This workgroup's tiles: its XCD's share, every `slots`-th from its own on.
+  const uint32_t total = tm * tn, xcd = blockIdx.x % 8, slots = (gridDim.x - xcd + 7) / 8;
+  const uint32_t per = total / 8, more = total % 8, begin = xcd * per + (xcd < more ? xcd : more);
+  const uint32_t end = begin + per + (xcd < more ? 1 : 0);
+  uint32_t tile = begin + blockIdx.x / 8;
+  if (tile >= end) return;
+
+  // A tile takes at least four steps, so that the transfers reach into the next
+  // tile only; steps past the contraction's end read zeros.
+  const int groups = (int)mx4_groups(k), steps = groups < 4 ? 4 : groups;
+  struct Tile {
+    const uint8_t *x, *w, *xs, *ws;   // codes and scales of its first rows, in group 0
+    uint32_t rows, cols;              // that exist, at most BM and BN; 0: no tile
+  };
+  auto place = [&](uint32_t row, uint32_t col, bool real) {
+    const int64_t r0 = (int64_t)row * BM, c0 = (int64_t)col * BN;
+    Tile t;
+    t.x = x + r0 * 64;
+    t.w = w + c0 * 64;
+    t.xs = xs + r0 * 4;
+    t.ws = ws + c0 * 4;
+    t.rows = real ? (uint32_t)(m - r0 < BM ? m - r0 : BM) : 0;
+    t.cols = real ? (uint32_t)(n - c0 < BN ? n - c0 : BN) : 0;
+    return t;
+  };
+  uint32_t trow, tcol, nrow, ncol;
+  tile_at(tile, tm, tn, trow, tcol);
+  Tile now = place(trow, tcol, true), next;
+  uint32_t following;
+  auto look_ahead = [&] {
+    following = tile + slots;
+    tile_at(following < end ? following : tile, tm, tn, nrow, ncol);
+    next = place(nrow, ncol, following < end);
+  };
+  look_ahead();
+
+  // One transfer is 16 rows of codes, or the scales of up to 256 rows (even
+  // waves fetch those of x, odd ones those of W).
+  constexpr int kFetches = FM + FN + 1;
+  uint32_t xo[FM], wo[FN];
 #pragma unroll
-  for (int i = 0; i < 16; i++) acc[i] = 0.0f;
-  for (int64_t b = h; b < p / 16; b += 2) {
-    const v4i av = *(const v4i*)(a + ar * p + b * 16), wv = *(const v4i*)(w + wr * p + b * 16);
-    const v8i A = {av[0], av[1], av[2], av[3], 0, 0, 0, 0}, W = {wv[0], wv[1], wv[2], wv[3], 0, 0, 0, 0};
-    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, W, acc, 4, 4, 0, as[ar * sp + b], 0, ws[wr * sp + b]);
+  for (int i = 0; i < FM; i++) {
+    const uint32_t t = (wave * FM + i) * 16 + (lane >> 2);
+    xo[i] = t * 64 + swizzled(t, lane & 3);
   }
 #pragma unroll
-  for (int i = 0; i < 16; i++) {
-    const int64_t row = row0 + 8 * (i / 4) + 4 * h + i % 4, col = col0 + r;
-    if (row < m && col < n) ((typename El<OUT>::T*)y)[row * ldy + col] = narrow<OUT>(acc[i]);
+  for (int i = 0; i < FN; i++) {
+    const uint32_t t = (wave * FN + i) * 16 + (lane >> 2);
+    wo[i] = t * 64 + swizzled(t, lane & 3);
   }
+  auto lds_at = [](const void* p) { return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p; };
+  const uint32_t lx = lds_at(&lds.x[0][wave * FM * 16][0]), lw = lds_at(&lds.w[0][wave * FN * 16][0]), ls = lds_at(&lds.s[0][wave & 1][0][0]);
+  const int64_t xgroup = m * 64, wgroup = n * 64, sgroup = mx4_scale_rows(wave & 1 ? n : m) * 4;
+  // The step whose transfers come next: what is left of its rows in memory.
+  struct Cursor {
+    const uint8_t *x, *w, *s;
+    int t;
+  } at = {now.x, now.w, wave & 1 ? now.ws : now.xs, 0};
+  uint32_t xbytes = now.rows * 64, wbytes = now.cols * 64, sbytes = ((wave & 1 ? now.cols : now.rows) + 3) / 4 * 16;
+  v4i fx, fw, fs;
+  auto point_x = [&] { fx = stretch(at.x, at.t < groups ? xbytes : 0); };
+  auto point_w = [&] { fw = stretch(at.w, at.t < groups ? wbytes : 0); };
+  auto point_s = [&] { fs = stretch(at.s, at.t < groups ? sbytes : 0); };
+  // (the transfers run four steps ahead: past the end of this tile, they are the next one's)
+  auto advance = [&] {
+    const bool wrap = ++at.t == steps;
+    at.x = wrap ? next.x : at.x + xgroup;
+    at.w = wrap ? next.w : at.w + wgroup;
+    at.s = wrap ? (wave & 1 ? next.ws : next.xs) : at.s + sgroup;
+    xbytes = wrap ? next.rows * 64 : xbytes;
+    wbytes = wrap ? next.cols * 64 : wbytes;
+    sbytes = wrap ? ((wave & 1 ? next.cols : next.rows) + 3) / 4 * 16 : sbytes;
+    at.t = wrap ? 0 : at.t;
+  };
+  // Transfer f into stage `st`.
+  auto fetch = [&](int st, int f) {
+    if (f < FM) to_lds(fx, xo[f], lx + st * BM * 64 + f * 1024);
+    else if (f < FM + FN) to_lds(fw, wo[f - FM], lw + st * BN * 64 + (f - FM) * 1024);
+    else to_lds(fs, lane * 16, ls + st * 2048);
+  };
+
+  // Operands of half a step: 32-row fragments of x and W; the scales of a step.
+  struct Operands { v4i x[FM], w[FN]; };
+  struct Scales { int x[FM], w[FN]; };
+  Operands A, B;
+  Scales E, F;
+  auto read = [&](int st, int s, Operands& o, int f) {
+    const int u = swizzled(r, 2 * h + s);
+    if (f < FM) o.x[f] = *(const v4i*)&lds.x[st][wm * 32 * FM + f * 32 + r][u];
+    else o.w[f - FM] = *(const v4i*)&lds.w[st][wn * 32 * FN + (f - FM) * 32 + r][u];
+  };
+  auto read_scale = [&](int st, Scales& e, int f) {
+    if (f < FM) e.x[f] = *(const uint16_t*)&lds.s[st][0][wm * 32 * FM + f * 32 + r][2 * h];
+    else e.w[f - FM] = *(const uint16_t*)&lds.s[st][1][wn * 32 * FN + (f - FM) * 32 + r][2 * h];
+  };
+  v16f acc[FM][FN];
+  // One half's products; `between` runs after each.
+  auto multiply = [&](auto which, const Operands& o, auto between) {
+    constexpr int s = decltype(which)::value;
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+      for (int j = 0; j < FN; j++) {
+        const v8i P = {o.w[j][0], o.w[j][1], o.w[j][2], o.w[j][3], 0, 0, 0, 0};
+        const v8i Q = {o.x[i][0], o.x[i][1], o.x[i][2], o.x[i][3], 0, 0, 0, 0};
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(P, Q, acc[i][j], 4, 4, s, E.w[j], s, E.x[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        between(i * FN + j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  };
+  typedef std::integral_constant<int, 0> First;
+  typedef std::integral_constant<int, 1> Second;
+
+  // Three steps, and the first transfers of a fourth (the rest run under the
+  // first products).
+  constexpr int early = (kFetches + 1) / 2, late = kFetches - early;
+#pragma unroll
+  for (int t = 0; t < 4; t++) {
+    if (t > 0) advance();
+    point_x();
+    point_w();
+    point_s();
+#pragma unroll
+    for (int f = 0; f < (t < 3 ? kFetches : early); f++) fetch(t, f);
+  }
+  drain_and_meet<2 * kFetches + early>();
+#pragma unroll
+  for (int f = 0; f < FM + FN; f++) {
+    read(0, 0, A, f);
+    read_scale(0, E, f);
+  }
+  int st = 0;
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+      for (int j = 0; j < FN; j++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
+    // A step. Under the first half's products the second half's operands are
+    // read, and the last of the transfers into the previous stage run. Then the
+    // next step has landed (two more are on their way) and nobody reads this
+    // stage any more: under the second half's products the next step's first
+    // operands are read and the transfers into this stage begin. Reads and
+    // transfers go one between two products: issued together they stall the
+    // wave, and the matrix core with it, until the memory pipes have taken them
+    // all. The scheduling barriers keep them there: left alone, the compiler
+    // moves all products below the last wait.
+    for (int t = 0; t < steps; t++) {
+      constexpr int per = FM * FN, reads = FM + FN;
+      const int before = (st + 3) & 3, after = (st + 1) & 3;
+      multiply(First(), A, [&](int done) {
+#pragma unroll
+        for (int f = 0; f < reads; f++)
+          if (f * per / (2 * reads) == done) read(st, 1, B, f);
+#pragma unroll
+        for (int f = 0; f < late; f++)
+          if (per / 2 + f * (per - per / 2) / (late + 1) == done) fetch(before, early + f);
+        if (done == per - 1) {
+          advance();
+          point_x();
+          point_w();
+          point_s();
+        }
+      });
+      drain_and_meet<2 * kFetches>();
+      multiply(Second(), B, [&](int done) {
+#pragma unroll
+        for (int f = 0; f < reads; f++)
+          if (f * per / (2 * reads) == done) {
+            read(after, 0, A, f);
+            read_scale(after, F, f);
+          }
+#pragma unroll
+        for (int f = 0; f < early; f++)
+          if (per / 2 + f * (per - per / 2) / early == done) fetch(st, f);
+      });
+      E = F;
+      st = after;
+    }
+
+    // A lane holds row r of a 32 x 32 block of y, columns 8q + 4h .. + 3: each
+    // wave turns 32 rows x CW columns at a time through LDS into row stretches.
+    // (The sums are pinned to accumulation registers up to here: the conversions
+    // below want ordinary ones, and the allocator would move the sums there and
+    // spill the rest. The lane's number is made opaque: every address of this part would
+    // otherwise be kept in registers through the whole loop over the tiles.)
+    constexpr int kRow = ProductLds<FM, FN>::kOut / 32, CW = kRow / (int)sizeof(T), V = 16 / (int)sizeof(T), units = CW / V;
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+      for (int j = 0; j < FN; j++) asm volatile("" : "+a"(acc[i][j]));
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    uint8_t* mine = lds.out[wave];
+    uint8_t* const put = mine + (l & 31) * kRow;
+    const int turn = (l & 31) >> 1, part = (l >> 5) * 4 * (int)sizeof(T);
+    const int64_t row0 = (int64_t)trow * BM + wm * 32 * FM, col0 = (int64_t)tcol * BN + wn * 32 * FN;
+    const int rr = l / units, cc = l % units;
+    T* const out = (T*)y + (row0 + rr) * ldy + col0 + cc * V;
+    const int rows_left = (int)(m - row0 < 32 * FM ? m - row0 : 32 * FM) - rr, cols_left = (int)(n - col0 < 32 * FN ? n - col0 : 32 * FN) - cc * V;
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+      for (int c = 0; c < 32 * FN / CW; c++) {
+#pragma unroll
+        for (int g = 0; g < CW / 8; g++) {
+          const int j = (c * CW + g * 8) / 32, q = (c * CW + g * 8) % 32 / 8;
+          T v[4];
+#pragma unroll
+          for (int e = 0; e < 4; e++) v[e] = narrow<OUT>(acc[i][j][4 * q + e]);
+          const int at = g * 8 * (int)sizeof(T) + part;
+          __builtin_memcpy(__builtin_assume_aligned(put + (((at >> 4) ^ turn) & (units - 1)) * 16 + (at & 15), 4 * sizeof(T)), v, sizeof(v));
+        }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int g = 0; g < units / 2; g++) {
+          constexpr int rows = 64 / units;   // a store instruction's
+          T v[V];
+          __builtin_memcpy(v, __builtin_assume_aligned(mine + (g * rows + rr) * kRow + ((cc ^ ((g * rows + rr) >> 1)) & (units - 1)) * 16, 16), 16);
+          if (i * 32 + g * rows < rows_left && c * CW < cols_left) {
+            T* o = out + (int64_t)(i * 32 + g * rows) * ldy + c * CW;
+            if (cols_left - c * CW >= V) {
+              __builtin_memcpy(o, v, 16);
+            } else {
+#pragma unroll
+              for (int e = 0; e < V; e++)
+                if (c * CW + e < cols_left) o[e] = v[e];
+            }
+          }
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    if (following >= end) break;
+    tile = following;
+    trow = nrow;
+    tcol = ncol;
+    now = next;
+    look_ahead();
+  }
+  // (the transfers after the last step wrote zeros into LDS: they end before it is given away)
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Compute units of the current device (256 on MI355X).
+int compute_units() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  int cus = cached[dev].load(std::memory_order_relaxed);
+  if (cus == 0) {
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) cus = 256;
+    cached[dev].store(cus, std::memory_order_relaxed);
+  }
+  return cus;
 }
 
 template <int DT>
 hipError_t quantize_dt(int format, const void* x, int64_t m, int64_t k, int64_t ldx, void* codes, void* scales,
                        void* ck, void* cks, hipStream_t s) {
-  const dim3 g(stream_grid(m * ((k + 511) / 512)));
+  const dim3 g(stream_grid((m + 3) / 4 * mx4_groups(k)));
   if (format == LQ_INT8)
     hipLaunchKernelGGL((k_mx4_quantize<DT, LQ_INT8>), g, dim3(256), 0, s, x, m, k, ldx, (uint8_t*)codes,
                        (uint8_t*)scales, (uint8_t*)ck, (uint8_t*)cks);
@@ -80,15 +381,48 @@ hipError_t quantize_dt(int format, const void* x, int64_t m, int64_t k, int64_t 
   return hipGetLastError();
 }
 
+// One workgroup a compute unit for the 256 x 256 tile (its LDS), more for the
+// smaller ones.
+template <int OUT, int FM, int FN>
+hipError_t product_tiled(const void* a, const void* as, const void* w, const void* ws, int64_t m, int64_t n, int64_t k,
+                         void* y, int64_t ldy, hipStream_t s) {
+  const int64_t tm = (m + 64 * FM - 1) / (64 * FM), tn = (n + 64 * FN - 1) / (64 * FN);
+  const int64_t most = (int64_t)compute_units() * (int)(163840 / sizeof(ProductLds<FM, FN>));
+  hipLaunchKernelGGL((k_mx4_product<OUT, FM, FN>), dim3((unsigned)(tm * tn < most ? tm * tn : most)), dim3(256), 0, s,
+                     (const uint8_t*)a, (const uint8_t*)as, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy,
+                     (uint32_t)tm, (uint32_t)tn);
+  return hipGetLastError();
+}
 template <int OUT>
 hipError_t product_dt(const void* a, const void* as, const void* w, const void* ws, int64_t m, int64_t n, int64_t k,
                       void* y, int64_t ldy, hipStream_t s) {
-  hipLaunchKernelGGL((k_mx4_product<OUT>), dim3((unsigned)((n + 63) / 64 * ((m + 63) / 64))), dim3(256), 0, s,
-                     (const uint8_t*)a, (const uint8_t*)as, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy);
-  return hipGetLastError();
+  if (k == 0) return launch_constant(m, n, OUT, nullptr, y, ldy, s);
+  const int64_t t4 = (m + 255) / 256 * ((n + 255) / 256), t2 = (m + 127) / 128 * ((n + 127) / 128);
+  if (t4 >= 200) return product_tiled<OUT, 4, 4>(a, as, w, ws, m, n, k, y, ldy, s);
+  if (t2 >= 128) return product_tiled<OUT, 2, 2>(a, as, w, ws, m, n, k, y, ldy, s);
+  return product_tiled<OUT, 1, 1>(a, as, w, ws, m, n, k, y, ldy, s);
+}
+
+// y = in, or zeros: what is left of a product over an empty contraction.
+template <typename T>
+__global__ __launch_bounds__(256) void k_constant(int64_t rows, int64_t cols, const T* in, T* y, int64_t ldy) {
+  const int64_t across = (cols + 255) / 256;
+  for (int64_t u = blockIdx.x; u < rows * across; u += gridDim.x) {
+    const int64_t row = u / across, col = u % across * 256 + threadIdx.x;
+    if (col < cols) y[row * ldy + col] = in ? in[row * ldy + col] : (T)0;
+  }
 }
 
 }  // namespace
+
+hipError_t launch_constant(int64_t rows, int64_t cols, int dtype, const void* in, void* y, int64_t ldy, hipStream_t s) {
+  const dim3 g(stream_grid(rows * ((cols + 255) / 256)));
+  if (dtype == LQ_F32)
+    hipLaunchKernelGGL((k_constant<float>), g, dim3(256), 0, s, rows, cols, (const float*)in, (float*)y, ldy);
+  else
+    hipLaunchKernelGGL((k_constant<uint16_t>), g, dim3(256), 0, s, rows, cols, (const uint16_t*)in, (uint16_t*)y, ldy);
+  return hipGetLastError();
+}
 
 hipError_t launch_mx4_quantize(int in_dtype, int ckpt_format, const void* x, int64_t m, int64_t k, int64_t ldx,
                                void* codes, void* scales, void* ck, void* cks, hipStream_t s) {

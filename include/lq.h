@@ -302,11 +302,12 @@ LQ_API int lq_call_kernels(const lq_desc* desc, int64_t rows, int64_t cols, uint
  *
  * Layouts (all row-major; ld_*: elements between the starts of two rows of a
  * caller's matrix, at least its row length, no alignment asked for):
- *   MX4 operand [rows, cols] (x or W): codes, two per byte as above, rows of
- *           128 * ceil(cols / 256) bytes; scales, rows of 16 * ceil(cols / 512)
- *           bytes. Elements and blocks past cols hold zeros. With cols a
- *           multiple of 512 these are lq_quantize's bytes for E2M1, PER_BLOCK
- *           32, UE8M0.
+ *   MX4 operand [rows, cols] (x or W): codes, two per byte as above, in groups
+ *           of 128 columns, [ceil(cols / 128)][rows][64 bytes]; scales,
+ *           [ceil(cols / 128)][rows up to a multiple of 4][4 bytes]. Elements
+ *           past cols are zeros. The codes and scales are lq_quantize's for
+ *           E2M1, PER_BLOCK 32, UE8M0, in the order in which the matrix cores
+ *           take them.
  *   checkpoint [rows, cols]: codes, one byte each, rows of 32 * ceil(cols / 32);
  *           scales, rows of ceil(cols / 32). With cols a multiple of 32 these
  *           are lq_quantize's bytes for INT8 or E4M3, PER_BLOCK 32, UE8M0, and

@@ -150,8 +150,8 @@ def test_swiglu_nothing_to_write():
 
 def test_sizes():
     lib = lq.load()
-    assert lib.lq_mx4_codes_bytes(3, 512) == 3 * 256 and lib.lq_mx4_scales_bytes(3, 512) == 3 * 16
-    assert lib.lq_mx4_codes_bytes(3, 257) == 3 * 256 and lib.lq_mx4_scales_bytes(3, 513) == 3 * 32
+    assert lib.lq_mx4_codes_bytes(3, 512) == 3 * 256 and lib.lq_mx4_scales_bytes(3, 512) == 4 * 16
+    assert lib.lq_mx4_codes_bytes(3, 129) == 3 * 128 and lib.lq_mx4_scales_bytes(5, 129) == 8 * 8
     assert lib.lq_ckpt8_codes_bytes(2, 33) == 128 and lib.lq_ckpt8_scales_bytes(2, 33) == 4
     assert lib.lq_mx4_codes_bytes(-1, 5) == 0 and lib.lq_ckpt8_codes_bytes(5, 1 << 31) == 0
     assert lib.lq_mx4_codes_bytes(0, 5) == 0 and lib.lq_ckpt8_scales_bytes(7, 0) == 0
