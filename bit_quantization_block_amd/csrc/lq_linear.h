@@ -189,6 +189,13 @@ inline unsigned stream_grid(int64_t units) {
   return (unsigned)(wgs < (1 << 20) ? wgs : (1 << 20));
 }
 
+// dy's rows are read 16 bytes at a time with 32-bit offsets within a tile: where
+// its columns or row stride are no multiple of 8, or the stride is very long, it
+// is first copied into the workspace, with rows padded by zeros (4 mn bytes
+// moved, against the product's 2 mnk operations).
+inline bool needs_padding(int64_t n, int64_t lddy) { return n % 8 != 0 || lddy % 8 != 0 || lddy > 1 << 21; }
+inline int64_t padded_columns(int64_t n) { return (n + 63) / 64 * 64; }
+
 // ------------------------------------------------------------ launchers
 // (lq_mx4.hip, lq_grad.hip, lq_swiglu.hip; arguments checked by lq_linear.hip)
 hipError_t launch_mx4_quantize(int in_dtype, int ckpt_format, const void* x, int64_t m, int64_t k, int64_t ldx,
@@ -197,9 +204,10 @@ hipError_t launch_constant(int64_t rows, int64_t cols, int dtype, const void* in
 hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
                               int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s);
 hipError_t launch_mx4_dgrad(const void* dy, int64_t m, int64_t n, int64_t lddy, const void* w_codes,
-                            const void* w_scales, int64_t k, int out_dtype, void* dx, int64_t lddx, hipStream_t s);
+                            const void* w_scales, int64_t k, int out_dtype, void* dx, int64_t lddx, void* ws,
+                            hipStream_t s);
 hipError_t launch_ckpt8_wgrad(int format, const void* dy, int64_t m, int64_t n, int64_t lddy, const void* x_codes,
-                              const void* x_scales, int64_t k, const float* dw_in, float* dw, int64_t lddw,
+                              const void* x_scales, int64_t k, const float* dw_in, float* dw, int64_t lddw, void* ws,
                               hipStream_t s);
 hipError_t launch_swiglu(int dtype, int format, const void* gate, const void* up, int64_t rows, int64_t cols,
                          int64_t ld, void* h, int64_t ldh, void* gc, void* gs, void* uc, void* us, hipStream_t s);

@@ -19,6 +19,8 @@ bool is_dtype(int d) { return d == LQ_F32 || d == LQ_BF16 || d == LQ_F16; }
 bool is_ckpt_format(int f) { return f == LQ_INT8 || f == LQ_E4M3; }
 // One side of a matrix; products of two sides and a stride stay within 64 bits.
 bool is_side(int64_t v) { return v >= 0 && v <= 0x7FFFFFFF; }
+// A row of W: its bytes times the 256 rows of a tile stay within 32 bits.
+bool is_width(int64_t v) { return v >= 0 && v <= 1 << 21; }
 bool is_stride(int64_t ld, int64_t cols) { return ld >= cols && ld <= (int64_t)1 << 31; }
 
 int status_of(hipError_t e) { return e == hipSuccess ? LQ_OK : LQ_ERR_HIP; }
@@ -28,7 +30,7 @@ int check_linear(const lq_linear_desc* d) {
   if (!is_dtype(d->in_dtype) || !is_dtype(d->out_dtype) || d->reserved != 0) return LQ_ERR_BAD_DESC;
   if (d->ckpt_format < LQ_INT8 || d->ckpt_format > LQ_E3M2) return LQ_ERR_BAD_DESC;
   if (!is_ckpt_format(d->ckpt_format)) return LQ_ERR_UNSUPPORTED;
-  if (!is_side(d->m) || !is_side(d->n) || !is_side(d->k)) return LQ_ERR_SHAPE;
+  if (!is_side(d->m) || !is_width(d->n) || !is_width(d->k)) return LQ_ERR_SHAPE;
   return LQ_OK;
 }
 
@@ -59,7 +61,10 @@ size_t lq_ckpt8_scales_bytes(int64_t rows, int64_t cols) {
 
 size_t lq_linear_workspace_bytes(const lq_linear_desc* d) {
   if (check_linear(d)) return 0;
-  const size_t b = operand_bytes(d);
+  // the forward call's operand, or a gradient call's padded dy
+  size_t b = operand_bytes(d);
+  const size_t dy = needs_padding(d->n, d->ld_in) ? (size_t)(d->m * padded_columns(d->n)) * 2 : 0;
+  b = b > dy ? b : dy;
   return b ? b : 256;
 }
 
@@ -123,7 +128,7 @@ int lq_mx4_dgrad(const lq_linear_desc* d, const void* dy, const void* w_codes, c
   if (!all_aligned(dy, w_codes, w_scales, (const void*)dx, (const void*)ws)) return LQ_ERR_ALIGN;
   if (!ws || ws_bytes < lq_linear_workspace_bytes(d)) return LQ_ERR_WORKSPACE;
   return status_of(launch_mx4_dgrad(dy, d->m, d->n, d->ld_in, w_codes, w_scales, d->k, d->out_dtype, dx, d->ld_out,
-                                    (hipStream_t)stream));
+                                    ws, (hipStream_t)stream));
 }
 
 int lq_ckpt8_wgrad(const lq_linear_desc* d, const void* dy, const void* ckpt_codes, const void* ckpt_scales,
@@ -137,7 +142,7 @@ int lq_ckpt8_wgrad(const lq_linear_desc* d, const void* dy, const void* ckpt_cod
   if (!all_aligned(dy, ckpt_codes, ckpt_scales, dw_in, (const void*)dw, (const void*)ws)) return LQ_ERR_ALIGN;
   if (!ws || ws_bytes < lq_linear_workspace_bytes(d)) return LQ_ERR_WORKSPACE;
   return status_of(launch_ckpt8_wgrad(d->ckpt_format, dy, d->m, d->n, d->ld_in, ckpt_codes, ckpt_scales, d->k,
-                                      (const float*)dw_in, (float*)dw, d->ld_out, (hipStream_t)stream));
+                                      (const float*)dw_in, (float*)dw, d->ld_out, ws, (hipStream_t)stream));
 }
 
 static int check_swiglu(const lq_swiglu_desc* d) {

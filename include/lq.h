@@ -313,7 +313,7 @@ LQ_API int lq_call_kernels(const lq_desc* desc, int64_t rows, int64_t cols, uint
  *           are lq_quantize's bytes for INT8 or E4M3, PER_BLOCK 32, UE8M0, and
  *           lq_dequantize reads them.
  *
- * Sides are 0 .. 2^31-1. Empty sides are no error: an empty contraction gives
+ * Sides are 0 .. 2^31-1, n and k of a layer at most 2^21. Empty sides are no error: an empty contraction gives
  * zeros (or dw_in). Pointers, ownership, streams and errors as above; buffers
  * of one call must not overlap, except that dw may be dw_in. Every call but the
  * quantisers and the activation needs a workspace of
