@@ -1,5 +1,9 @@
 // lq_grad.hip — the linear layer's gradients: dx = dy W from the 4-bit weights,
 // dw = dw0 + dy^T x8 from the 8-bit checkpoint of x.
+#include <stddef.h>
+
+#include <type_traits>
+
 #include "lq_linear.h"
 
 namespace lql {
@@ -24,20 +28,26 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 // contraction values that a lane of v_mfma_f32_32x32x16_bf16 takes.
 //
 // A workgroup of 2 x 2 waves makes a (64 FM) x (64 FN) tile, 64 of the
-// contraction a step. LDS holds two steps; the step after the next is on its way
-// in registers. Each step's loads, conversions, LDS writes and reads go between
+// contraction a step. LDS holds two steps; the next two are on their way in
+// registers (with one, a step waited for its loads: 1.5 us against the 0.85 us of
+// its products on an idle chip). Each step's loads, conversions, LDS writes and reads go between
 // its products, a few instructions at a time, so that the matrix cores are
 // never without work; one barrier a step.
 enum Kind { kDgrad, kWgrad };
 constexpr int kStep = 64;
 
+// Place of a row's 16-byte unit in a column operand. A transposing read takes
+// four rows, 64 bytes of each: they lie in the four 64-byte quarters of the
+// banks. A store has one unit of each of 16 rows: all 16 lie apart.
+__device__ __forceinline__ int column_unit(int row, int unit) { return unit ^ ((row & 3) << 2 | (row >> 2 & 3)); }
+
 template <int KIND, int FM, int FN>
 struct GradLds {
   // dgrad's dy: 128 bytes a row, its 16-byte units in the order u ^ (row / 2 & 7) (16 lanes at a time read 16
   // different units of 256 bytes)
-  static constexpr int kRowA = KIND == kDgrad ? 2 * kStep : 128 * FM + 64, kRowsA = KIND == kDgrad ? 64 * FM : kStep;
-  // columns: four rows that a transposing read takes at a time start 64 bytes apart in the banks
-  static constexpr int kRowB = 128 * FN + 64;
+  static constexpr int kRowA = KIND == kDgrad ? 2 * kStep : 128 * FM, kRowsA = KIND == kDgrad ? 64 * FM : kStep;
+  // columns: 16-byte units in the order of column_unit()
+  static constexpr int kRowB = 128 * FN;
   __attribute__((aligned(128))) uint8_t a[2][kRowsA * kRowA];
   __attribute__((aligned(128))) uint8_t b[2][kStep * kRowB];
 };
@@ -49,45 +59,36 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t stretch(const void* p, int64_t
   void* q = (void*)(uintptr_t)((uint64_t)hi << 32 | lo);
   return __builtin_amdgcn_make_buffer_rsrc(q, 0, __builtin_amdgcn_readfirstlane((uint32_t)(bytes > 0 ? bytes : 0)), 0x00020000);
 }
-__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t s, uint32_t offset) {
-  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(s, (int)offset, 0, 0));
+__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t s, uint32_t offset, uint32_t further = 0) {
+  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(s, (int)offset, (int)further, 0));
 }
-__device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t s, uint32_t offset) {
-  return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(s, (int)offset, 0, 0);
+__device__ __forceinline__ uint8_t load1(__amdgpu_buffer_rsrc_t s, uint32_t offset, uint32_t further = 0) {
+  return __builtin_amdgcn_raw_buffer_load_b8(s, (int)offset, (int)further, 0);
 }
-__device__ __forceinline__ v4s read_columns(const uint8_t* p) {
+// LDS by address. The few registers that a thread's places come from are made
+// opaque, and all else is an instruction's constant offset (at most 65535):
+// left alone, the compiler keeps every place in a register of its own, 60 of
+// them, and spills.
+typedef uint32_t place_t;
+__device__ __forceinline__ place_t place(place_t p) {
+  asm volatile("" : "+v"(p));
+  return p;
+}
+__device__ __forceinline__ v4i get16(place_t p) { return *(const __attribute__((address_space(3))) v4i*)p; }
+__device__ __forceinline__ void put16(place_t p, v4i v) { *(__attribute__((address_space(3))) v4i*)p = v; }
+__device__ __forceinline__ v4s read_columns(place_t p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
 }
 
-// Eight E2M1 codes times their scale as bfloat16.
-__device__ __forceinline__ v4i widen_e2m1(uint32_t w, float s) {
-  v4i o;
-  o[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-  o[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-  o[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-  o[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
-  return o;
-}
-// Four 8-bit codes times their scale. INT8: code + 128 is an unsigned byte, so
-// one conversion and one fused multiply-add give the exact binary32 value,
-// whose upper half is the bfloat16.
-template <int F>
-__device__ __forceinline__ uint2 widen_8(uint32_t w, float s) {
-  uint2 o;
-  if constexpr (F == LQ_INT8) {
-    const uint32_t u = w ^ 0x80808080u;
-    const float off = -128.0f * s;
-    const uint32_t a = __float_as_uint(__builtin_fmaf((float)(u & 0xFFu), s, off));
-    const uint32_t b = __float_as_uint(__builtin_fmaf((float)(u >> 8 & 0xFFu), s, off));
-    const uint32_t c = __float_as_uint(__builtin_fmaf((float)(u >> 16 & 0xFFu), s, off));
-    const uint32_t d = __float_as_uint(__builtin_fmaf((float)(u >> 24), s, off));
-    o.x = __builtin_amdgcn_perm(b, a, 0x07060302u);
-    o.y = __builtin_amdgcn_perm(d, c, 0x07060302u);
-  } else {
-    o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, s, false));
-    o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, s, true));
-  }
-  return o;
+// Two INT8 codes (the low bytes) times their scale as bfloat16: code + 128 is an
+// unsigned byte, so one conversion and one fused multiply-add give the exact
+// binary32 value, whose upper half is the bfloat16.
+__device__ __forceinline__ int widen_int8(uint32_t w, float s) {
+  const uint32_t u = w ^ 0x8080u;
+  const float off = -128.0f * s;
+  const uint32_t a = __float_as_uint(__builtin_fmaf((float)(u & 0xFFu), s, off));
+  const uint32_t b = __float_as_uint(__builtin_fmaf((float)(u >> 8 & 0xFFu), s, off));
+  return (int)__builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
 struct GradArgs {
@@ -99,6 +100,7 @@ struct GradArgs {
   void* out;
   int64_t ldo;
   uint32_t tm, tn;
+  int parts, part;         // of the contraction: steps of each; with parts > 1, out is `parts` planes
 };
 
 // F: the checkpoint's format (wgrad); OUT: the result's type.
@@ -112,123 +114,172 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
   const int r = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
 
   // The XCD's share of the tiles is a contiguous run in bands of 4 rows of tiles (as in the 4-bit product).
-  const uint32_t total = g.tm * g.tn, xcd = blockIdx.x % 8, per8 = total / 8, more = total % 8;
-  const uint32_t t0 = xcd * per8 + (xcd < more ? xcd : more) + blockIdx.x / 8;
+  const uint32_t tiles = g.tm * g.tn, total = tiles * g.parts, xcd = blockIdx.x % 8, per8 = total / 8, more = total % 8;
+  const uint32_t mine8 = xcd * per8 + (xcd < more ? xcd : more) + blockIdx.x / 8;
+  const uint32_t part = __builtin_amdgcn_readfirstlane(mine8 / tiles), t0 = mine8 - part * tiles;
   const uint32_t band = t0 / (4 * g.tn), first = band * 4, high = g.tm - first < 4 ? g.tm - first : 4, in = t0 - band * 4 * g.tn;
   const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane(first + in % high) * BM;
   const int64_t col0 = (int64_t)__builtin_amdgcn_readfirstlane(in / high) * BN;
 
   const int64_t rows = KIND == kDgrad ? g.m : g.n, depth = KIND == kDgrad ? g.n : g.m;   // of A
-  const int steps = (int)((depth + kStep - 1) / kStep);
+  const int all = (int)((depth + kStep - 1) / kStep), begin = (int)part * g.part;
+  const int steps = begin + g.part < all ? begin + g.part : all;
 
   // ---- A: 16 bytes a load, 2 FM loads a step
   constexpr int kLoadsA = 2 * FM;
-  uint32_t ao[kLoadsA], aw[kLoadsA];   // place in memory from the step's corner on, place in LDS
+  const place_t lds0 = (place_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds;
+  const place_t ldsb = lds0 + (place_t)offsetof(Lds, b);
+  uint32_t ao;               // place in memory of the first load, from the step's corner on; load i is `astep` i further
+  constexpr int kPlacesA = KIND == kDgrad ? 2 : kLoadsA;   // (the order of the units repeats every other load, or not at all)
+  place_t aw[kPlacesA];      // in LDS, of the first loads
+  constexpr int awide = KIND == kDgrad ? 8 * Lds::kRowA : 8 / FM * Lds::kRowA;   // LDS bytes of a load's rows
+  const uint32_t astep = (uint32_t)((KIND == kDgrad ? 8 : 8 / FM) * g.lddy * 2);
+  {
+    constexpr int across = KIND == kDgrad ? 8 : 8 * FM;   // lanes of a row
+    const int row = wave * kLoadsA * (64 / across) + lane / across, u = lane % across;
+    ao = (uint32_t)(row * g.lddy * 2) + u * 16;
 #pragma unroll
-  for (int i = 0; i < kLoadsA; i++) {
-    if (KIND == kDgrad) {
-      const uint32_t row = (wave * kLoadsA + i) * 8 + (lane >> 3), u = lane & 7;
-      ao[i] = (uint32_t)(row * g.lddy * 2) + u * 16;
-      aw[i] = row * Lds::kRowA + (u ^ (row >> 1 & 7)) * 16;
-    } else {
-      constexpr int across = 8 * FM;   // lanes of a row
-      const uint32_t row = (wave * kLoadsA + i) * (64 / across) + lane / across, u = lane % across;
-      ao[i] = (uint32_t)(row * g.lddy * 2) + u * 16;
-      aw[i] = row * Lds::kRowA + u * 16;
+    for (int i = 0; i < kPlacesA; i++) {
+      const int rr = row + i * (64 / across);
+      aw[i] = place(lds0 + row * Lds::kRowA + i * awide + (KIND == kDgrad ? u ^ (rr >> 1 & 7) : column_unit(rr, u)) * 16);
     }
   }
-  v4i ra[kLoadsA];
+  v4i ra[2][kLoadsA];   // of the even and the odd steps
   const int64_t left = rows - row0 < BM ? rows - row0 : BM;   // of A's rows (dgrad) or columns (wgrad)
-  // dgrad: units past the row's end are sent past the stretch's end, as rows past m are.
-  auto corner_a = [&](int t) {
-    const int64_t at = (int64_t)t * kStep;
-    if (KIND == kDgrad) return stretch(g.dy + row0 * g.lddy + at, at < depth ? ((left - 1) * g.lddy + g.row - at) * 2 : 0);
-    const int64_t deep = depth - at < kStep ? depth - at : kStep;
-    return stretch(g.dy + at * g.lddy + row0, deep > 0 ? ((deep - 1) * g.lddy + g.row - row0) * 2 : 0);
+
+  // ---- where the next loads begin. What a stretch's end cuts off reads as zero: rows past the tile's last, the
+  // contraction past its end (`rest` values of it are left; from the part's last step on, none).
+  constexpr int kPieces = KIND == kDgrad ? FN / 2 : 1;   // groups of W, or the checkpoint
+  struct Cursor {
+    const uint8_t *a, *c[kPieces], *s[kPieces];
+    int64_t rest;
+    int steps;   // left of this part
+    __amdgpu_buffer_rsrc_t ra, rc[kPieces], rs[kPieces];
+  } at;
+  const int64_t pitch = ckpt_pitch(g.k), spitch = ckpt_scale_pitch(g.k);
+  at.rest = depth - (int64_t)begin * kStep;
+  at.steps = steps - begin;
+  at.a = (const uint8_t*)(KIND == kDgrad ? g.dy + row0 * g.lddy + (int64_t)begin * kStep : g.dy + (int64_t)begin * kStep * g.lddy + row0);
+#pragma unroll
+  for (int i = 0; i < kPieces; i++) {
+    if (KIND == kDgrad) {
+      const int64_t group = col0 / 128 + i;
+      at.c[i] = g.b + (group * g.n + (int64_t)begin * kStep) * 64;
+      at.s[i] = g.bs + (group * mx4_scale_rows(g.n) + (int64_t)begin * kStep) * 4;
+    } else {
+      at.c[i] = g.b + (int64_t)begin * kStep * pitch + col0;
+      at.s[i] = g.bs + (int64_t)begin * kStep * spitch + col0 / 32;
+    }
+  }
+  const int64_t groups = mx4_groups(g.k);
+  auto point_a = [&] {
+    const int64_t deep = at.rest < kStep ? at.rest : kStep;
+    const int64_t bytes = KIND == kDgrad ? ((left - 1) * g.lddy + g.row - (depth - at.rest)) * 2 : ((deep - 1) * g.lddy + g.row - row0) * 2;
+    at.ra = stretch(at.a, at.steps > 0 ? bytes : 0);
+    at.a += KIND == kDgrad ? kStep * 2 : kStep * 2 * g.lddy;
   };
-  auto load_a = [&](__amdgpu_buffer_rsrc_t s, int t, int i) {
-    uint32_t o = ao[i];
-    if (KIND == kDgrad) o = (int64_t)t * kStep + (lane & 7) * 8 < g.row ? o : 0xFFFFFFF0u;
-    ra[i] = load16(s, o);
+  auto point_b = [&](int i) {
+    const int64_t deep = at.rest < kStep ? at.rest : kStep;
+    const bool real = at.steps > 0 && (KIND == kWgrad || col0 / 128 + i < groups);
+    at.rc[i] = stretch(at.c[i], real ? (KIND == kDgrad ? deep * 64 : deep * pitch - col0) : 0);
+    at.rs[i] = stretch(at.s[i], real ? (KIND == kDgrad ? deep * 4 : deep * spitch - col0 / 32) : 0);
+    at.c[i] += KIND == kDgrad ? kStep * 64 : kStep * pitch;
+    at.s[i] += KIND == kDgrad ? kStep * 4 : kStep * spitch;
   };
+  auto point_on = [&] {
+    at.rest -= kStep;
+    at.steps--;
+  };
+  // (dgrad: units past the row's end are sent past the stretch's end)
+  auto load_a = [&](int t, int set, int i) {
+    uint32_t o = ao;
+    if (KIND == kDgrad) o = t * kStep + (lane & 7) * 8 < (int)g.row ? o : 0xFFFFFFF0u;
+    ra[set][i] = load16(at.ra, o, i * astep);
+  };
+  auto put_a = [&](int st, int set, int i) { put16(aw[i % kPlacesA] + st * (place_t)sizeof(lds.a[0]) + i / kPlacesA * kPlacesA * awide, ra[set][i]); };
 
   // ---- B: dgrad: 32 codes of a row of W (one block); wgrad: 16 codes of a row of x8 (half a block)
   constexpr int kLoadsB = KIND == kDgrad ? FN / 2 : FN;
-  v4i rb[kLoadsB];
-  uint32_t rs[kLoadsB];
-  struct CornerB { __amdgpu_buffer_rsrc_t c[KIND == kDgrad ? FN / 2 : 1], s[KIND == kDgrad ? FN / 2 : 1]; };
-  auto corner_b = [&](int t) {
-    CornerB c;
-    const int64_t at = (int64_t)t * kStep;
-    if (KIND == kDgrad) {
+  v4i rb[2][kLoadsB];
+  uint8_t rs[2][kLoadsB];
+  // (dgrad: a wave takes one block of each of the 64 rows, load i in group i; wgrad: half a block of rows 4 or 8 a wave)
+  constexpr int kUnitsB = KIND == kDgrad ? 4 * kLoadsB : 2 * kLoadsB, kEach = kUnitsB / kLoadsB;   // 8 codes each
+  const int brow = KIND == kDgrad ? lane : tid / (4 * FN), bcol = KIND == kDgrad ? wave : tid % (4 * FN);
+  constexpr int bwide = KIND == kDgrad ? 256 : 256 / (4 * FN) * Lds::kRowB;                       // LDS bytes from load to load
+  const uint32_t bo = (uint32_t)(brow * (KIND == kDgrad ? 64 : pitch)) + bcol * 16, bstep = KIND == kDgrad ? 0 : (uint32_t)(256 / (4 * FN) * pitch);
+  const uint32_t bso = (uint32_t)(brow * (KIND == kDgrad ? 4 : spitch)) + (KIND == kDgrad ? bcol : bcol / 2);
+  const uint32_t bsstep = KIND == kDgrad ? 0 : (uint32_t)(256 / (4 * FN) * spitch);
+  place_t bw[kEach];
 #pragma unroll
-      for (int i = 0; i < FN / 2; i++) {
-        const int64_t group = col0 / 128 + i;
-        const bool real = group < mx4_groups(g.k) && at < depth;
-        c.c[i] = stretch(g.b + (group * g.n + at) * 64, real ? (depth - at < kStep ? depth - at : kStep) * 64 : 0);
-        c.s[i] = stretch(g.bs + (group * mx4_scale_rows(g.n) + at) * 4, real ? (depth - at < kStep ? depth - at : kStep) * 4 : 0);
-      }
-    } else {
-      const int64_t deep = depth - at < kStep ? depth - at : kStep, p = ckpt_pitch(g.k), sp = ckpt_scale_pitch(g.k);
-      c.c[0] = stretch(g.b + at * p + col0, deep > 0 ? (deep - 1) * p + p - col0 : 0);
-      c.s[0] = stretch(g.bs + at * sp + col0 / 32, deep > 0 ? (deep - 1) * sp + sp - col0 / 32 : 0);
-    }
-    return c;
-  };
-  uint32_t bo[kLoadsB], bso[kLoadsB], bw[kLoadsB];
-#pragma unroll
-  for (int i = 0; i < kLoadsB; i++) {
-    if (KIND == kDgrad) {
-      const uint32_t row = tid >> 2, q = tid & 3;
-      bo[i] = row * 64 + q * 16;
-      bso[i] = row * 4 + q;
-      bw[i] = row * Lds::kRowB + i * 256 + q * 64;
-    } else {
-      const uint32_t row = (i * 256 + tid) / (4 * FN), c = (i * 256 + tid) % (4 * FN);
-      bo[i] = (uint32_t)(row * ckpt_pitch(g.k)) + c * 16;
-      bso[i] = (uint32_t)(row * ckpt_scale_pitch(g.k)) + c / 2;
-      bw[i] = row * Lds::kRowB + c * 32;
-    }
-  }
-  auto load_b = [&](const CornerB& c, int i) {
+  for (int u = 0; u < kEach; u++) bw[u] = place(ldsb + brow * Lds::kRowB + column_unit(brow, bcol * kEach + u) * 16);
+  auto load_b = [&](int set, int i) {
     const int j = KIND == kDgrad ? i : 0;
-    rb[i] = load16(c.c[j], bo[i]);
-    rs[i] = load1(c.s[j], bso[i]);
+    rb[set][i] = load16(at.rc[j], bo, i * bstep);
+    rs[set][i] = load1(at.rs[j], bso, i * bsstep);
   };
-  // One quarter of load i: 8 codes of W (16 bytes) or 4 of x8 (8 bytes).
-  auto put_b = [&](int st, int i, int part) {
-    const float s = scale_value(rs[i]);
+  // Unit i of the step's W or x8: 8 codes, converted in kBits bits and stored with the last.
+  constexpr int kBits = KIND == kWgrad && F == LQ_INT8 ? 4 : 2;
+  static_assert(kUnitsB == kLoadsA, "a thread has as many units of either operand");
+  float scale[kLoadsB];
+  v4i made;
+  auto put_b = [&](int st, int set, int i, int bit) {
+    const int l = i / kEach, u = i % kEach;
+    const float s = scale[l];
     if (KIND == kDgrad) {
-      // lanes of one 16-lane turn write different 16 bytes of their 64, so that they meet different banks
-      const int turn = (part + (tid >> 2)) & 3;
-      const uint32_t lo = turn & 1 ? rb[i][1] : rb[i][0], hi = turn & 1 ? rb[i][3] : rb[i][2];
-      *(v4i*)&lds.b[st][bw[i] + turn * 16] = widen_e2m1(turn & 2 ? hi : lo, s);
+      const uint32_t w = rb[set][l][u];
+      if (bit == 0) {
+        made[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+        made[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+      } else {
+        made[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+        made[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+      }
+    } else if (F == LQ_INT8) {
+      made[bit] = widen_int8(rb[set][l][2 * u + bit / 2] >> (bit & 1) * 16, s);
     } else {
-      *(uint2*)&lds.b[st][bw[i] + part * 8] = widen_8<F>(rb[i][part], s);
+      const int w = rb[set][l][2 * u + bit];
+      made[2 * bit] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
+      made[2 * bit + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true));
     }
+    if (bit == kBits - 1) put16(bw[u] + st * (place_t)sizeof(lds.b[0]) + l * bwide, made);
   };
 
   // ---- operands of 16 of the contraction
   struct Operands { v4i a[FM], b[FN]; };
   Operands P, Q;
-  const uint32_t ra0 = KIND == kDgrad ? 0 : (8 * h + ((lane & 15) >> 2)) * Lds::kRowA + (wm * 32 * FM + (lane >> 4 & 1) * 16 + (lane & 3) * 4) * 2;
-  const uint32_t rb0 = (8 * h + ((lane & 15) >> 2)) * Lds::kRowB + (wn * 32 * FN + (lane >> 4 & 1) * 16 + (lane & 3) * 4) * 2;
-  auto columns = [&](const uint8_t* p, int row) {
-    const v4s x = read_columns(p), y = read_columns(p + 4 * row);
+  // Place of the lane's piece of four rows of 32 columns from `col` on, rows 8h .. + 3 or, four further, 8h + 4 .. + 7.
+  const int crow = 8 * h + ((lane & 15) >> 2);
+  auto piece = [&](int row_bytes, int col, int further) {
+    const int row = crow + further, c = col + (lane >> 4 & 1) * 16 + (lane & 3) * 4;
+    return row * row_bytes + column_unit(row, c >> 3) * 16 + (c & 7) * 2;
+  };
+  place_t pa[KIND == kDgrad ? 4 : 2 * FM], pb[2 * FN];
+#pragma unroll
+  for (int x = 0; x < 2; x++) {
+    if (KIND == kWgrad) {
+#pragma unroll
+      for (int f = 0; f < FM; f++) pa[2 * f + x] = place(lds0 + piece(Lds::kRowA, wm * 32 * FM + f * 32, 4 * x));
+    }
+#pragma unroll
+    for (int f = 0; f < FN; f++) pb[2 * f + x] = place(ldsb + piece(Lds::kRowB, wn * 32 * FN + f * 32, 4 * x));
+  }
+  if (KIND == kDgrad) {
+#pragma unroll
+    for (int q = 0; q < 4; q++) pa[q] = place(lds0 + (wm * 32 * FM + r) * Lds::kRowA + ((2 * q + h) ^ (r >> 1 & 7)) * 16);
+  }
+  auto columns = [&](place_t p, place_t q) {
+    const v4s x = read_columns(p), y = read_columns(q);
     typedef short v8s __attribute__((ext_vector_type(8)));
     const v8s v = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     return __builtin_bit_cast(v4i, v);
   };
   auto read = [&](int st, int q, Operands& o, int f) {
+    const place_t a = st * (place_t)sizeof(lds.a[0]), b = st * (place_t)sizeof(lds.b[0]) + q * 16 * Lds::kRowB;
     if (f < FM) {
-      if (KIND == kDgrad) {
-        const int row = wm * 32 * FM + f * 32 + r;
-        o.a[f] = *(const v4i*)&lds.a[st][row * Lds::kRowA + ((2 * q + h) ^ (r >> 1 & 7)) * 16];
-      } else {
-        o.a[f] = columns(&lds.a[st][ra0 + q * 16 * Lds::kRowA + f * 64], Lds::kRowA);
-      }
+      if (KIND == kDgrad) o.a[f] = get16(pa[q] + a + f * 32 * Lds::kRowA);
+      else o.a[f] = columns(pa[2 * f % (2 * FM)] + a + q * 16 * Lds::kRowA, pa[(2 * f + 1) % (2 * FM)] + a + q * 16 * Lds::kRowA);
     } else {
-      o.b[f - FM] = columns(&lds.b[st][rb0 + q * 16 * Lds::kRowB + (f - FM) * 64], Lds::kRowB);
+      o.b[f - FM] = columns(pb[2 * (f - FM)] + b, pb[2 * (f - FM) + 1] + b);
     }
   };
 
@@ -240,6 +291,9 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
 #pragma unroll
       for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
   constexpr int per = FM * FN;
+  // One quarter's products; `between` runs after each. 28 of a product's 32 cycles are free for other
+  // instructions: what goes between two products is kept to about six of them (in bursts of 16 the conversions
+  // alone cost a third of the step), and scheduling barriers keep it there.
   auto multiply = [&](const Operands& o, auto between) {
 #pragma unroll
     for (int i = 0; i < FM; i++)
@@ -251,69 +305,87 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
         __builtin_amdgcn_sched_barrier(0);
       }
   };
-  // The `reads` of the next operands go under the first half of a quarter's products.
-  auto spread = [&](int done, int from, int to, int count, auto what) {
+  // `count` pieces of work over `over` places between products
+  auto spread = [&](int done, int over, int count, auto what) {
 #pragma unroll
     for (int f = 0; f < count; f++)
-      if (from + f * (to - from) / count == done) what(f);
+      if (f * over / count == done) what(f);
   };
 
-  {
-    const auto ca = corner_a(0);
-    const auto cb = corner_b(0);
+  auto point = [&] {
+    point_a();
 #pragma unroll
-    for (int i = 0; i < kLoadsA; i++) load_a(ca, 0, i);
+    for (int i = 0; i < kPieces; i++) point_b(i);
+    point_on();
+  };
+  auto load = [&](int t, int set) {
+    point();
 #pragma unroll
-    for (int i = 0; i < kLoadsB; i++) load_b(cb, i);
-  }
+    for (int i = 0; i < kLoadsA; i++) load_a(t, set, i);
 #pragma unroll
-  for (int i = 0; i < kLoadsA; i++) *(v4i*)&lds.a[0][aw[i]] = ra[i];
+    for (int i = 0; i < kLoadsB; i++) load_b(set, i);
+  };
+  auto take_scales = [&](int set, int i) { scale[i] = scale_value(rs[set][i]); };
+  load(begin, 0);
+  load(begin + 1, 1);
 #pragma unroll
-  for (int i = 0; i < kLoadsB; i++)
+  for (int i = 0; i < kLoadsA; i++) put_a(0, 0, i);
 #pragma unroll
-    for (int q = 0; q < 4; q++) put_b(0, i, q);
-  {
-    const auto ca = corner_a(1);
-    const auto cb = corner_b(1);
+  for (int i = 0; i < kLoadsB; i++) take_scales(0, i);
 #pragma unroll
-    for (int i = 0; i < kLoadsA; i++) load_a(ca, 1, i);
+  for (int i = 0; i < kUnitsB * kBits; i++) put_b(0, 0, i / kBits, i % kBits);
+  load(begin + 2, 0);
+  point();
 #pragma unroll
-    for (int i = 0; i < kLoadsB; i++) load_b(cb, i);
-  }
+  for (int i = 0; i < kLoadsB; i++) take_scales(1, i);
   __syncthreads();
 #pragma unroll
   for (int f = 0; f < FM + FN; f++) read(0, 0, P, f);
 
-  for (int t = 0; t < steps; t++) {
-    const int st = t & 1, other = st ^ 1;
-    const auto ca = corner_a(t + 2);
-    const auto cb = corner_b(t + 2);
-    // first quarter: the next step's dy goes into LDS, the one after it is asked for
-    multiply(P, [&](int done) {
-      spread(done, 0, per / 2, FM + FN, [&](int f) { read(st, 1, Q, f); });
-      spread(done, per / 2, per, kLoadsA, [&](int i) {
-        *(v4i*)&lds.a[other][aw[i]] = ra[i];
-        load_a(ca, t + 2, i);
+  // Step t, in LDS stage ST: the next step's data, which came into registers two
+  // steps ago, goes into the other stage, and the step three on is asked for.
+  auto step = [&](auto stage, int t) {
+    constexpr int ST = decltype(stage)::value, OTHER = ST ^ 1;
+    // The units of either operand go over three quarters. Each quarter also reads the next one's operands, early
+    // enough for the last to arrive.
+    constexpr int window = (per * 3 + 3) / 4, bits = kUnitsB * kBits, bit_third = (bits + 2) / 3, third = (kLoadsA + 2) / 3;
+    auto work = [&](int quarter, int done) {
+      const int a0 = quarter * third, an = kLoadsA - a0 < third ? kLoadsA - a0 : third;
+      spread(done, per, an, [&](int f) {
+        put_a(OTHER, OTHER, a0 + f);
+        load_a(t + 3, OTHER, a0 + f);
       });
+      const int b0 = quarter * bit_third, bn = bits - b0 < bit_third ? bits - b0 : bit_third;
+      spread(done, per, bn, [&](int f) { put_b(OTHER, OTHER, (b0 + f) / kBits, (b0 + f) % kBits); });
+    };
+    multiply(P, [&](int done) {
+      spread(done, window, FM + FN, [&](int f) { read(ST, 1, Q, f); });
+      work(0, done);
     });
-    // second and third quarter: likewise W or x8, converted
     multiply(Q, [&](int done) {
-      spread(done, 0, per / 2, FM + FN, [&](int f) { read(st, 2, P, f); });
-      spread(done, per / 2, per, 2 * kLoadsB, [&](int f) { put_b(other, f / 4, f % 4); });
+      spread(done, window, FM + FN, [&](int f) { read(ST, 2, P, f); });
+      work(1, done);
     });
     multiply(P, [&](int done) {
-      spread(done, 0, per / 2, FM + FN, [&](int f) { read(st, 3, Q, f); });
-      spread(done, per / 2, per, 2 * kLoadsB, [&](int f) { put_b(other, (2 * kLoadsB + f) / 4, (2 * kLoadsB + f) % 4); });
-      if (done == per - 1) {
-#pragma unroll
-        for (int i = 0; i < kLoadsB; i++) load_b(cb, i);
-      }
+      spread(done, window, FM + FN, [&](int f) { read(ST, 3, Q, f); });
+      work(2, done);
     });
     // the next step is in LDS, and nobody reads this one any more
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     multiply(Q, [&](int done) {
-      spread(done, 0, per / 2, FM + FN, [&](int f) { read(other, 0, P, f); });
+      spread(done, window, FM + FN, [&](int f) { read(OTHER, 0, P, f); });
+      spread(done, per / 2, kLoadsB, [&](int i) { load_b(OTHER, i); });
+      spread(done, per / 2, kLoadsB, [&](int i) { take_scales(ST, i); });
+      if (done == per / 2) point_a();
+      if (done == per * 3 / 4) point_b(0);
+      if (kPieces > 1 && done == per - 2) point_b(kPieces - 1);
+      if (done == per - 1) point_on();
     });
+  };
+  // (of an odd number of steps, the last is followed by one of zeros)
+  for (int t = begin; t < steps; t += 2) {
+    step(std::integral_constant<int, 0>(), t);
+    step(std::integral_constant<int, 1>(), t + 1);
   }
 
   // A lane holds row r of a 32 x 32 block of the result, columns 8q + 4h .. + 3:
@@ -347,7 +419,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
       T v[V];
       __builtin_memcpy(v, __builtin_assume_aligned(mine + rr * kRow + cc * (int)sizeof(T), 16), 16);
       if (row < rows && col < g.k) {
-        T* o = (T*)g.out + row * g.ldo + col;
+        T* o = (T*)g.out + (part * rows + row) * g.ldo + col;
         if (g.k - col >= V) {
           if constexpr (KIND == kWgrad) {
             if (g.in) {
@@ -396,21 +468,37 @@ hipError_t grad_tiled(GradArgs& g, hipStream_t s) {
   const int64_t rows = KIND == kDgrad ? g.m : g.n;
   g.tm = (uint32_t)((rows + 64 * FM - 1) / (64 * FM));
   g.tn = (uint32_t)((g.k + 64 * FN - 1) / (64 * FN));
-  hipLaunchKernelGGL((k_grad<KIND, F, OUT, FM, FN>), dim3(g.tm * g.tn), dim3(256), 0, s, g);
+  hipLaunchKernelGGL((k_grad<KIND, F, OUT, FM, FN>), dim3(g.tm * g.tn * g.parts), dim3(256), 0, s, g);
   return hipGetLastError();
 }
 template <int KIND, int F, int OUT>
+hipError_t grad_tile(int tile, GradArgs& g, hipStream_t s) {
+  return tile == 4 ? grad_tiled<KIND, F, OUT, 4, 4>(g, s) : grad_tiled<KIND, F, OUT, 2, 2>(g, s);
+}
+template <int KIND, int F, int OUT>
 hipError_t grad(GradArgs g, void* ws, hipStream_t s) {
+  uint8_t* planes = (uint8_t*)ws;
   if (needs_padding(g.n, g.lddy)) {
     const int64_t ld = padded_columns(g.n);
     hipLaunchKernelGGL(k_pad_rows, dim3(stream_grid(g.m * ((ld + 511) / 512))), dim3(256), 0, s, g.dy, g.m, g.n, g.lddy, (uint16_t*)ws, ld);
     if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
     g.dy = (const uint16_t*)ws;
     g.lddy = g.row = ld;
+    planes += (g.m * ld * 2 + 255) / 256 * 256;
   }
   const int64_t rows = KIND == kDgrad ? g.m : g.n;
-  if ((rows + 255) / 256 * ((g.k + 255) / 256) >= 200) return grad_tiled<KIND, F, OUT, 4, 4>(g, s);
-  return grad_tiled<KIND, F, OUT, 2, 2>(g, s);
+  const Split c = split_grad(rows, g.k, KIND == kDgrad ? g.n : g.m);
+  g.parts = c.parts;
+  g.part = c.part;
+  if (c.parts == 1) return grad_tile<KIND, F, OUT>(c.tile, g, s);
+  void* const out = g.out;
+  const float* const in = g.in;
+  const int64_t ldo = g.ldo;
+  g.out = planes;
+  g.in = nullptr;
+  g.ldo = plane_stride(g.k);
+  const hipError_t e = grad_tile<KIND, F, LQ_F32>(c.tile, g, s);
+  return e != hipSuccess ? e : launch_join(rows, g.k, OUT, c.parts, (const float*)planes, in, out, ldo, s);
 }
 
 }  // namespace
@@ -419,7 +507,7 @@ hipError_t launch_mx4_dgrad(const void* dy, int64_t m, int64_t n, int64_t lddy, 
                             const void* w_scales, int64_t k, int out_dtype, void* dx, int64_t lddx, void* ws,
                             hipStream_t s) {
   if (n == 0) return launch_constant(m, k, out_dtype, nullptr, dx, lddx, s);
-  const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)w_codes, (const uint8_t*)w_scales, nullptr, dx, lddx, 0, 0};
+  const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)w_codes, (const uint8_t*)w_scales, nullptr, dx, lddx, 0, 0, 1, 0};
   switch (out_dtype) {
     case LQ_F32: return grad<kDgrad, LQ_E2M1, LQ_F32>(g, ws, s);
     case LQ_BF16: return grad<kDgrad, LQ_E2M1, LQ_BF16>(g, ws, s);
@@ -431,7 +519,7 @@ hipError_t launch_ckpt8_wgrad(int format, const void* dy, int64_t m, int64_t n, 
                               const void* x_scales, int64_t k, const float* dw_in, float* dw, int64_t lddw, void* ws,
                               hipStream_t s) {
   if (m == 0) return launch_constant(n, k, LQ_F32, dw_in, dw, lddw, s);
-  const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)x_codes, (const uint8_t*)x_scales, dw_in, dw, lddw, 0, 0};
+  const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)x_codes, (const uint8_t*)x_scales, dw_in, dw, lddw, 0, 0, 1, 0};
   if (format == LQ_INT8) return grad<kWgrad, LQ_INT8, LQ_F32>(g, ws, s);
   return grad<kWgrad, LQ_E4M3, LQ_F32>(g, ws, s);
 }

@@ -22,6 +22,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "lq.h"
 #include "lq_device.h"
 
@@ -196,13 +198,47 @@ inline unsigned stream_grid(int64_t units) {
 inline bool needs_padding(int64_t n, int64_t lddy) { return n % 8 != 0 || lddy % 8 != 0 || lddy > 1 << 21; }
 inline int64_t padded_columns(int64_t n) { return (n + 63) / 64 * 64; }
 
+// ------------------------------------------------------------ shapes of the products
+// Compute units of the current device (256 on MI355X, or with no device).
+inline int compute_units() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  int cus = cached[dev].load(std::memory_order_relaxed);
+  if (cus == 0) {
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) cus = 256;
+    cached[dev].store(cus, std::memory_order_relaxed);
+  }
+  return cus;
+}
+// How a product of rows x cols over `steps` steps of its contraction is shared
+// out: tiles of 64 tile x 64 tile, each of whose contraction is cut into
+// `parts` runs of `part` steps, whose sums are added up afterwards.
+struct Split { int tile, parts, part; };
+Split split_product(int64_t m, int64_t n, int64_t k);              // steps of 128
+Split split_grad(int64_t rows, int64_t cols, int64_t depth);       // steps of 64
+// Workspace of the parts' sums: planes with rows of a multiple of 4 values.
+__host__ __device__ inline int64_t plane_stride(int64_t cols) { return (cols + 3) / 4 * 4; }
+inline size_t planes_bytes(const Split& c, int64_t rows, int64_t cols) {
+  return c.parts > 1 ? (size_t)c.parts * (size_t)(rows * plane_stride(cols)) * 4 : 0;
+}
+
 // ------------------------------------------------------------ launchers
 // (lq_mx4.hip, lq_grad.hip, lq_swiglu.hip; arguments checked by lq_linear.hip)
 hipError_t launch_mx4_quantize(int in_dtype, int ckpt_format, const void* x, int64_t m, int64_t k, int64_t ldx,
                                void* codes, void* scales, void* ckpt_codes, void* ckpt_scales, hipStream_t s);
 hipError_t launch_constant(int64_t rows, int64_t cols, int dtype, const void* in, void* y, int64_t ldy, hipStream_t s);
+hipError_t launch_join(int64_t rows, int64_t cols, int dtype, int parts, const float* planes, const float* in, void* y,
+                       int64_t ldy, hipStream_t s);
 hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
-                              int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s);
+                              int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, void* planes,
+                              hipStream_t s);
+// The forward product of a few rows straight from x: at most kFewBlocks blocks
+// of it (padded to whole groups), which a workgroup quantises into its LDS.
+constexpr int64_t kFewRows = 16, kFewBlocks = 2048;
+inline bool few_rows(int64_t m, int64_t k) { return m <= kFewRows && m * mx4_groups(k) * 4 <= kFewBlocks; }
+hipError_t launch_mx4_few(int in_dtype, const void* x, int64_t ldx, const void* w_codes, const void* w_scales, int64_t m,
+                          int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s);
 hipError_t launch_mx4_dgrad(const void* dy, int64_t m, int64_t n, int64_t lddy, const void* w_codes,
                             const void* w_scales, int64_t k, int out_dtype, void* dx, int64_t lddx, void* ws,
                             hipStream_t s);

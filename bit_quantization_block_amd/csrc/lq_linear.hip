@@ -44,6 +44,19 @@ size_t operand_bytes(const lq_linear_desc* d) {
 
 }  // namespace
 
+namespace lql {
+
+Split split_product(int64_t m, int64_t n, int64_t k) {
+  const int64_t t4 = (m + 255) / 256 * ((n + 255) / 256), t2 = (m + 127) / 128 * ((n + 127) / 128);
+  return {t4 >= 200 ? 4 : t2 >= 128 ? 2 : 1, 1, (int)mx4_groups(k)};
+}
+Split split_grad(int64_t rows, int64_t cols, int64_t depth) {
+  const int64_t t4 = (rows + 255) / 256 * ((cols + 255) / 256);
+  return {t4 >= 200 ? 4 : 2, 1, (int)((depth + 63) / 64)};
+}
+
+}  // namespace lql
+
 extern "C" {
 
 size_t lq_mx4_codes_bytes(int64_t rows, int64_t cols) {
@@ -61,10 +74,12 @@ size_t lq_ckpt8_scales_bytes(int64_t rows, int64_t cols) {
 
 size_t lq_linear_workspace_bytes(const lq_linear_desc* d) {
   if (check_linear(d)) return 0;
-  // the forward call's operand, or a gradient call's padded dy
-  size_t b = operand_bytes(d);
-  const size_t dy = needs_padding(d->n, d->ld_in) ? (size_t)(d->m * padded_columns(d->n)) * 2 : 0;
-  b = b > dy ? b : dy;
+  // the most of: the forward call's operand and its parts' sums; a gradient
+  // call's padded dy and its parts' sums
+  const size_t forward = operand_bytes(d) + planes_bytes(split_product(d->m, d->n, d->k), d->m, d->n);
+  const size_t dy = needs_padding(d->n, d->ld_in) ? round256((size_t)(d->m * padded_columns(d->n)) * 2) : 0;
+  const size_t dx = planes_bytes(split_grad(d->m, d->k, d->n), d->m, d->k), dw = planes_bytes(split_grad(d->n, d->k, d->m), d->n, d->k);
+  const size_t backward = dy + (dx > dw ? dx : dw), b = forward > backward ? forward : backward;
   return b ? b : 256;
 }
 
@@ -91,7 +106,7 @@ int lq_mx4_product(const lq_linear_desc* d, const void* x_codes, const void* x_s
   if (!all_aligned(x_codes, x_scales, w_codes, w_scales, (const void*)y, (const void*)ws)) return LQ_ERR_ALIGN;
   if (!ws || ws_bytes < lq_linear_workspace_bytes(d)) return LQ_ERR_WORKSPACE;
   return status_of(launch_mx4_product(x_codes, x_scales, w_codes, w_scales, d->m, d->n, d->k, d->out_dtype, y,
-                                      d->ld_out, (hipStream_t)stream));
+                                      d->ld_out, ws, (hipStream_t)stream));
 }
 
 int lq_mx4_linear(const lq_linear_desc* d, const void* x, const void* w_codes, const void* w_scales, void* y,
@@ -106,6 +121,9 @@ int lq_mx4_linear(const lq_linear_desc* d, const void* x, const void* w_codes, c
                    (const void*)ws))
     return LQ_ERR_ALIGN;
   if (!ws || ws_bytes < lq_linear_workspace_bytes(d)) return LQ_ERR_WORKSPACE;
+  if (few_rows(d->m, d->k) && d->n > 0 && d->k > 0 && !ckpt_codes)
+    return status_of(launch_mx4_few(d->in_dtype, x, d->ld_in, w_codes, w_scales, d->m, d->n, d->k, d->out_dtype, y,
+                                    d->ld_out, (hipStream_t)stream));
   uint8_t *codes = (uint8_t*)ws, *scales = (uint8_t*)ws + operand_codes(d);
   if (d->k > 0) {
     const hipError_t e = launch_mx4_quantize(d->in_dtype, d->ckpt_format, x, d->m, d->k, d->ld_in, codes, scales,
@@ -114,7 +132,7 @@ int lq_mx4_linear(const lq_linear_desc* d, const void* x, const void* w_codes, c
   }
   if (d->n == 0) return LQ_OK;
   return status_of(launch_mx4_product(codes, scales, w_codes, w_scales, d->m, d->n, d->k, d->out_dtype, y, d->ld_out,
-                                      (hipStream_t)stream));
+                                      (uint8_t*)ws + operand_bytes(d), (hipStream_t)stream));
 }
 
 int lq_mx4_dgrad(const lq_linear_desc* d, const void* dy, const void* w_codes, const void* w_scales, void* dx,

@@ -1,5 +1,4 @@
 // lq_mx4.hip — 4-bit microscaled quantisation and product.
-#include <atomic>
 #include <type_traits>
 
 #include "lq_linear.h"
@@ -102,7 +101,7 @@ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t tm, uint32_t tn, ui
 template <int OUT, int FM, int FN>
 __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                                                         int64_t m, int64_t n, int64_t k, void* y, int64_t ldy,
-                                                        uint32_t tm, uint32_t tn) {
+                                                        uint32_t tm, uint32_t tn, uint32_t parts, int part_groups) {
   typedef typename El<OUT>::T T;
   constexpr int BM = 64 * FM, BN = 64 * FN;
   __shared__ ProductLds<FM, FN> lds;
@@ -110,7 +109,9 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
   const int r = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
 
   // This workgroup's tiles: its XCD's share, every `slots`-th from its own on.
-  const uint32_t total = tm * tn, xcd = blockIdx.x % 8, slots = (gridDim.x - xcd + 7) / 8;
+  // With the contraction in parts, part p of a tile is a tile of its own, whose
+  // sums go to plane p of y.
+  const uint32_t total = tm * tn * parts, xcd = blockIdx.x % 8, slots = (gridDim.x - xcd + 7) / 8;
   const uint32_t per = total / 8, more = total % 8, begin = xcd * per + (xcd < more ? xcd : more);
   const uint32_t end = begin + per + (xcd < more ? 1 : 0);
   uint32_t tile = begin + blockIdx.x / 8;
@@ -118,30 +119,36 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
 
   // A tile takes at least four steps, so that the transfers reach into the next
   // tile only; steps past the contraction's end read zeros.
-  const int groups = (int)mx4_groups(k), steps = groups < 4 ? 4 : groups;
+  const int groups = (int)mx4_groups(k), steps = part_groups < 4 ? 4 : part_groups;
   struct Tile {
     const uint8_t *x, *w, *xs, *ws;   // codes and scales of its first rows, in group 0
     uint32_t rows, cols;              // that exist, at most BM and BN; 0: no tile
+    int deep;                         // groups of the contraction
   };
-  auto place = [&](uint32_t row, uint32_t col, bool real) {
-    const int64_t r0 = (int64_t)row * BM, c0 = (int64_t)col * BN;
+  auto place = [&](uint32_t row, uint32_t col, uint32_t part, bool real) {
+    const int64_t r0 = (int64_t)row * BM, c0 = (int64_t)col * BN, g0 = (int64_t)part * part_groups;
     Tile t;
-    t.x = x + r0 * 64;
-    t.w = w + c0 * 64;
-    t.xs = xs + r0 * 4;
-    t.ws = ws + c0 * 4;
+    t.x = x + (g0 * m + r0) * 64;
+    t.w = w + (g0 * n + c0) * 64;
+    t.xs = xs + (g0 * mx4_scale_rows(m) + r0) * 4;
+    t.ws = ws + (g0 * mx4_scale_rows(n) + c0) * 4;
+    t.deep = groups - g0 < part_groups ? groups - (int)g0 : part_groups;
     t.rows = real ? (uint32_t)(m - r0 < BM ? m - r0 : BM) : 0;
     t.cols = real ? (uint32_t)(n - c0 < BN ? n - c0 : BN) : 0;
     return t;
   };
-  uint32_t trow, tcol, nrow, ncol;
-  tile_at(tile, tm, tn, trow, tcol);
-  Tile now = place(trow, tcol, true), next;
+  uint32_t trow, tcol, tpart, nrow, ncol, npart;
+  auto tile_of = [&](uint32_t t, uint32_t& row, uint32_t& col, uint32_t& part) {
+    part = parts == 1 ? 0 : __builtin_amdgcn_readfirstlane(t / (tm * tn));
+    tile_at(t - part * (tm * tn), tm, tn, row, col);
+  };
+  tile_of(tile, trow, tcol, tpart);
+  Tile now = place(trow, tcol, tpart, true), next;
   uint32_t following;
   auto look_ahead = [&] {
     following = tile + slots;
-    tile_at(following < end ? following : tile, tm, tn, nrow, ncol);
-    next = place(nrow, ncol, following < end);
+    tile_of(following < end ? following : tile, nrow, ncol, npart);
+    next = place(nrow, ncol, npart, following < end);
   };
   look_ahead();
 
@@ -165,13 +172,13 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
   // The step whose transfers come next: what is left of its rows in memory.
   struct Cursor {
     const uint8_t *x, *w, *s;
-    int t;
-  } at = {now.x, now.w, wave & 1 ? now.ws : now.xs, 0};
+    int t, deep;
+  } at = {now.x, now.w, wave & 1 ? now.ws : now.xs, 0, now.deep};
   uint32_t xbytes = now.rows * 64, wbytes = now.cols * 64, sbytes = ((wave & 1 ? now.cols : now.rows) + 3) / 4 * 16;
   v4i fx, fw, fs;
-  auto point_x = [&] { fx = stretch(at.x, at.t < groups ? xbytes : 0); };
-  auto point_w = [&] { fw = stretch(at.w, at.t < groups ? wbytes : 0); };
-  auto point_s = [&] { fs = stretch(at.s, at.t < groups ? sbytes : 0); };
+  auto point_x = [&] { fx = stretch(at.x, at.t < at.deep ? xbytes : 0); };
+  auto point_w = [&] { fw = stretch(at.w, at.t < at.deep ? wbytes : 0); };
+  auto point_s = [&] { fs = stretch(at.s, at.t < at.deep ? sbytes : 0); };
   // (the transfers run four steps ahead: past the end of this tile, they are the next one's)
   auto advance = [&] {
     const bool wrap = ++at.t == steps;
@@ -182,6 +189,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
     wbytes = wrap ? next.cols * 64 : wbytes;
     sbytes = wrap ? ((wave & 1 ? next.cols : next.rows) + 3) / 4 * 16 : sbytes;
     at.t = wrap ? 0 : at.t;
+    at.deep = wrap ? next.deep : at.deep;
   };
   // Transfer f into stage `st`.
   auto fetch = [&](int st, int f) {
@@ -309,7 +317,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
     const int turn = (l & 31) >> 1, part = (l >> 5) * 4 * (int)sizeof(T);
     const int64_t row0 = (int64_t)trow * BM + wm * 32 * FM, col0 = (int64_t)tcol * BN + wn * 32 * FN;
     const int rr = l / units, cc = l % units;
-    T* const out = (T*)y + (row0 + rr) * ldy + col0 + cc * V;
+    T* const out = (T*)y + (tpart * m + row0 + rr) * ldy + col0 + cc * V;
     const int rows_left = (int)(m - row0 < 32 * FM ? m - row0 : 32 * FM) - rr, cols_left = (int)(n - col0 < 32 * FN ? n - col0 : 32 * FN) - cc * V;
 #pragma unroll
     for (int i = 0; i < FM; i++)
@@ -348,6 +356,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
     tile = following;
     trow = nrow;
     tcol = ncol;
+    tpart = npart;
     now = next;
     look_ahead();
   }
@@ -355,17 +364,154 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// Compute units of the current device (256 on MI355X).
-int compute_units() {
-  static std::atomic<int> cached[64];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  int cus = cached[dev].load(std::memory_order_relaxed);
-  if (cus == 0) {
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) cus = 256;
-    cached[dev].store(cus, std::memory_order_relaxed);
+// ---------------------------------------------------------------- a few rows
+// Up to 16 CT rows of x: the call is bound by reading W once. Eight waves of a
+// workgroup share 16 R rows of W, each taking a run of the contraction's groups
+// with v_mfma_scale_f32_16x16x128_f8f6f4, whose operand of 16 rows and 128
+// columns is one kilobyte of W as it is stored; their sums meet in LDS. With SRC
+// a float type (up to kFewRows rows) every workgroup quantises x itself, a block
+// a thread, into LDS while its first reads of W are on their way: a launch of
+// its own for x would cost a quarter of the call. Otherwise x is an MX4 operand.
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint16_t v2u __attribute__((ext_vector_type(2)));
+constexpr int kOperand = -1;
+constexpr int kFewWaves = 8;
+
+// One block of x, `valid` of whose 32 elements exist: its codes and scale byte.
+template <int SRC>
+__device__ __forceinline__ v4i quantise_block(const typename El<SRC>::T* p, int valid, uint32_t& scale) {
+  float v[32];
+  if (valid >= 32) {
+    typename El<SRC>::T t[32];
+    __builtin_memcpy(t, p, sizeof(t));
+#pragma unroll
+    for (int i = 0; i < 32; i++) v[i] = widen<SRC>(t[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; i++) v[i] = i < valid ? widen<SRC>(p[i]) : 0.0f;
   }
-  return cus;
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 32; i++) {
+    const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    amax = amax > b ? amax : b;
+  }
+  scale = scale_byte<LQ_E2M1>(amax);
+  const float r = scale_recip(scale);
+  v4i out;
+#pragma unroll
+  for (int i = 0; i < 4; i++) out[i] = (int)encode_e2m1(v + 8 * i, r);
+  return out;
+}
+
+template <int SRC, int OUT, int R, int CT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64_t ldx, const uint8_t* xs, const uint8_t* w,
+                                                            const uint8_t* ws, int64_t m, int64_t n, int64_t k, void* y,
+                                                            int64_t ldy) {
+  typedef typename El<OUT>::T T;
+  constexpr bool own = SRC != kOperand;
+  __shared__ v4f sums[kFewWaves][R * CT][64];
+  __shared__ v4i xcodes[own ? kFewBlocks : 1];
+  __shared__ uint8_t xscales[own ? kFewBlocks : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int64_t row0 = (int64_t)blockIdx.x * 16 * R;
+  const int groups = (int)mx4_groups(k), per = (groups + kFewWaves - 1) / kFewWaves;
+  const int begin = wave * per, end = begin + per < groups ? begin + per : groups;
+  const int64_t wstep = mx4_scale_rows(n) * 4, xstep = mx4_scale_rows(m) * 4;
+  int64_t wrow[R];   // rows past the last are the last again
+#pragma unroll
+  for (int i = 0; i < R; i++) wrow[i] = row0 + i * 16 + r < n ? row0 + i * 16 + r : n - 1;
+
+  constexpr int U = 4;   // groups whose reads are in flight together
+  struct Reads {
+    v4i wc[U][R], xc[own ? 1 : U][CT];
+    uint32_t we[U][R], xe[own ? 1 : U][CT];
+  };
+  auto load = [&](Reads& a, int g0) {
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int g = g0 + u < groups ? g0 + u : groups - 1;
+#pragma unroll
+      for (int i = 0; i < R; i++) {
+        a.wc[u][i] = *(const v4i*)(w + (g * n + wrow[i]) * 64 + q * 16);
+        a.we[u][i] = ws[g * wstep + wrow[i] * 4 + q];
+      }
+      if constexpr (!own) {
+#pragma unroll
+        for (int c = 0; c < CT; c++) {
+          const int64_t at = c * 16 + r < m ? c * 16 + r : m - 1;
+          a.xc[u][c] = *(const v4i*)((const uint8_t*)x + (g * m + at) * 64 + q * 16);
+          a.xe[u][c] = xs[g * xstep + at * 4 + q];
+        }
+      }
+    }
+  };
+  Reads a, b;
+  if (begin < end) load(a, begin);
+  if constexpr (own) {
+    const int blocks = groups * 4;
+    for (int i = threadIdx.x; i < (int)m * blocks; i += 64 * kFewWaves) {
+      const int row = i / blocks, col = (i - row * blocks) * 32;
+      const int valid = k - col < 32 ? (int)(k - col) : 32;
+      uint32_t e;
+      xcodes[i] = quantise_block<SRC>((const typename El<SRC>::T*)x + row * ldx + col, valid, e);
+      xscales[i] = (uint8_t)e;
+    }
+    __syncthreads();
+  }
+  v4f acc[R][CT];
+#pragma unroll
+  for (int i = 0; i < R; i++)
+#pragma unroll
+    for (int c = 0; c < CT; c++) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int g0 = begin; g0 < end; g0 += U) {
+    if (g0 + U < end) load(b, g0 + U);
+#pragma unroll
+    for (int u = 0; u < U; u++)
+      if (g0 + u < end) {
+#pragma unroll
+        for (int c = 0; c < CT; c++) {
+          v4i xc = {0, 0, 0, 0};
+          uint32_t xe = 0;
+          if constexpr (own) {
+            if (r < m) {
+              const int at = (r * groups + g0 + u) * 4 + q;
+              xc = xcodes[at];
+              xe = xscales[at];
+            }
+          } else {
+            xc = a.xc[u][c];
+            xe = a.xe[u][c];
+          }
+#pragma unroll
+          for (int i = 0; i < R; i++) {
+            const v8i A = {a.wc[u][i][0], a.wc[u][i][1], a.wc[u][i][2], a.wc[u][i][3], 0, 0, 0, 0};
+            const v8i B = {xc[0], xc[1], xc[2], xc[3], 0, 0, 0, 0};
+            acc[i][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc[i][c], 4, 4, 0, (int)a.we[u][i], 0, (int)xe);
+          }
+        }
+      }
+    a = b;
+  }
+#pragma unroll
+  for (int i = 0; i < R; i++)
+#pragma unroll
+    for (int c = 0; c < CT; c++) sums[wave][i * CT + c][lane] = acc[i][c];
+  __syncthreads();
+  // A lane's four sums are columns 4q .. 4q + 3 of one row of y.
+  for (int t = wave; t < R * CT; t += kFewWaves) {
+    v4f s = sums[0][t][lane];
+#pragma unroll
+    for (int v = 1; v < kFewWaves; v++) s += sums[v][t][lane];
+    const int64_t row = t % CT * 16 + r, col = row0 + t / CT * 16 + 4 * q;
+    if (row < m) {
+      T* o = (T*)y + row * ldy + col;
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (col + e < n) o[e] = narrow<OUT>(s[e]);
+    }
+  }
 }
 
 template <int DT>
@@ -382,25 +528,56 @@ hipError_t quantize_dt(int format, const void* x, int64_t m, int64_t k, int64_t 
 }
 
 // One workgroup a compute unit for the 256 x 256 tile (its LDS), more for the
-// smaller ones.
+// smaller ones. With parts > 1, y is `parts` planes of m x n.
 template <int OUT, int FM, int FN>
 hipError_t product_tiled(const void* a, const void* as, const void* w, const void* ws, int64_t m, int64_t n, int64_t k,
-                         void* y, int64_t ldy, hipStream_t s) {
-  const int64_t tm = (m + 64 * FM - 1) / (64 * FM), tn = (n + 64 * FN - 1) / (64 * FN);
+                         int parts, int part_groups, void* y, int64_t ldy, hipStream_t s) {
+  const int64_t tm = (m + 64 * FM - 1) / (64 * FM), tn = (n + 64 * FN - 1) / (64 * FN), tiles = tm * tn * parts;
   const int64_t most = (int64_t)compute_units() * (int)(163840 / sizeof(ProductLds<FM, FN>));
-  hipLaunchKernelGGL((k_mx4_product<OUT, FM, FN>), dim3((unsigned)(tm * tn < most ? tm * tn : most)), dim3(256), 0, s,
+  hipLaunchKernelGGL((k_mx4_product<OUT, FM, FN>), dim3((unsigned)(tiles < most ? tiles : most)), dim3(256), 0, s,
                      (const uint8_t*)a, (const uint8_t*)as, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy,
-                     (uint32_t)tm, (uint32_t)tn);
+                     (uint32_t)tm, (uint32_t)tn, (uint32_t)parts, part_groups);
+  return hipGetLastError();
+}
+template <int SRC, int OUT, int CT>
+hipError_t few(const void* x, int64_t ldx, const void* xs, const void* w, const void* ws, int64_t m, int64_t n, int64_t k,
+               void* y, int64_t ldy, hipStream_t s) {
+  if (n > 16 * 512) {
+    hipLaunchKernelGGL((k_mx4_few<SRC, OUT, 2, CT>), dim3((unsigned)((n + 31) / 32)), dim3(64 * kFewWaves), 0, s, x, ldx,
+                       (const uint8_t*)xs, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy);
+  } else {
+    hipLaunchKernelGGL((k_mx4_few<SRC, OUT, 1, CT>), dim3((unsigned)((n + 15) / 16)), dim3(64 * kFewWaves), 0, s, x, ldx,
+                       (const uint8_t*)xs, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy);
+  }
   return hipGetLastError();
 }
 template <int OUT>
+hipError_t few_src(int in_dtype, const void* x, int64_t ldx, const void* w, const void* ws, int64_t m, int64_t n, int64_t k,
+                   void* y, int64_t ldy, hipStream_t s) {
+  switch (in_dtype) {
+    case LQ_F32: return few<LQ_F32, OUT, 1>(x, ldx, nullptr, w, ws, m, n, k, y, ldy, s);
+    case LQ_BF16: return few<LQ_BF16, OUT, 1>(x, ldx, nullptr, w, ws, m, n, k, y, ldy, s);
+    default: return few<LQ_F16, OUT, 1>(x, ldx, nullptr, w, ws, m, n, k, y, ldy, s);
+  }
+}
+
+template <int OUT>
+hipError_t product_tile(int tile, const void* a, const void* as, const void* w, const void* ws, int64_t m, int64_t n,
+                        int64_t k, int parts, int part_groups, void* y, int64_t ldy, hipStream_t s) {
+  if (tile == 4) return product_tiled<OUT, 4, 4>(a, as, w, ws, m, n, k, parts, part_groups, y, ldy, s);
+  if (tile == 2) return product_tiled<OUT, 2, 2>(a, as, w, ws, m, n, k, parts, part_groups, y, ldy, s);
+  return product_tiled<OUT, 1, 1>(a, as, w, ws, m, n, k, parts, part_groups, y, ldy, s);
+}
+template <int OUT>
 hipError_t product_dt(const void* a, const void* as, const void* w, const void* ws, int64_t m, int64_t n, int64_t k,
-                      void* y, int64_t ldy, hipStream_t s) {
+                      void* y, int64_t ldy, void* planes, hipStream_t s) {
   if (k == 0) return launch_constant(m, n, OUT, nullptr, y, ldy, s);
-  const int64_t t4 = (m + 255) / 256 * ((n + 255) / 256), t2 = (m + 127) / 128 * ((n + 127) / 128);
-  if (t4 >= 200) return product_tiled<OUT, 4, 4>(a, as, w, ws, m, n, k, y, ldy, s);
-  if (t2 >= 128) return product_tiled<OUT, 2, 2>(a, as, w, ws, m, n, k, y, ldy, s);
-  return product_tiled<OUT, 1, 1>(a, as, w, ws, m, n, k, y, ldy, s);
+  if (m <= 16) return few<kOperand, OUT, 1>(a, 0, as, w, ws, m, n, k, y, ldy, s);
+  if (m <= 32) return few<kOperand, OUT, 2>(a, 0, as, w, ws, m, n, k, y, ldy, s);
+  const Split c = split_product(m, n, k);
+  if (c.parts == 1) return product_tile<OUT>(c.tile, a, as, w, ws, m, n, k, 1, c.part, y, ldy, s);
+  const hipError_t e = product_tile<LQ_F32>(c.tile, a, as, w, ws, m, n, k, c.parts, c.part, planes, plane_stride(n), s);
+  return e != hipSuccess ? e : launch_join(m, n, OUT, c.parts, (const float*)planes, nullptr, y, ldy, s);
 }
 
 // y = in, or zeros: what is left of a product over an empty contraction.
@@ -413,7 +590,52 @@ __global__ __launch_bounds__(256) void k_constant(int64_t rows, int64_t cols, co
   }
 }
 
+// y = in + the planes' sum, in the planes' order: four columns a lane, a wave's
+// on one row.
+template <int OUT>
+__global__ __launch_bounds__(256) void k_join(int64_t rows, int64_t cols, int parts, const float* planes,
+                                              const float* in, void* y, int64_t ldy) {
+  const int64_t stride = plane_stride(cols), plane = rows * stride;
+  const uint32_t across = (uint32_t)((cols + 255) / 256);
+  const int64_t units = rows * across;
+  for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < units; u += (int64_t)gridDim.x * 4) {
+    const int64_t row = u / across, col = u % across * 256 + (threadIdx.x & 63) * 4;
+    if (col >= cols) continue;
+    const float* p = planes + row * stride + col;
+    float4 s = *(const float4*)p;
+#pragma unroll 4
+    for (int i = 1; i < parts; i++) {
+      const float4 t = *(const float4*)(p + i * plane);
+      s.x += t.x;
+      s.y += t.y;
+      s.z += t.z;
+      s.w += t.w;
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    typename El<OUT>::T* o = (typename El<OUT>::T*)y + row * ldy + col;
+    typename El<OUT>::T t[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) t[e] = narrow<OUT>(in && col + e < cols ? v[e] + in[row * ldy + col + e] : v[e]);
+    if (cols - col >= 4) {
+      __builtin_memcpy(o, t, sizeof(t));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (col + e < cols) o[e] = t[e];
+    }
+  }
+}
+
 }  // namespace
+
+hipError_t launch_join(int64_t rows, int64_t cols, int dtype, int parts, const float* planes, const float* in, void* y,
+                       int64_t ldy, hipStream_t s) {
+  const dim3 g(stream_grid(rows * ((cols + 255) / 256)));
+  if (dtype == LQ_F32) hipLaunchKernelGGL((k_join<LQ_F32>), g, dim3(256), 0, s, rows, cols, parts, planes, in, y, ldy);
+  else if (dtype == LQ_BF16) hipLaunchKernelGGL((k_join<LQ_BF16>), g, dim3(256), 0, s, rows, cols, parts, planes, in, y, ldy);
+  else hipLaunchKernelGGL((k_join<LQ_F16>), g, dim3(256), 0, s, rows, cols, parts, planes, in, y, ldy);
+  return hipGetLastError();
+}
 
 hipError_t launch_constant(int64_t rows, int64_t cols, int dtype, const void* in, void* y, int64_t ldy, hipStream_t s) {
   const dim3 g(stream_grid(rows * ((cols + 255) / 256)));
@@ -433,12 +655,22 @@ hipError_t launch_mx4_quantize(int in_dtype, int ckpt_format, const void* x, int
   }
 }
 
-hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
-                              int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s) {
+hipError_t launch_mx4_few(int in_dtype, const void* x, int64_t ldx, const void* w_codes, const void* w_scales, int64_t m,
+                          int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s) {
   switch (out_dtype) {
-    case LQ_F32: return product_dt<LQ_F32>(a_codes, a_scales, w_codes, w_scales, m, n, k, y, ldy, s);
-    case LQ_BF16: return product_dt<LQ_BF16>(a_codes, a_scales, w_codes, w_scales, m, n, k, y, ldy, s);
-    default: return product_dt<LQ_F16>(a_codes, a_scales, w_codes, w_scales, m, n, k, y, ldy, s);
+    case LQ_F32: return few_src<LQ_F32>(in_dtype, x, ldx, w_codes, w_scales, m, n, k, y, ldy, s);
+    case LQ_BF16: return few_src<LQ_BF16>(in_dtype, x, ldx, w_codes, w_scales, m, n, k, y, ldy, s);
+    default: return few_src<LQ_F16>(in_dtype, x, ldx, w_codes, w_scales, m, n, k, y, ldy, s);
+  }
+}
+
+hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
+                              int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, void* planes,
+                              hipStream_t s) {
+  switch (out_dtype) {
+    case LQ_F32: return product_dt<LQ_F32>(a_codes, a_scales, w_codes, w_scales, m, n, k, y, ldy, planes, s);
+    case LQ_BF16: return product_dt<LQ_BF16>(a_codes, a_scales, w_codes, w_scales, m, n, k, y, ldy, planes, s);
+    default: return product_dt<LQ_F16>(a_codes, a_scales, w_codes, w_scales, m, n, k, y, ldy, planes, s);
   }
 }
 

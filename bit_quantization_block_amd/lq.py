@@ -142,6 +142,21 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+_raw_stream = None
+
+
+def _stream_of(device: int, stream):
+    """The stream given, or torch's current one on this device, without the objects around it."""
+    global _raw_stream
+    if stream is not None:
+        return stream
+    if _raw_stream is None:
+        import torch
+
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(device)
+
+
 def _check(fn, rc):
     if rc != LQ_OK:
         raise LQError(fn, rc)
@@ -376,14 +391,19 @@ class Ckpt8:
                                                            _ptr(self.scales), _stream(stream)))
 
 
+def _layout(*tensors):
+    """What a call's checks depend on: shapes, strides, types and devices."""
+    return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in tensors])
+
+
 class Mx4Linear:
     """A linear layer y = x W^T with W held in 4 bits (MXFP4), and its
     gradients. `w` [n, k] is quantised once; `rows` is the most rows of x or
-    dy a call may have, for which the workspace and the results' buffers are
-    allocated once (a call's result is a view of the layer's buffer, which the
-    layer's next call of that kind overwrites, unless the caller passes its
-    own as `out`). `dtype`: of x; `out`: of y and dx; dy is bfloat16 and dw
-    float32."""
+    dy a call may have, for which the results' buffers are allocated once (a
+    call's result is a view of the layer's buffer, which the layer's next call
+    of that kind overwrites, unless the caller passes its own as `out`).
+    `dtype`: of x; `out`: of y and dx; dy is bfloat16 and dw float32. Calls of
+    one layer share its workspace: on two streams at a time, use two layers."""
 
     def __init__(self, w, rows: int, dtype: str = "bf16", out: str = "bf16", lib=None):
         import torch
@@ -400,78 +420,91 @@ class Mx4Linear:
         d = LinearDesc(DTYPE[_dtype_name(w)], 0, 0, 0, self.n, 0, self.k, ld, 0)
         _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(w), _ptr(self.codes),
                                                            _ptr(self.scales), None, None, _stream(None)))
-        self._w = (self.codes.data_ptr(), self.scales.data_ptr())
-        self._descs = {}
+        self._wc, self._ws = ctypes.c_void_p(self.codes.data_ptr()), ctypes.c_void_p(self.scales.data_ptr())
+        self._index = w.device.index
+        self._plans = {}
         self._buffers = {}
-        self.ws, self._old_ws = None, []
+        self._workspaces = []
 
-    def _desc(self, kind, m, ld_in, ld_out, in_dtype, out_dtype, fmt):
-        key = (kind, m, ld_in, ld_out, fmt)
-        d = self._descs.get(key)
-        if d is None:
-            if m > self.rows:
-                raise ValueError(f"{m} rows in a layer planned for {self.rows}")
-            d = LinearDesc(DTYPE[in_dtype], DTYPE[out_dtype], FORMAT[fmt], 0, m, self.n, self.k, ld_in, ld_out)
-            need = self.lib.lq_linear_workspace_bytes(ctypes.byref(d))
-            if need == 0:
-                raise LQError(kind, self.lib.lq_mx4_quantize(ctypes.byref(d), None, None, None, None, None, None))
-            if self.ws is None or self.ws.numel() < need:
-                # a smaller one stays alive: a captured graph may hold its address
-                self._old_ws.append(self.ws)
-                self.ws = self.torch.empty(need, dtype=self.torch.uint8, device=self.device)
-            if len(self._descs) > 256:
-                self._descs.clear()
-            self._descs[key] = d
-        return d
+    def _workspace(self, need):
+        """One of at least this size. Smaller ones stay alive: a captured graph may hold their addresses."""
+        if not self._workspaces or self._workspaces[-1].numel() < need:
+            self._workspaces.append(self.torch.empty(need, dtype=self.torch.uint8, device=self.device))
+        return self._workspaces[-1]
 
-    def _result(self, kind, rows, cols, dtype, out):
-        """The result's tensor and row stride: the caller's, or a view of the layer's buffer."""
+    def _plan(self, key, kind, a, what, cols_in, cols_out, in_dtype, out_dtype, fmt, out):
+        """The checked descriptor, the workspace and the result's buffer of a call with this layout."""
+        m = a.shape[0]
+        if m > self.rows:
+            raise ValueError(f"{m} rows in a layer planned for {self.rows}")
+        ld_in = _matrix(a, m, cols_in, _torch_dtype(in_dtype), what)
+        rows_out = self.n if kind == "dw" else m
         if out is not None:
-            return out, _matrix(out, rows, cols, _torch_dtype(dtype), "out")
-        b = self._buffers.get(kind)
-        if b is None:
-            most = self.n if kind == "dw" else self.rows
-            b = self._buffers[kind] = self.torch.empty(most, cols, dtype=_torch_dtype(dtype), device=self.device)
-        return (b if b.shape[0] == rows else b[:rows]), cols
+            buffer, ld_out = None, _matrix(out, rows_out, cols_out, _torch_dtype(out_dtype), "out")
+        else:
+            b = self._buffers.get(kind)
+            if b is None:
+                most = self.n if kind == "dw" else self.rows
+                b = self._buffers[kind] = self.torch.empty(most, cols_out, dtype=_torch_dtype(out_dtype),
+                                                           device=self.device)
+            buffer, ld_out = b[:rows_out], cols_out
+        d = LinearDesc(DTYPE[in_dtype], DTYPE[out_dtype], FORMAT[fmt], 0, m, self.n, self.k, ld_in, ld_out)
+        ref = ctypes.byref(d)
+        need = self.lib.lq_linear_workspace_bytes(ref)
+        if need == 0:   # the descriptor is refused: by this call too, with the status
+            _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ref, None, None, None, None, None, None))
+        ws = self._workspace(need)
+        if len(self._plans) >= 256:
+            self._plans.clear()
+        plan = self._plans[key] = (ref, ctypes.c_void_p(ws.data_ptr()), ws.numel(), buffer)
+        return plan
 
     def forward(self, x, ckpt: Ckpt8 | None = None, out=None, stream=None):
         """y = Q4(x) W^T; `ckpt` also receives x in 8 bits."""
-        m = x.shape[0]
-        ld = _matrix(x, m, self.k, _torch_dtype(self.dtype), "x")
-        self._check_ckpt(ckpt, m)
-        y, ldy = self._result("y", m, self.n, self.out, out)
-        d = self._desc("lq_mx4_linear", m, ld, ldy, self.dtype, self.out, ckpt.fmt if ckpt else "int8")
-        _check("lq_mx4_linear", self.lib.lq_mx4_linear(
-            ctypes.byref(d), x.data_ptr(), *self._w, y.data_ptr(), ckpt.codes.data_ptr() if ckpt else None,
-            ckpt.scales.data_ptr() if ckpt else None, self.ws.data_ptr(), self.ws.numel(), _stream(stream)))
+        key = ("y", ckpt.fmt if ckpt else "int8", _layout(x, out))
+        plan = self._plans.get(key) or self._plan(key, "y", x, "x", self.k, self.n, self.dtype, self.out, key[1], out)
+        cc = cs = None
+        if ckpt is not None:
+            self._check_ckpt(ckpt, x.shape[0])
+            cc, cs = ckpt.codes.data_ptr(), ckpt.scales.data_ptr()
+        y = plan[3] if out is None else out
+        rc = self.lib.lq_mx4_linear(plan[0], x.data_ptr(), self._wc, self._ws, y.data_ptr(), cc, cs, plan[1], plan[2],
+                                    _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_mx4_linear", rc)
         return y
 
     def dgrad(self, dy, out=None, stream=None):
         """dx = dy W."""
-        m = dy.shape[0]
-        ld = _matrix(dy, m, self.n, self.torch.bfloat16, "dy")
-        dx, ldx = self._result("dx", m, self.k, self.out, out)
-        d = self._desc("lq_mx4_dgrad", m, ld, ldx, "bf16", self.out, "int8")
-        _check("lq_mx4_dgrad", self.lib.lq_mx4_dgrad(ctypes.byref(d), dy.data_ptr(), *self._w, dx.data_ptr(),
-                                                     self.ws.data_ptr(), self.ws.numel(), _stream(stream)))
+        key = ("dx", _layout(dy, out))
+        plan = self._plans.get(key) or self._plan(key, "dx", dy, "dy", self.n, self.k, "bf16", self.out, "int8", out)
+        dx = plan[3] if out is None else out
+        rc = self.lib.lq_mx4_dgrad(plan[0], dy.data_ptr(), self._wc, self._ws, dx.data_ptr(), plan[1], plan[2],
+                                   _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_mx4_dgrad", rc)
         return dx
 
     def wgrad(self, dy, ckpt: Ckpt8, dw_in=None, out=None, stream=None):
         """dw = dw_in + dy^T x8, x8 the checkpoint that forward wrote; `out` may be dw_in."""
-        m = dy.shape[0]
-        ld = _matrix(dy, m, self.n, self.torch.bfloat16, "dy")
-        self._check_ckpt(ckpt, m)
-        dw, lddw = self._result("dw", self.n, self.k, "f32", out)
-        if dw_in is not None and _matrix(dw_in, self.n, self.k, self.torch.float32, "dw_in") != lddw:
-            raise ValueError("dw_in and the result differ in their row strides")
-        d = self._desc("lq_ckpt8_wgrad", m, ld, lddw, "bf16", "f32", ckpt.fmt)
-        _check("lq_ckpt8_wgrad", self.lib.lq_ckpt8_wgrad(
-            ctypes.byref(d), dy.data_ptr(), ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), _ptr(dw_in), dw.data_ptr(),
-            self.ws.data_ptr(), self.ws.numel(), _stream(stream)))
+        key = ("dw", ckpt.fmt, _layout(dy, dw_in, out))
+        plan = self._plans.get(key)
+        if plan is None:
+            if dw_in is not None:
+                ld = _matrix(dw_in, self.n, self.k, self.torch.float32, "dw_in")
+                if ld != (self.k if out is None else _matrix(out, self.n, self.k, self.torch.float32, "out")):
+                    raise ValueError("dw_in and the result differ in their row strides")
+            plan = self._plan(key, "dw", dy, "dy", self.n, self.k, "bf16", "f32", ckpt.fmt, out)
+        self._check_ckpt(ckpt, dy.shape[0])
+        dw = plan[3] if out is None else out
+        rc = self.lib.lq_ckpt8_wgrad(plan[0], dy.data_ptr(), ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), _ptr(dw_in),
+                                     dw.data_ptr(), plan[1], plan[2], _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_ckpt8_wgrad", rc)
         return dw
 
     def _check_ckpt(self, ckpt, m):
-        if ckpt is not None and (ckpt.rows != m or ckpt.cols != self.k):
+        if ckpt.rows != m or ckpt.cols != self.k:
             raise ValueError(f"the checkpoint is {ckpt.rows} x {ckpt.cols}, the call's x {m} x {self.k}")
 
 
@@ -489,47 +522,60 @@ class SwigluCkpt8:
         self._t = _torch_dtype(dtype)
         self.gate = Ckpt8(rows, cols, fmt, device, lib)
         self.up = Ckpt8(rows, cols, fmt, device, lib)
-        self._kept = (self.gate.codes.data_ptr(), self.gate.scales.data_ptr(), self.up.codes.data_ptr(),
-                      self.up.scales.data_ptr())
-        self._device = device
-        self._descs = {}
+        self._kept = tuple(ctypes.c_void_p(t.data_ptr()) for c in (self.gate, self.up) for t in (c.codes, c.scales))
+        self.device = self.gate.codes.device
+        self._index = self.device.index
+        self._plans = {}
         self._buffers = {}
 
-    def _desc(self, ld, ld_h):
-        d = self._descs.get((ld, ld_h))
-        if d is None:
-            d = self._descs[(ld, ld_h)] = SwigluDesc(DTYPE[self.dtype], FORMAT[self.fmt], self.rows, self.cols, ld,
-                                                     ld_h)
-        return d
-
     def _result(self, kind, out):
+        """The result's tensor if it is the object's own, and its row stride."""
         if out is not None:
-            return out, _matrix(out, self.rows, self.cols, self._t, "out")
+            return None, _matrix(out, self.rows, self.cols, self._t, "out")
         b = self._buffers.get(kind)
         if b is None:
-            b = self._buffers[kind] = self.torch.empty(self.rows, self.cols, dtype=self._t, device=self._device)
+            b = self._buffers[kind] = self.torch.empty(self.rows, self.cols, dtype=self._t, device=self.device)
         return b, self.cols
 
+    def _remember(self, key, ld, ld_h, *own):
+        if len(self._plans) >= 256:
+            self._plans.clear()
+        d = SwigluDesc(DTYPE[self.dtype], FORMAT[self.fmt], self.rows, self.cols, ld, ld_h)
+        plan = self._plans[key] = (ctypes.byref(d), *own)
+        return plan
+
     def forward(self, gate, up, out=None, stream=None):
-        ld = _matrix(gate, self.rows, self.cols, self._t, "gate")
-        if _matrix(up, self.rows, self.cols, self._t, "up") != ld:
-            raise ValueError("gate and up differ in their row strides")
-        h, ldh = self._result("h", out)
-        _check("lq_swiglu_ckpt8", self.lib.lq_swiglu_ckpt8(
-            ctypes.byref(self._desc(ld, ldh)), gate.data_ptr(), up.data_ptr(), h.data_ptr(), *self._kept,
-            _stream(stream)))
+        key = _layout(gate, up, out)
+        plan = self._plans.get(key)
+        if plan is None:
+            ld = _matrix(gate, self.rows, self.cols, self._t, "gate")
+            if _matrix(up, self.rows, self.cols, self._t, "up") != ld:
+                raise ValueError("gate and up differ in their row strides")
+            own, ldh = self._result("h", out)
+            plan = self._remember(key, ld, ldh, own)
+        h = plan[1] if out is None else out
+        rc = self.lib.lq_swiglu_ckpt8(plan[0], gate.data_ptr(), up.data_ptr(), h.data_ptr(), *self._kept,
+                                      _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_swiglu_ckpt8", rc)
         return h
 
     def backward(self, dh, out=None, stream=None):
         """(dgate, dup); `out`: a pair of tensors for them."""
-        ldh = _matrix(dh, self.rows, self.cols, self._t, "dh")
-        dg, ld = self._result("dgate", out[0] if out else None)
-        du, ld2 = self._result("dup", out[1] if out else None)
-        if ld != ld2:
-            raise ValueError("dgate and dup differ in their row strides")
-        _check("lq_swiglu_ckpt8_backward", self.lib.lq_swiglu_ckpt8_backward(
-            ctypes.byref(self._desc(ld, ldh)), dh.data_ptr(), *self._kept, dg.data_ptr(), du.data_ptr(),
-            _stream(stream)))
+        key = _layout(dh) if out is None else _layout(dh, out[0], out[1], None)
+        plan = self._plans.get(key)
+        if plan is None:
+            ldh = _matrix(dh, self.rows, self.cols, self._t, "dh")
+            own0, ld = self._result("dgate", out[0] if out else None)
+            own1, ld1 = self._result("dup", out[1] if out else None)
+            if ld != ld1:
+                raise ValueError("dgate and dup differ in their row strides")
+            plan = self._remember(key, ld, ldh, own0, own1)
+        dg, du = (plan[1], plan[2]) if out is None else out
+        rc = self.lib.lq_swiglu_ckpt8_backward(plan[0], dh.data_ptr(), *self._kept, dg.data_ptr(), du.data_ptr(),
+                                               _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_swiglu_ckpt8_backward", rc)
         return dg, du
 
 
