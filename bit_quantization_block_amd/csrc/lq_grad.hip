@@ -80,14 +80,13 @@ __device__ __forceinline__ v4s read_columns(place_t p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
 }
 
-// Two INT8 codes (the low bytes) times their scale as bfloat16: code + 128 is an
-// unsigned byte, so one conversion and one fused multiply-add give the exact
+// Two INT8 codes times their scale as bfloat16: bytes `first` and first + 1 of w,
+// the codes with their top bit turned, which are code + 128 as unsigned bytes.
+// One conversion and one fused multiply-add (off = -128 s) give the exact
 // binary32 value, whose upper half is the bfloat16.
-__device__ __forceinline__ int widen_int8(uint32_t w, float s) {
-  const uint32_t u = w ^ 0x8080u;
-  const float off = -128.0f * s;
-  const uint32_t a = __float_as_uint(__builtin_fmaf((float)(u & 0xFFu), s, off));
-  const uint32_t b = __float_as_uint(__builtin_fmaf((float)(u >> 8 & 0xFFu), s, off));
+__device__ __forceinline__ int widen_int8(uint32_t w, int first, float s, float off) {
+  const uint32_t a = __float_as_uint(__builtin_fmaf((float)(w >> 8 * first & 0xFFu), s, off));
+  const uint32_t b = __float_as_uint(__builtin_fmaf((float)(w >> 8 * (first + 1) & 0xFFu), s, off));
   return (int)__builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
@@ -220,7 +219,8 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
   // Unit i of the step's W or x8: 8 codes, converted in kBits bits and stored with the last.
   constexpr int kBits = KIND == kWgrad && F == LQ_INT8 ? 4 : 2;
   static_assert(kUnitsB == kLoadsA, "a thread has as many units of either operand");
-  float scale[kLoadsB];
+  float scale[kLoadsB], offset[kLoadsB];
+  uint32_t turned;
   v4i made;
   auto put_b = [&](int st, int set, int i, int bit) {
     const int l = i / kEach, u = i % kEach;
@@ -235,7 +235,8 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
         made[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
       }
     } else if (F == LQ_INT8) {
-      made[bit] = widen_int8(rb[set][l][2 * u + bit / 2] >> (bit & 1) * 16, s);
+      if (bit % 2 == 0) turned = (uint32_t)rb[set][l][2 * u + bit / 2] ^ 0x80808080u;
+      made[bit] = widen_int8(turned, bit % 2 * 2, s, offset[l]);
     } else {
       const int w = rb[set][l][2 * u + bit];
       made[2 * bit] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
@@ -325,7 +326,10 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
 #pragma unroll
     for (int i = 0; i < kLoadsB; i++) load_b(set, i);
   };
-  auto take_scales = [&](int set, int i) { scale[i] = scale_value(rs[set][i]); };
+  auto take_scales = [&](int set, int i) {
+    scale[i] = scale_value(rs[set][i]);
+    offset[i] = -128.0f * scale[i];
+  };
   load(begin, 0);
   load(begin + 1, 1);
 #pragma unroll

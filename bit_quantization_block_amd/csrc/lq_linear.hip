@@ -46,14 +46,64 @@ size_t operand_bytes(const lq_linear_desc* d) {
 
 namespace lql {
 
-Split split_product(int64_t m, int64_t n, int64_t k) {
-  const int64_t t4 = (m + 255) / 256 * ((n + 255) / 256), t2 = (m + 127) / 128 * ((n + 127) / 128);
-  return {t4 >= 200 ? 4 : t2 >= 128 ? 2 : 1, 1, (int)mx4_groups(k)};
+namespace {
+
+// What a tile of a product costs, in microseconds: a fixed part, and a step of
+// its contraction with almost no other workgroup running, with one on each of
+// 256 compute units, and with more of them on each.
+struct TileCost { int tile, most; double fixed, alone, full[4]; };
+// (64: 11008 x 4096 times 64 rows 9.5 us in one part, 14.6 in two; 128: 2048 x
+// 4096 x 4096 23.2 us, with 256 30.0; 256: 8192 x 8192 x 8192 262 us)
+constexpr TileCost kProductTiles[] = {{1, 3, 3.0, 0.18, {0, 0.20, 0.34, 0.50}},
+                                      {2, 2, 3.5, 0.22, {0, 0.38, 0.62}},
+                                      {4, 1, 6.0, 0.55, {0, 0.95}}};
+// (128: 2048 x 4096 x 4096 64 us in one part, with 256 76 us in two; 256: 8192
+// x 11008 x 4096 634 us)
+constexpr TileCost kGradTiles[] = {{2, 2, 4.0, 0.50, {0, 0.62, 1.02}}, {4, 1, 9.0, 1.25, {0, 1.70}}};
+
+// The tile and the number of parts that the figures above say is fastest. Few
+// tiles over a long contraction gain from parts (512 x 1024 outputs over 16384:
+// 130 us in one part, 32 in eight); adding the parts up costs a launch and their
+// sums' way through memory and back.
+template <size_t N>
+Split cheapest(const TileCost (&tiles)[N], int64_t rows, int64_t cols, int64_t steps) {
+  const double cus = compute_units();
+  Split best = {tiles[0].tile, 1, (int)steps};
+  double least = 1e300;
+  for (const TileCost& c : tiles) {
+    const int64_t side = 64 * c.tile, count = (rows + side - 1) / side * ((cols + side - 1) / side);
+    for (int64_t wanted : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      const int64_t part = (steps + wanted - 1) / wanted, parts = part ? (steps + part - 1) / part : 1;
+      if (wanted > 1 && (part < 4 || parts != wanted)) continue;
+      const double wgs = (double)count * parts, planes = (double)parts * rows * cols * 4;
+      if (parts > 1 && planes > 256e6) continue;
+      double us = c.fixed;
+      if (wgs <= cus) {
+        us += part * (c.alone + (c.full[1] - c.alone) * wgs / cus);
+      } else {
+        double left = wgs;   // full rounds, then what is left over
+        us = 0.0;
+        while (left > 0) {
+          const int each = left >= cus * c.most ? c.most : (int)((left + cus - 1) / cus);
+          const double rounds = left >= cus * c.most ? (double)(int64_t)(left / (cus * c.most)) : 1.0;
+          us += rounds * (c.fixed + part * c.full[each]);
+          left -= rounds * cus * each;
+        }
+      }
+      if (parts > 1) us += 2.5 + planes * 2 / 4.5e6;
+      if (us < least) {
+        least = us;
+        best = {c.tile, (int)parts, (int)part};
+      }
+    }
+  }
+  return best;
 }
-Split split_grad(int64_t rows, int64_t cols, int64_t depth) {
-  const int64_t t4 = (rows + 255) / 256 * ((cols + 255) / 256);
-  return {t4 >= 200 ? 4 : 2, 1, (int)((depth + 63) / 64)};
-}
+
+}  // namespace
+
+Split split_product(int64_t m, int64_t n, int64_t k) { return cheapest(kProductTiles, m, n, mx4_groups(k)); }
+Split split_grad(int64_t rows, int64_t cols, int64_t depth) { return cheapest(kGradTiles, rows, cols, (depth + 63) / 64); }
 
 }  // namespace lql
 
