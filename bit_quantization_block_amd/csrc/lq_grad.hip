@@ -451,10 +451,9 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
 // dy with rows of a multiple of 64 elements, zeros past n.
 __global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* dy, int64_t m, int64_t n, int64_t ld, uint16_t* out,
                                                   int64_t ldo) {
-  const int64_t across = (ldo + 511) / 512;
-  for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < m * across; u += (int64_t)gridDim.x * 4) {
-    const int64_t row = u / across, col = u % across * 512 + (threadIdx.x & 63) * 8;
-    if (col >= ldo) continue;
+  const int64_t col = (int64_t)blockIdx.x * 512 + (threadIdx.x & 63) * 8;
+  if (col >= ldo) return;
+  for (int64_t row = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); row < m; row += (int64_t)gridDim.y * 4) {
     uint16_t v[8];
     const uint16_t* p = dy + row * ld + col;
     if (n - col >= 8) {
@@ -484,7 +483,7 @@ hipError_t grad(GradArgs g, void* ws, hipStream_t s) {
   uint8_t* planes = (uint8_t*)ws;
   if (needs_padding(g.n, g.lddy)) {
     const int64_t ld = padded_columns(g.n);
-    hipLaunchKernelGGL(k_pad_rows, dim3(stream_grid(g.m * ((ld + 511) / 512))), dim3(256), 0, s, g.dy, g.m, g.n, g.lddy, (uint16_t*)ws, ld);
+    hipLaunchKernelGGL(k_pad_rows, matrix_grid((ld + 511) / 512, g.m), dim3(256), 0, s, g.dy, g.m, g.n, g.lddy, (uint16_t*)ws, ld);
     if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
     g.dy = (const uint16_t*)ws;
     g.lddy = g.row = ld;

@@ -64,23 +64,34 @@ __device__ __forceinline__ typename El<DT>::T narrow(float f) {
   else return __builtin_bit_cast(uint16_t, (_Float16)f);
 }
 
-// Eight consecutive elements of a row, the first `valid` of which exist; the
-// rest are zero. Rows need not start at a multiple of 16 bytes (the caller's
-// row stride is any number of elements): the vector loads carry the element's
-// alignment, which gfx950's global memory instructions take as they are.
+// Eight consecutive elements of a row as they are stored, the first `valid` of
+// which exist; the rest are zero. Rows need not start at a multiple of 16 bytes
+// (the caller's row stride is any number of elements): the vector loads carry
+// the element's alignment, which gfx950's global memory instructions take as
+// they are.
 template <int DT>
-__device__ __forceinline__ void load8(const void* row, int64_t col, int valid, float v[8]) {
+struct Raw8 { typename El<DT>::T t[8]; };
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_raw8(const void* row, int64_t col, int valid) {
   typedef typename El<DT>::T T;
   const T* p = (const T*)row + col;
-  T t[8];
+  Raw8<DT> r;
   if (valid >= 8) {
-    __builtin_memcpy(t, p, sizeof(t));
+    __builtin_memcpy(r.t, p, sizeof(r.t));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; i++) t[i] = i < valid ? p[i] : (T)0;
+    for (int i = 0; i < 8; i++) r.t[i] = i < valid ? p[i] : (T)0;
   }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw8<DT>& r, float v[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = widen<DT>(t[i]);
+  for (int i = 0; i < 8; i++) v[i] = widen<DT>(r.t[i]);
+}
+template <int DT>
+__device__ __forceinline__ void load8(const void* row, int64_t col, int valid, float v[8]) {
+  widen8<DT>(load_raw8<DT>(row, col, valid), v);
 }
 template <int DT>
 __device__ __forceinline__ void store8(void* row, int64_t col, int valid, const float v[8]) {
@@ -132,14 +143,28 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);
   return v > o ? v : o;
 }
-__device__ __forceinline__ uint32_t amax8_bits(const float v[8]) {
-  uint32_t a = 0;
+// The bits of max|v| as binary32, of eight elements: magnitudes order like their
+// bits, also where a comparison of the values would lose a NaN; 16-bit ones two
+// at a time.
+typedef uint16_t v2u16 __attribute__((ext_vector_type(2)));
+template <int DT>
+__device__ __forceinline__ uint32_t amax8_bits(const Raw8<DT>& r) {
+  if constexpr (DT == LQ_F32) {
+    uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-    a = a > b ? a : b;
+    for (int i = 0; i < 8; i++) {
+      const uint32_t b = __float_as_uint(r.t[i]) & 0x7FFFFFFFu;
+      a = a > b ? a : b;
+    }
+    return a;
+  } else {
+    uint32_t w[4];
+    __builtin_memcpy(w, r.t, 16);
+    v2u16 top = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; i++) top = __builtin_elementwise_max(top, __builtin_bit_cast(v2u16, w[i] & 0x7FFF7FFFu));
+    return __float_as_uint(widen<DT>(top[0] > top[1] ? top[0] : top[1]));
   }
-  return a;
 }
 
 // Eight elements of one block as codes; r the scale's reciprocal, 0 for the
@@ -155,11 +180,15 @@ template <int F>
 __device__ __forceinline__ uint2 encode8(const float v[8], float r) {
   uint2 w;
   if constexpr (F == LQ_INT8) {
+    // v r is exact and at most 127 in magnitude; adding 1.5 * 2^23 rounds it to
+    // an integer, half to even, whose low byte is the code
     uint32_t c[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) c[i] = (uint32_t)(int)__builtin_rintf(lqd::clampf(v[i] * r, -127.0f, 127.0f));
-    w.x = (c[0] & 0xFFu) | ((c[1] & 0xFFu) << 8) | ((c[2] & 0xFFu) << 16) | (c[3] << 24);
-    w.y = (c[4] & 0xFFu) | ((c[5] & 0xFFu) << 8) | ((c[6] & 0xFFu) << 16) | (c[7] << 24);
+    for (int i = 0; i < 8; i++) c[i] = __float_as_uint(__builtin_fmaf(v[i], r, 12582912.0f));
+    const uint32_t ab = __builtin_amdgcn_perm(c[1], c[0], 0x0C0C0400u), cd = __builtin_amdgcn_perm(c[3], c[2], 0x04000C0Cu);
+    const uint32_t ef = __builtin_amdgcn_perm(c[5], c[4], 0x0C0C0400u), gh = __builtin_amdgcn_perm(c[7], c[6], 0x04000C0Cu);
+    w.x = ab | cd;
+    w.y = ef | gh;
   } else {
     float q[8];
 #pragma unroll
@@ -183,12 +212,11 @@ __device__ __forceinline__ void decode4(uint32_t w, float s, float o[4]) {
   }
 }
 
-// Workgroups of four waves for `units` one-wave units of a streaming kernel;
-// beyond 2^20 the waves take several each (and the launch's thread count stays
-// within 32 bits).
-inline unsigned stream_grid(int64_t units) {
-  const int64_t wgs = (units + 3) / 4;
-  return (unsigned)(wgs < (1 << 20) ? wgs : (1 << 20));
+// A launch over a matrix: `across` workgroups in x, and in y one for each four
+// rows, each taking several beyond the grid's limit.
+inline dim3 matrix_grid(int64_t across, int64_t rows) {
+  const int64_t bands = (rows + 3) / 4;
+  return dim3((unsigned)across, (unsigned)(bands < 65535 ? bands : 65535));
 }
 
 // dy's rows are read 16 bytes at a time with 32-bit offsets within a tile: where

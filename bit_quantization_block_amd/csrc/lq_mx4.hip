@@ -11,22 +11,22 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 // ---------------------------------------------------------------- quantise
-// One wave per 4 rows x 128 columns; a lane holds 8 consecutive elements, so a
-// block of 32 is the four lanes of a quad, and the wave's codes are 256 bytes
-// in one stretch. One read of x gives the 4-bit operand and the 8-bit
-// checkpoint.
+// One wave per 4 rows x 128 columns, four side by side in a workgroup; a lane
+// holds 8 consecutive elements, so a block of 32 is the four lanes of a quad,
+// and the wave's codes are 256 bytes in one stretch. One read of x gives the
+// 4-bit operand and the 8-bit checkpoint.
 template <int DT, int F>
 __global__ __launch_bounds__(256) void k_mx4_quantize(const void* x, int64_t m, int64_t k, int64_t ldx,
                                                       uint8_t* codes, uint8_t* scales, uint8_t* ck, uint8_t* cks) {
-  const int64_t bands = (m + 3) / 4, units = bands * mx4_groups(k);
   const int lane = threadIdx.x & 63;
-  for (int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); unit < units; unit += (int64_t)gridDim.x * 4) {
-    const int64_t row = unit % bands * 4 + (lane >> 4), col = unit / bands * 128 + (lane & 15) * 8;
-    const int valid = row >= m || col >= k ? 0 : (k - col >= 8 ? 8 : (int)(k - col));
+  const int64_t col = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 128 + (lane & 15) * 8;
+  if (col / 128 >= mx4_groups(k)) return;
+  for (int64_t row = (int64_t)blockIdx.y * 4 + (lane >> 4); row < m; row += (int64_t)gridDim.y * 4) {
+    const int valid = col >= k ? 0 : (k - col >= 8 ? 8 : (int)(k - col));
+    const Raw8<DT> raw = load_raw8<DT>((const typename El<DT>::T*)x + row * ldx, col, valid);
+    const uint32_t amax = quad_max(amax8_bits<DT>(raw));
     float v[8];
-    load8<DT>((const typename El<DT>::T*)x + row * ldx, col, valid, v);
-    const uint32_t amax = quad_max(amax8_bits(v));
-    if (row >= m) continue;
+    widen8<DT>(raw, v);
     if (codes) {
       const uint32_t sb = scale_byte<LQ_E2M1>(amax);
       *(uint32_t*)(codes + mx4_code_at(m, row, col)) = encode_e2m1(v, scale_recip(sb));
@@ -517,7 +517,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64
 template <int DT>
 hipError_t quantize_dt(int format, const void* x, int64_t m, int64_t k, int64_t ldx, void* codes, void* scales,
                        void* ck, void* cks, hipStream_t s) {
-  const dim3 g(stream_grid((m + 3) / 4 * mx4_groups(k)));
+  const dim3 g = matrix_grid((mx4_groups(k) + 3) / 4, m);
   if (format == LQ_INT8)
     hipLaunchKernelGGL((k_mx4_quantize<DT, LQ_INT8>), g, dim3(256), 0, s, x, m, k, ldx, (uint8_t*)codes,
                        (uint8_t*)scales, (uint8_t*)ck, (uint8_t*)cks);
@@ -583,11 +583,10 @@ hipError_t product_dt(const void* a, const void* as, const void* w, const void* 
 // y = in, or zeros: what is left of a product over an empty contraction.
 template <typename T>
 __global__ __launch_bounds__(256) void k_constant(int64_t rows, int64_t cols, const T* in, T* y, int64_t ldy) {
-  const int64_t across = (cols + 255) / 256;
-  for (int64_t u = blockIdx.x; u < rows * across; u += gridDim.x) {
-    const int64_t row = u / across, col = u % across * 256 + threadIdx.x;
-    if (col < cols) y[row * ldy + col] = in ? in[row * ldy + col] : (T)0;
-  }
+  const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  if (col >= cols) return;
+  for (int64_t row = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); row < rows; row += (int64_t)gridDim.y * 4)
+    y[row * ldy + col] = in ? in[row * ldy + col] : (T)0;
 }
 
 // y = in + the planes' sum, in the planes' order: four columns a lane, a wave's
@@ -596,11 +595,9 @@ template <int OUT>
 __global__ __launch_bounds__(256) void k_join(int64_t rows, int64_t cols, int parts, const float* planes,
                                               const float* in, void* y, int64_t ldy) {
   const int64_t stride = plane_stride(cols), plane = rows * stride;
-  const uint32_t across = (uint32_t)((cols + 255) / 256);
-  const int64_t units = rows * across;
-  for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < units; u += (int64_t)gridDim.x * 4) {
-    const int64_t row = u / across, col = u % across * 256 + (threadIdx.x & 63) * 4;
-    if (col >= cols) continue;
+  const int64_t col = (int64_t)blockIdx.x * 256 + (threadIdx.x & 63) * 4;
+  if (col >= cols) return;
+  for (int64_t row = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); row < rows; row += (int64_t)gridDim.y * 4) {
     const float* p = planes + row * stride + col;
     float4 s = *(const float4*)p;
 #pragma unroll 4
@@ -630,7 +627,7 @@ __global__ __launch_bounds__(256) void k_join(int64_t rows, int64_t cols, int pa
 
 hipError_t launch_join(int64_t rows, int64_t cols, int dtype, int parts, const float* planes, const float* in, void* y,
                        int64_t ldy, hipStream_t s) {
-  const dim3 g(stream_grid(rows * ((cols + 255) / 256)));
+  const dim3 g = matrix_grid((cols + 255) / 256, rows);
   if (dtype == LQ_F32) hipLaunchKernelGGL((k_join<LQ_F32>), g, dim3(256), 0, s, rows, cols, parts, planes, in, y, ldy);
   else if (dtype == LQ_BF16) hipLaunchKernelGGL((k_join<LQ_BF16>), g, dim3(256), 0, s, rows, cols, parts, planes, in, y, ldy);
   else hipLaunchKernelGGL((k_join<LQ_F16>), g, dim3(256), 0, s, rows, cols, parts, planes, in, y, ldy);
@@ -638,7 +635,7 @@ hipError_t launch_join(int64_t rows, int64_t cols, int dtype, int parts, const f
 }
 
 hipError_t launch_constant(int64_t rows, int64_t cols, int dtype, const void* in, void* y, int64_t ldy, hipStream_t s) {
-  const dim3 g(stream_grid(rows * ((cols + 255) / 256)));
+  const dim3 g = matrix_grid((cols + 63) / 64, rows);
   if (dtype == LQ_F32)
     hipLaunchKernelGGL((k_constant<float>), g, dim3(256), 0, s, rows, cols, (const float*)in, (float*)y, ldy);
   else

@@ -5,52 +5,60 @@
 namespace lql {
 namespace {
 
-// 1 / (1 + exp(-g)) in binary32: exp's library function and an IEEE division,
-// so that binary32 outputs are good to a few units in the last place; an
-// exp that overflows gives 0.
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+// 1 / (1 + exp(-g)), in binary32. The kernels are bound by memory only if this
+// is short. For 16-bit matrices: exp(-g) = 2^t (1 + ln2 (-g log2(e) - t)) with t
+// the rounded product, whose remainder is exact by fused multiply-adds over
+// log2(e) in two parts; v_exp_f32 and v_rcp_f32 are good to a unit in the last
+// place, so the whole is within 2^-21 relative, far below the result's rounding.
+// For 32-bit matrices: exp's library function and an IEEE division. An exp that
+// overflows gives 0.
+template <int DT>
+__device__ __forceinline__ float sigmoid(float g) {
+  if constexpr (DT == LQ_F32) return 1.0f / (1.0f + expf(-g));
+  constexpr float hi = -1.4426950216293335f, lo = -1.925963e-08f, ln2 = 0.6931471805599453f;
+  const float t = g * hi, rest = __builtin_fmaf(g, lo, __builtin_fmaf(g, hi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  // (an infinite g has no remainder, and neither have an exp of 0 or infinity)
+  const float fine = __builtin_fabsf(t) < 128.0f ? __builtin_fmaf(e * ln2, rest, e) : e;
+  // (1 + exp)/4 keeps the reciprocal, which has no subnormal numbers, a normal one
+  return 0.25f * __builtin_amdgcn_rcpf(__builtin_fmaf(fine, 0.25f, 0.25f));
+}
 
-template <int F>
-__device__ __forceinline__ void keep(const float v[8], uint8_t* codes, uint8_t* scales, int64_t row, int64_t col,
-                                     int64_t cols, int lane) {
-  const uint32_t sb = scale_byte<F>(quad_max(amax8_bits(v)));
+template <int DT, int F>
+__device__ __forceinline__ void keep(const Raw8<DT>& raw, const float v[8], uint8_t* codes, uint8_t* scales, int64_t row,
+                                     int64_t col, int64_t cols, int lane) {
+  const uint32_t sb = scale_byte<F>(quad_max(amax8_bits<DT>(raw)));
   const uint2 w = encode8<F>(v, scale_recip(sb));
   if (col < ckpt_pitch(cols)) {
     *(uint2*)(codes + row * ckpt_pitch(cols) + col) = w;
     if ((lane & 3) == 0) scales[row * ckpt_scale_pitch(cols) + col / 32] = (uint8_t)sb;
   }
 }
-template <int F>
-__device__ __forceinline__ void recall(float v[8], const uint8_t* codes, const uint8_t* scales, int64_t row,
-                                       int64_t col, int64_t cols) {
-  const uint2 w = *(const uint2*)(codes + row * ckpt_pitch(cols) + col);
-  const float s = scale_value(scales[row * ckpt_scale_pitch(cols) + col / 32]);
-  decode4<F>(w.x, s, v);
-  decode4<F>(w.y, s, v + 4);
-}
 
-// One wave per 512 columns of a row, 8 consecutive elements per lane.
+// One wave per 512 columns of a row, 8 consecutive elements per lane, four rows
+// a workgroup.
 template <int DT, int F>
 __global__ __launch_bounds__(256) void k_swiglu(const void* gate, const void* up, int64_t rows, int64_t cols,
                                                 int64_t ld, void* h, int64_t ldh, uint8_t* gc, uint8_t* gs,
                                                 uint8_t* uc, uint8_t* us) {
   typedef typename El<DT>::T T;
-  const int64_t segs = (cols + 511) / 512;
-  for (int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); unit < rows * segs; unit += (int64_t)gridDim.x * 4) {
-  const int64_t row = unit / segs;
   const int lane = threadIdx.x & 63;
-  const int64_t col = (unit % segs) * 512 + lane * 8;
+  const int64_t col = (int64_t)blockIdx.x * 512 + lane * 8;
   const int valid = col >= cols ? 0 : (cols - col >= 8 ? 8 : (int)(cols - col));
-  float g[8], u[8];
-  load8<DT>((const T*)gate + row * ld, col, valid, g);
-  load8<DT>((const T*)up + row * ld, col, valid, u);
-  if (gc) keep<F>(g, gc, gs, row, col, cols, lane);
-  if (uc) keep<F>(u, uc, us, row, col, cols, lane);
-  if (h) {
+  for (int64_t row = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); row < rows; row += (int64_t)gridDim.y * 4) {
+    const Raw8<DT> rg = load_raw8<DT>((const T*)gate + row * ld, col, valid), ru = load_raw8<DT>((const T*)up + row * ld, col, valid);
+    float g[8], u[8];
+    widen8<DT>(rg, g);
+    widen8<DT>(ru, u);
+    if (gc) {
+      keep<DT, F>(rg, g, gc, gs, row, col, cols, lane);
+      keep<DT, F>(ru, u, uc, us, row, col, cols, lane);
+    }
+    if (h) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) g[i] = g[i] * sigmoid(g[i]) * u[i];
-    store8<DT>((T*)h + row * ldh, col, valid, g);
-  }
+      for (int i = 0; i < 8; i++) g[i] = g[i] * sigmoid<DT>(g[i]) * u[i];
+      store8<DT>((T*)h + row * ldh, col, valid, g);
+    }
   }
 }
 
@@ -59,31 +67,34 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(const void* dh, int64_t
                                                          const uint8_t* gc, const uint8_t* gs, const uint8_t* uc,
                                                          const uint8_t* us, void* dgate, void* dup, int64_t ld) {
   typedef typename El<DT>::T T;
-  const int64_t segs = (cols + 511) / 512;
-  for (int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); unit < rows * segs; unit += (int64_t)gridDim.x * 4) {
-  const int64_t row = unit / segs;
-  const int64_t col = (unit % segs) * 512 + (threadIdx.x & 63) * 8;
-  if (col >= cols) continue;
+  const int64_t col = (int64_t)blockIdx.x * 512 + (threadIdx.x & 63) * 8;
+  if (col >= cols) return;
   const int valid = cols - col >= 8 ? 8 : (int)(cols - col);
-  float d[8], g[8], u[8];
-  load8<DT>((const T*)dh + row * lddh, col, valid, d);
-  recall<F>(g, gc, gs, row, col, cols);
-  recall<F>(u, uc, us, row, col, cols);
+  for (int64_t row = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); row < rows; row += (int64_t)gridDim.y * 4) {
+    const int64_t code = row * ckpt_pitch(cols) + col, scale = row * ckpt_scale_pitch(cols) + col / 32;
+    const uint2 wg = *(const uint2*)(gc + code), wu = *(const uint2*)(uc + code);
+    const float sg = scale_value(gs[scale]), su = scale_value(us[scale]);
+    float d[8], g[8], u[8];
+    load8<DT>((const T*)dh + row * lddh, col, valid, d);
+    decode4<F>(wg.x, sg, g);
+    decode4<F>(wg.y, sg, g + 4);
+    decode4<F>(wu.x, su, u);
+    decode4<F>(wu.y, su, u + 4);
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const float s = sigmoid(g[i]);
-    u[i] = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
-    g[i] = d[i] * (g[i] * s);
-  }
-  store8<DT>((T*)dgate + row * ld, col, valid, u);
-  store8<DT>((T*)dup + row * ld, col, valid, g);
+    for (int i = 0; i < 8; i++) {
+      const float s = sigmoid<DT>(g[i]);
+      u[i] = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+      g[i] = d[i] * (g[i] * s);
+    }
+    store8<DT>((T*)dgate + row * ld, col, valid, u);
+    store8<DT>((T*)dup + row * ld, col, valid, g);
   }
 }
 
 template <int DT, int F>
 hipError_t forward_dt(const void* gate, const void* up, int64_t rows, int64_t cols, int64_t ld, void* h, int64_t ldh,
                       void* gc, void* gs, void* uc, void* us, hipStream_t s) {
-  const dim3 grid(stream_grid(rows * ((cols + 511) / 512)));
+  const dim3 grid = matrix_grid((cols + 511) / 512, rows);
   hipLaunchKernelGGL((k_swiglu<DT, F>), grid, dim3(256), 0, s, gate, up, rows, cols, ld, h, ldh, (uint8_t*)gc,
                      (uint8_t*)gs, (uint8_t*)uc, (uint8_t*)us);
   return hipGetLastError();
@@ -91,7 +102,7 @@ hipError_t forward_dt(const void* gate, const void* up, int64_t rows, int64_t co
 template <int DT, int F>
 hipError_t backward_dt(const void* dh, int64_t rows, int64_t cols, int64_t lddh, const void* gc, const void* gs,
                        const void* uc, const void* us, void* dgate, void* dup, int64_t ld, hipStream_t s) {
-  const dim3 grid(stream_grid(rows * ((cols + 511) / 512)));
+  const dim3 grid = matrix_grid((cols + 511) / 512, rows);
   hipLaunchKernelGGL((k_swiglu_backward<DT, F>), grid, dim3(256), 0, s, dh, rows, cols, lddh, (const uint8_t*)gc,
                      (const uint8_t*)gs, (const uint8_t*)uc, (const uint8_t*)us, dgate, dup, ld);
   return hipGetLastError();
