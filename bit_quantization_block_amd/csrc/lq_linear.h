@@ -93,6 +93,11 @@ template <int DT>
 __device__ __forceinline__ void load8(const void* row, int64_t col, int valid, float v[8]) {
   widen8<DT>(load_raw8<DT>(row, col, valid), v);
 }
+// Eight results of a streaming kernel. 16-bit ones go past the caches, a wave's
+// store covering whole lines: 8192 x 11008 bf16 gated units take 123 instead of
+// 141 us forward and 121 instead of 150 backward, and 185 instead of 192 with the
+// quantiser that reads the result next. 32-bit ones take two stores a lane that
+// each cover half of every line, and are 8% slower that way.
 template <int DT>
 __device__ __forceinline__ void store8(void* row, int64_t col, int valid, const float v[8]) {
   typedef typename El<DT>::T T;
@@ -101,7 +106,14 @@ __device__ __forceinline__ void store8(void* row, int64_t col, int valid, const 
 #pragma unroll
   for (int i = 0; i < 8; i++) t[i] = narrow<DT>(v[i]);
   if (valid >= 8) {
-    __builtin_memcpy(p, t, sizeof(t));
+    if constexpr (sizeof(T) == 2) {
+      typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
+      v4 w;
+      __builtin_memcpy(&w, t, sizeof(t));
+      __builtin_nontemporal_store(w, (v4*)p);
+    } else {
+      __builtin_memcpy(p, t, sizeof(t));
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; i++)
