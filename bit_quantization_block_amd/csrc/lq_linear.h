@@ -256,7 +256,7 @@ inline int compute_units() {
 // `parts` runs of `part` steps, whose sums are added up afterwards.
 struct Split { int tile, parts, part; };
 Split split_product(int64_t m, int64_t n, int64_t k);              // steps of 128
-Split split_grad(int64_t rows, int64_t cols, int64_t depth);       // steps of 64
+Split split_dgrad(int64_t m, int64_t n, int64_t k), split_wgrad(int64_t m, int64_t n, int64_t k);   // steps of 64
 // Workspace of the parts' sums: planes with rows of a multiple of 4 values.
 __host__ __device__ inline int64_t plane_stride(int64_t cols) { return (cols + 3) / 4 * 4; }
 inline size_t planes_bytes(const Split& c, int64_t rows, int64_t cols) {

@@ -57,9 +57,13 @@ struct TileCost { int tile, most; double fixed, alone, full[4]; };
 constexpr TileCost kProductTiles[] = {{1, 3, 3.0, 0.18, {0, 0.20, 0.34, 0.50}},
                                       {2, 2, 3.5, 0.22, {0, 0.38, 0.62}},
                                       {4, 1, 6.0, 0.55, {0, 0.95}}};
-// (128: 2048 x 4096 x 4096 64 us in one part, with 256 76 us in two; 256: 8192
-// x 11008 x 4096 634 us)
-constexpr TileCost kGradTiles[] = {{2, 2, 4.0, 0.50, {0, 0.62, 1.02}}, {4, 1, 9.0, 1.25, {0, 1.70}}};
+// (dx, 128: 64 x 4096 x 4096 32 us in one part, 16.5 in eight, 2048 x 4096 x
+// 4096 68 us; 256: 83 us for the latter, 8192 x 11008 x 4096 549 us. dw, whose
+// tile has four bytes an element to write: 128: 4096 x 512 x 512 41 us in one
+// part, 17 in eight, 2000 x 3000 x 1500 38 us; 256: 58 us for the latter, 8192 x
+// 11008 x 4096 700 us)
+constexpr TileCost kDgradTiles[] = {{2, 2, 5.0, 0.43, {0, 0.59, 0.99}}, {4, 1, 9.0, 1.06, {0, 1.54}}};
+constexpr TileCost kWgradTiles[] = {{2, 2, 6.0, 0.56, {0, 0.70, 1.17}}, {4, 1, 14.5, 1.27, {0, 1.71}}};
 
 // The tile and the number of parts that the figures above say is fastest. Few
 // tiles over a long contraction gain from parts (512 x 1024 outputs over 16384:
@@ -103,7 +107,8 @@ Split cheapest(const TileCost (&tiles)[N], int64_t rows, int64_t cols, int64_t s
 }  // namespace
 
 Split split_product(int64_t m, int64_t n, int64_t k) { return cheapest(kProductTiles, m, n, mx4_groups(k)); }
-Split split_grad(int64_t rows, int64_t cols, int64_t depth) { return cheapest(kGradTiles, rows, cols, (depth + 63) / 64); }
+Split split_dgrad(int64_t m, int64_t n, int64_t k) { return cheapest(kDgradTiles, m, k, (n + 63) / 64); }
+Split split_wgrad(int64_t m, int64_t n, int64_t k) { return cheapest(kWgradTiles, n, k, (m + 63) / 64); }
 
 }  // namespace lql
 
@@ -128,7 +133,7 @@ size_t lq_linear_workspace_bytes(const lq_linear_desc* d) {
   // call's padded dy and its parts' sums
   const size_t forward = operand_bytes(d) + planes_bytes(split_product(d->m, d->n, d->k), d->m, d->n);
   const size_t dy = needs_padding(d->n, d->ld_in) ? round256((size_t)(d->m * padded_columns(d->n)) * 2) : 0;
-  const size_t dx = planes_bytes(split_grad(d->m, d->k, d->n), d->m, d->k), dw = planes_bytes(split_grad(d->n, d->k, d->m), d->n, d->k);
+  const size_t dx = planes_bytes(split_dgrad(d->m, d->n, d->k), d->m, d->k), dw = planes_bytes(split_wgrad(d->m, d->n, d->k), d->n, d->k);
   const size_t backward = dy + (dx > dw ? dx : dw), b = forward > backward ? forward : backward;
   return b ? b : 256;
 }
