@@ -416,15 +416,21 @@ class Mx4Linear:
         u8 = dict(dtype=torch.uint8, device=w.device)
         self.codes = torch.empty(max(16, self.lib.lq_mx4_codes_bytes(self.n, self.k)), **u8)
         self.scales = torch.empty(max(16, self.lib.lq_mx4_scales_bytes(self.n, self.k)), **u8)
-        ld = _matrix(w, self.n, self.k, w.dtype, "w")
-        d = LinearDesc(DTYPE[_dtype_name(w)], 0, 0, 0, self.n, 0, self.k, ld, 0)
-        _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(w), _ptr(self.codes),
-                                                           _ptr(self.scales), None, None, _stream(None)))
+        self.load(w)
         self._wc, self._ws = ctypes.c_void_p(self.codes.data_ptr()), ctypes.c_void_p(self.scales.data_ptr())
         self._index = w.device.index
         self._plans = {}
         self._buffers = {}
         self._workspaces = []
+
+    def load(self, w, stream=None):
+        """Quantises w into the layer: its weights from the next call on, as after an optimizer's step."""
+        ld = _matrix(w, self.n, self.k, w.dtype, "w")
+        if w.device != self.device:
+            raise ValueError(f"w is on {w.device}, the layer on {self.device}")
+        d = LinearDesc(DTYPE[_dtype_name(w)], 0, 0, 0, self.n, 0, self.k, ld, 0)
+        _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(w), _ptr(self.codes),
+                                                           _ptr(self.scales), None, None, _stream(stream)))
 
     def _workspace(self, need):
         """One of at least this size. Smaller ones stay alive: a captured graph may hold their addresses."""
@@ -438,6 +444,9 @@ class Mx4Linear:
         if m > self.rows:
             raise ValueError(f"{m} rows in a layer planned for {self.rows}")
         ld_in = _matrix(a, m, cols_in, _torch_dtype(in_dtype), what)
+        for t in (a, out):
+            if t is not None and t.device != self.device:
+                raise ValueError(f"a tensor is on {t.device}, the layer on {self.device}")
         rows_out = self.n if kind == "dw" else m
         if out is not None:
             buffer, ld_out = None, _matrix(out, rows_out, cols_out, _torch_dtype(out_dtype), "out")
