@@ -94,7 +94,7 @@ __device__ __forceinline__ int widen_int8(uint32_t w, int first, float s, float 
 struct GradArgs {
   const uint16_t* dy;
   int64_t m, n, k, lddy;
-  int64_t row;             // elements of a row of dy that may be read: n, or n padded; a multiple of 8
+  int64_t row;             // elements of a row of dy that may be read: n, or n padded
   const uint8_t *b, *bs;   // W's codes and scales, or the checkpoint's
   const float* in;         // dw_in
   void* out;
@@ -103,8 +103,9 @@ struct GradArgs {
   int parts, part;         // of the contraction: steps of each; with parts > 1, out is `parts` planes
 };
 
-// F: the checkpoint's format (wgrad); OUT: the result's type.
-template <int KIND, int F, int OUT, int FM, int FN>
+// F: the checkpoint's format (wgrad); OUT: the result's type; RAGGED (dgrad): dy's
+// rows end inside a unit of 8 elements, of whose last the rest is cut off.
+template <int KIND, int F, int OUT, int FM, int FN, bool RAGGED>
 __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradArgs g) {
   typedef typename El<OUT>::T T;
   typedef GradLds<KIND, FM, FN> Lds;
@@ -154,8 +155,8 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
   constexpr int kPieces = KIND == kDgrad ? FN / 2 : 1;   // groups of W, or the checkpoint
   const int64_t pitch = ckpt_pitch(g.k), spitch = ckpt_scale_pitch(g.k);
   const int64_t start = (int64_t)begin * kStep, end = (int64_t)steps * kStep < depth ? (int64_t)steps * kStep : depth;
-  // dgrad: dy's stretch moves along the rows and keeps its length; columns past the end are sent out of it one by
-  // one. W's groups lie still, and the step's place in them moves.
+  // dgrad: dy's stretch moves along the rows, and its end stays where it is; units past the rows' end are sent out of
+  // it one by one. W's groups lie still, and the step's place in them moves.
   const int columns_end = steps == all ? (int)g.row : steps * kStep;
   uint32_t wstep = (uint32_t)start * 64, wsstep = (uint32_t)start * 4;
   // wgrad: all three move down the rows, 64 at a time, the part's last step with what is left
@@ -163,11 +164,14 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
   const uint8_t *pa8 = (const uint8_t*)(KIND == kDgrad ? g.dy + row0 * g.lddy + start : g.dy + start * g.lddy + row0);
   const uint8_t *pc8 = g.b + start * pitch + col0, *ps8 = g.bs + start * spitch + col0 / 32;
   const int64_t tail = end - start - (to_come - 1) * (int64_t)kStep;   // rows of the last step
-  auto size_a = [&](int64_t rows_left) { return (uint32_t)(((rows_left - 1) * g.lddy + g.row - row0) * 2); };
+  // (a load's every 4 bytes have to end before the stretch does: of rows of odd length, 2 more are let in, which the
+  // rules of reads_in_place() keep inside the matrix or its last 4 bytes)
+  const int64_t row_bytes = (g.row + (g.row & 1)) * 2;
+  auto size_a = [&](int64_t rows_left) { return (uint32_t)((rows_left - 1) * g.lddy * 2 + row_bytes - row0 * 2); };   // (below 2^31)
   auto size_c = [&](int64_t rows_left) { return (uint32_t)(rows_left * pitch - col0); };
   auto size_s = [&](int64_t rows_left) { return (uint32_t)(rows_left * spitch - col0 / 32); };
   const uint32_t last_a = uniform(size_a(tail)), last_c = uniform(size_c(tail)), last_s = uniform(size_s(tail));
-  uint32_t bytes_a = uniform(KIND == kDgrad ? (uint32_t)(((left - 1) * g.lddy + g.row) * 2) : size_a(kStep));
+  uint32_t bytes_a = uniform(KIND == kDgrad ? (uint32_t)((left - 1) * g.lddy * 2 + row_bytes - start * 2) : size_a(kStep));
   uint32_t bytes_c = uniform(size_c(kStep)), bytes_s = uniform(size_s(kStep));
   const uint32_t move_a = uniform((uint32_t)(KIND == kDgrad ? kStep * 2 : kStep * 2 * g.lddy)), move_c = uniform((uint32_t)(kStep * pitch)), move_s = uniform((uint32_t)(kStep * spitch));
   __amdgpu_buffer_rsrc_t sa, sc[kPieces], ss[kPieces];
@@ -190,15 +194,32 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
       ps8 += move_s;
     }
     to_come--;
-    sa = stretch(pa8, bytes_a);
+    sa = stretch(pa8, (int)bytes_a);
     pa8 += move_a;
+    if (KIND == kDgrad) bytes_a -= move_a;
   };
   auto load_a = [&](int t, int set, int i) {
     uint32_t o = ao;
     if (KIND == kDgrad) o = t * kStep + (lane & 7) * 8 < columns_end ? o : 0xFFFFFFF0u;
     ra[set][i] = load16(sa, o, i * astep);
   };
-  auto put_a = [&](int st, int set, int i) { put16(aw[i % kPlacesA] + st * (place_t)sizeof(lds.a[0]) + i / kPlacesA * kPlacesA * awide, ra[set][i]); };
+  v4i keep, cut;   // RAGGED: of the lane's unit in the contraction's last step, and in the step that is put into LDS
+  if (RAGGED) {
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+      const int there = (int)g.n - (all - 1) * kStep - (lane & 7) * 8 - 2 * d;
+      keep[d] = there >= 2 ? -1 : there == 1 ? 0xFFFF : 0;
+    }
+  }
+  auto cut_for = [&](int t) {
+    if (RAGGED) {
+#pragma unroll
+      for (int d = 0; d < 4; d++) cut[d] = t == all - 1 ? keep[d] : -1;
+    }
+  };
+  auto put_a = [&](int st, int set, int i) {
+    put16(aw[i % kPlacesA] + st * (place_t)sizeof(lds.a[0]) + i / kPlacesA * kPlacesA * awide, RAGGED ? ra[set][i] & cut : ra[set][i]);
+  };
 
   // ---- B: dgrad: 32 codes of a row of W (one block); wgrad: 16 codes of a row of x8 (half a block)
   constexpr int kLoadsB = KIND == kDgrad ? FN / 2 : FN;
@@ -333,6 +354,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
   };
   load(begin, 0);
   load(begin + 1, 1);
+  cut_for(begin);
 #pragma unroll
   for (int i = 0; i < kLoadsA; i++) put_a(0, 0, i);
 #pragma unroll
@@ -363,6 +385,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
       const int b0 = quarter * bit_third, bn = bits - b0 < bit_third ? bits - b0 : bit_third;
       spread(done, per, bn, [&](int f) { put_b(OTHER, OTHER, (b0 + f) / kBits, (b0 + f) % kBits); });
     };
+    cut_for(t + 1);
     multiply(P, [&](int done) {
       spread(done, window, FM + FN, [&](int f) { read(ST, 1, Q, f); });
       work(0, done);
@@ -466,10 +489,13 @@ __global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* dy, int64_t m,
 
 template <int KIND, int F, int OUT, int FM, int FN>
 hipError_t grad_tiled(GradArgs& g, hipStream_t s) {
+  constexpr bool kMayBe = KIND == kDgrad;
   const int64_t rows = KIND == kDgrad ? g.m : g.n;
   g.tm = (uint32_t)((rows + 64 * FM - 1) / (64 * FM));
   g.tn = (uint32_t)((g.k + 64 * FN - 1) / (64 * FN));
-  hipLaunchKernelGGL((k_grad<KIND, F, OUT, FM, FN>), dim3(g.tm * g.tn * g.parts), dim3(256), 0, s, g);
+  const dim3 grid(g.tm * g.tn * g.parts);
+  if (kMayBe && g.row % 8 != 0) hipLaunchKernelGGL((k_grad<KIND, F, OUT, FM, FN, kMayBe>), grid, dim3(256), 0, s, g);
+  else hipLaunchKernelGGL((k_grad<KIND, F, OUT, FM, FN, false>), grid, dim3(256), 0, s, g);
   return hipGetLastError();
 }
 template <int KIND, int F, int OUT>
@@ -479,7 +505,7 @@ hipError_t grad_tile(int tile, GradArgs& g, hipStream_t s) {
 template <int KIND, int F, int OUT>
 hipError_t grad(GradArgs g, void* ws, hipStream_t s) {
   uint8_t* planes = (uint8_t*)ws;
-  if (needs_padding(g.n, g.lddy)) {
+  if (!reads_in_place(g.m, g.n, g.k, g.lddy)) {
     const int64_t ld = padded_columns(g.n);
     hipLaunchKernelGGL(k_pad_rows, matrix_grid((ld + 511) / 512, g.m), dim3(256), 0, s, g.dy, g.m, g.n, g.lddy, (uint16_t*)ws, ld);
     if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;

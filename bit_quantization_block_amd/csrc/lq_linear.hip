@@ -132,7 +132,7 @@ size_t lq_linear_workspace_bytes(const lq_linear_desc* d) {
   // the most of: the forward call's operand and its parts' sums; a gradient
   // call's padded dy and its parts' sums
   const size_t forward = operand_bytes(d) + planes_bytes(split_product(d->m, d->n, d->k), d->m, d->n);
-  const size_t dy = needs_padding(d->n, d->ld_in) ? round256((size_t)(d->m * padded_columns(d->n)) * 2) : 0;
+  const size_t dy = !reads_in_place(d->m, d->n, d->k, d->ld_in) ? round256((size_t)(d->m * padded_columns(d->n)) * 2) : 0;
   const size_t dx = planes_bytes(split_dgrad(d->m, d->n, d->k), d->m, d->k), dw = planes_bytes(split_wgrad(d->m, d->n, d->k), d->n, d->k);
   const size_t backward = dy + (dx > dw ? dx : dw), b = forward > backward ? forward : backward;
   return b ? b : 256;

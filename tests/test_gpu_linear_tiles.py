@@ -151,6 +151,29 @@ def test_activation_at_the_ends_of_its_range(dtype):
     assert (err <= bound[fin]).all()
 
 
+@pytest.mark.parametrize("m,n,k,ld", [(77, 1001, 520, 1002), (76, 1001, 520, 1001), (77, 1001, 520, 1001), (5, 9, 40, 12),
+                                      (64, 63, 33, 65), (130, 130, 70, 131), (3, 1, 1, 8), (1, 7, 64, 7), (2, 7, 64, 7),
+                                      (200, 36, 100, 36), (129, 44, 40, 64)])
+def test_nothing_around_dy_is_used(m, n, k, ld):
+    """Rows of dy that end inside 16 bytes, of any stride: NaN between the rows and after the last change no bit."""
+    say(f"[gpu] around dy {m}x{n}x{k} stride {ld}")
+    w = random(n, k, "bf16", 0, 1, 0.05)
+    layer = lq.Mx4Linear(w, rows=m, out="f32")
+    kept = lq.Ckpt8(m, k, "e4m3")
+    kept.save(random(m, k, "bf16", 0, 2))
+    values = random(m, n, "bf16", 0, 3)
+    got = []
+    for around in (0.0, float("nan")):
+        flat = torch.full((m * ld + 64,), around, dtype=torch.bfloat16, device="cuda")
+        dy = flat.as_strided((m, n), (ld, 1))
+        dy.copy_(values)
+        got.append((layer.dgrad(dy).clone(), layer.wgrad(dy, kept).clone()))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    w4, d, x8 = kept_values(w, "e2m1"), values.double(), kept_values(random(m, k, "bf16", 0, 2), "e4m3")
+    close(got[1][0], d @ w4, d.abs() @ w4.abs(), n, "f32", "dx")
+    close(got[1][1], d.t() @ x8, d.abs().t() @ x8.abs(), m, "f32", "dw")
+
+
 def example():
     path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "gated_mlp.py")
     spec = importlib.util.spec_from_file_location("gated_mlp", path)
