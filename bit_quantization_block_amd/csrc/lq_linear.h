@@ -93,11 +93,22 @@ template <int DT>
 __device__ __forceinline__ void load8(const void* row, int64_t col, int valid, float v[8]) {
   widen8<DT>(load_raw8<DT>(row, col, valid), v);
 }
-// Eight results of a streaming kernel. 16-bit ones go past the caches, a wave's
-// store covering whole lines: 8192 x 11008 bf16 gated units take 123 instead of
-// 141 us forward and 121 instead of 150 backward, and 185 instead of 192 with the
-// quantiser that reads the result next. 32-bit ones take two stores a lane that
-// each cover half of every line, and are 8% slower that way.
+// 16 bytes of a result, past the caches: what these kernels write is larger than
+// an L2, and lines that it would have to make room for and give back cost more
+// than they are worth to the next reader. 8192 x 11008 x 4096 forward 203 instead
+// of 224 us, 2548 x 16384 x 256 30 instead of 46; 154 x 11008 x 4096 added to dw
+// 72 instead of 92; the gated unit 123 instead of 141 forward, 121 instead of 150
+// backward. A gated MLP's forward of these kernels, each of which reads what the
+// last one wrote, takes 765 instead of 816 us at 8192 x 11008 x 4096, 134 instead
+// of 145 at 1024 rows, and 2 us of 31 more at 256 rows of 2048 x 1024.
+__device__ __forceinline__ void store16(void* p, const void* v) {
+  typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
+  v4 w;
+  __builtin_memcpy(&w, v, 16);
+  __builtin_nontemporal_store(w, (v4*)p);
+}
+// Eight results of a streaming kernel. (32-bit ones take two stores a lane that
+// each cover half of every line, and are 8% slower past the caches.)
 template <int DT>
 __device__ __forceinline__ void store8(void* row, int64_t col, int valid, const float v[8]) {
   typedef typename El<DT>::T T;
@@ -106,14 +117,8 @@ __device__ __forceinline__ void store8(void* row, int64_t col, int valid, const 
 #pragma unroll
   for (int i = 0; i < 8; i++) t[i] = narrow<DT>(v[i]);
   if (valid >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
-      v4 w;
-      __builtin_memcpy(&w, t, sizeof(t));
-      __builtin_nontemporal_store(w, (v4*)p);
-    } else {
-      __builtin_memcpy(p, t, sizeof(t));
-    }
+    if constexpr (sizeof(T) == 2) store16(p, t);
+    else __builtin_memcpy(p, t, sizeof(t));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; i++)
@@ -265,8 +270,8 @@ inline int compute_units() {
 // out: tiles of 64 tile x 64 tile, each of whose contraction is cut into
 // `parts` runs of `part` steps, whose sums are added up afterwards.
 struct Split { int tile, parts, part; };
-Split split_product(int64_t m, int64_t n, int64_t k);              // steps of 128
-Split split_dgrad(int64_t m, int64_t n, int64_t k), split_wgrad(int64_t m, int64_t n, int64_t k);   // steps of 64
+Split split_product(int64_t m, int64_t n, int64_t k, int out_dtype);                                     // steps of 128
+Split split_dgrad(int64_t m, int64_t n, int64_t k), split_wgrad(int64_t m, int64_t n, int64_t k, bool adds);   // steps of 64
 // Workspace of the parts' sums: planes with rows of a multiple of 4 values.
 __host__ __device__ inline int64_t plane_stride(int64_t cols) { return (cols + 3) / 4 * 4; }
 inline size_t planes_bytes(const Split& c, int64_t rows, int64_t cols) {

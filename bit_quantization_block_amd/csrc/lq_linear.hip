@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "lq_linear.h"
 
 using namespace lql;
@@ -50,27 +52,29 @@ namespace {
 
 // What a tile of a product costs, in microseconds: a fixed part, and a step of
 // its contraction with almost no other workgroup running, with one on each of
-// 256 compute units, and with more of them on each.
-struct TileCost { int tile, most; double fixed, alone, full[4]; };
+// 256 compute units, and with more of them on each. Results of 16 bits of a
+// product and of 32 bits of a gradient are in the fixed part; the further bytes of
+// a 32-bit product, or of what dw is added to, pass at `rate` TB/s.
+struct TileCost { int tile, most; double fixed, alone, full[4], rate; };
 // (64: 11008 x 4096 times 64 rows 9.5 us in one part, 14.6 in two; 128: 2048 x
 // 4096 x 4096 23.2 us, with 256 30.0; 256: 8192 x 8192 x 8192 262 us)
-constexpr TileCost kProductTiles[] = {{1, 3, 3.0, 0.18, {0, 0.20, 0.34, 0.50}},
-                                      {2, 2, 3.5, 0.22, {0, 0.38, 0.62}},
-                                      {4, 1, 6.0, 0.55, {0, 0.95}}};
+constexpr TileCost kProductTiles[] = {{1, 3, 3.0, 0.18, {0, 0.20, 0.34, 0.50}, 2.5},
+                                      {2, 2, 3.5, 0.22, {0, 0.38, 0.62}, 2.5},
+                                      {4, 1, 6.0, 0.55, {0, 0.95}, 5.0}};
 // (dx, 128: 64 x 4096 x 4096 32 us in one part, 16.5 in eight, 2048 x 4096 x
 // 4096 68 us; 256: 83 us for the latter, 8192 x 11008 x 4096 549 us. dw, whose
 // tile has four bytes an element to write: 128: 4096 x 512 x 512 41 us in one
 // part, 17 in eight, 2000 x 3000 x 1500 38 us; 256: 58 us for the latter, 8192 x
 // 11008 x 4096 700 us)
-constexpr TileCost kDgradTiles[] = {{2, 2, 5.0, 0.43, {0, 0.59, 0.99}}, {4, 1, 9.0, 1.06, {0, 1.54}}};
-constexpr TileCost kWgradTiles[] = {{2, 2, 6.0, 0.56, {0, 0.70, 1.17}}, {4, 1, 14.5, 1.27, {0, 1.71}}};
+constexpr TileCost kDgradTiles[] = {{2, 2, 5.0, 0.43, {0, 0.59, 0.99}, 0}, {4, 1, 9.0, 1.06, {0, 1.54}, 0}};
+constexpr TileCost kWgradTiles[] = {{2, 2, 6.0, 0.56, {0, 0.70, 1.17}, 8.0}, {4, 1, 14.5, 1.27, {0, 1.71}, 4.3}};
 
 // The tile and the number of parts that the figures above say is fastest. Few
 // tiles over a long contraction gain from parts (512 x 1024 outputs over 16384:
 // 130 us in one part, 32 in eight); adding the parts up costs a launch and their
 // sums' way through memory and back.
 template <size_t N>
-Split cheapest(const TileCost (&tiles)[N], int64_t rows, int64_t cols, int64_t steps) {
+Split cheapest(const TileCost (&tiles)[N], int64_t rows, int64_t cols, int64_t steps, double further) {
   const double cus = compute_units();
   Split best = {tiles[0].tile, 1, (int)steps};
   double least = 1e300;
@@ -94,7 +98,8 @@ Split cheapest(const TileCost (&tiles)[N], int64_t rows, int64_t cols, int64_t s
           left -= rounds * cus * each;
         }
       }
-      if (parts > 1) us += 2.5 + planes * 2 / 4.5e6;
+      if (parts > 1) us += 2.5 + (planes * 2 + further) / 4.5e6;
+      else if (further > 0) us += further / (c.rate * 1e6);
       if (us < least) {
         least = us;
         best = {c.tile, (int)parts, (int)part};
@@ -106,9 +111,13 @@ Split cheapest(const TileCost (&tiles)[N], int64_t rows, int64_t cols, int64_t s
 
 }  // namespace
 
-Split split_product(int64_t m, int64_t n, int64_t k) { return cheapest(kProductTiles, m, n, mx4_groups(k)); }
-Split split_dgrad(int64_t m, int64_t n, int64_t k) { return cheapest(kDgradTiles, m, k, (n + 63) / 64); }
-Split split_wgrad(int64_t m, int64_t n, int64_t k) { return cheapest(kWgradTiles, n, k, (m + 63) / 64); }
+Split split_product(int64_t m, int64_t n, int64_t k, int out_dtype) {
+  return cheapest(kProductTiles, m, n, mx4_groups(k), out_dtype == LQ_F32 ? (double)m * n * 2 : 0.0);
+}
+Split split_dgrad(int64_t m, int64_t n, int64_t k) { return cheapest(kDgradTiles, m, k, (n + 63) / 64, 0.0); }
+Split split_wgrad(int64_t m, int64_t n, int64_t k, bool adds) {
+  return cheapest(kWgradTiles, n, k, (m + 63) / 64, adds ? (double)n * k * 4 : 0.0);
+}
 
 }  // namespace lql
 
@@ -131,10 +140,12 @@ size_t lq_linear_workspace_bytes(const lq_linear_desc* d) {
   if (check_linear(d)) return 0;
   // the most of: the forward call's operand and its parts' sums; a gradient
   // call's padded dy and its parts' sums
-  const size_t forward = operand_bytes(d) + planes_bytes(split_product(d->m, d->n, d->k), d->m, d->n);
+  const size_t forward = operand_bytes(d) + planes_bytes(split_product(d->m, d->n, d->k, d->out_dtype), d->m, d->n);
   const size_t dy = !reads_in_place(d->m, d->n, d->k, d->ld_in) ? round256((size_t)(d->m * padded_columns(d->n)) * 2) : 0;
-  const size_t dx = planes_bytes(split_dgrad(d->m, d->n, d->k), d->m, d->k), dw = planes_bytes(split_wgrad(d->m, d->n, d->k), d->n, d->k);
-  const size_t backward = dy + (dx > dw ? dx : dw), b = forward > backward ? forward : backward;
+  const size_t dx = planes_bytes(split_dgrad(d->m, d->n, d->k), d->m, d->k);
+  const size_t dw0 = planes_bytes(split_wgrad(d->m, d->n, d->k, false), d->n, d->k);
+  const size_t dw1 = planes_bytes(split_wgrad(d->m, d->n, d->k, true), d->n, d->k);
+  const size_t backward = dy + std::max(dx, std::max(dw0, dw1)), b = std::max(forward, backward);
   return b ? b : 256;
 }
 

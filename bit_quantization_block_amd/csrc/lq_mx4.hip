@@ -341,7 +341,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
           if (i * 32 + g * rows < rows_left && c * CW < cols_left) {
             T* o = out + (int64_t)(i * 32 + g * rows) * ldy + c * CW;
             if (cols_left - c * CW >= V) {
-              __builtin_memcpy(o, v, 16);
+              store16(o, v);
             } else {
 #pragma unroll
               for (int e = 0; e < V; e++)
@@ -574,7 +574,7 @@ hipError_t product_dt(const void* a, const void* as, const void* w, const void* 
   if (k == 0) return launch_constant(m, n, OUT, nullptr, y, ldy, s);
   if (m <= 16) return few<kOperand, OUT, 1>(a, 0, as, w, ws, m, n, k, y, ldy, s);
   if (m <= 32) return few<kOperand, OUT, 2>(a, 0, as, w, ws, m, n, k, y, ldy, s);
-  const Split c = split_product(m, n, k);
+  const Split c = split_product(m, n, k, OUT);
   if (c.parts == 1) return product_tile<OUT>(c.tile, a, as, w, ws, m, n, k, 1, c.part, y, ldy, s);
   const hipError_t e = product_tile<LQ_F32>(c.tile, a, as, w, ws, m, n, k, c.parts, c.part, planes, plane_stride(n), s);
   return e != hipSuccess ? e : launch_join(m, n, OUT, c.parts, (const float*)planes, nullptr, y, ldy, s);
