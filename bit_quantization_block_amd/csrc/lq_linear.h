@@ -289,9 +289,15 @@ hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const v
                               int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, void* planes,
                               hipStream_t s);
 // The forward product of a few rows straight from x: at most kFewBlocks blocks
-// of it (padded to whole groups), which a workgroup quantises into its LDS.
-constexpr int64_t kFewRows = 16, kFewBlocks = 2048;
-inline bool few_rows(int64_t m, int64_t k) { return m <= kFewRows && m * mx4_groups(k) * 4 <= kFewBlocks; }
+// of it (padded to whole groups), which each workgroup, of 16 columns, quantises
+// into its LDS. With more than one workgroup on a compute unit that work counts
+// more than once, and a launch of its own for it is sooner worth it (in place, or
+// apart; 11008 x 4096: 10 rows 8.7 or 8.9 us, 12 rows 9.9 or 9.3; 4096 x 4096: 12
+// rows 6.0 or 8.0, 16 rows 7.0 or 7.6).
+constexpr int64_t kFewRows = 16, kFewBlocks = 2048, kFewBlocksWide = 1280;
+inline bool few_rows(int64_t m, int64_t n, int64_t k) {
+  return m <= kFewRows && m * mx4_groups(k) * 4 <= (n <= 16 * compute_units() ? kFewBlocks : kFewBlocksWide);
+}
 hipError_t launch_mx4_few(int in_dtype, const void* x, int64_t ldx, const void* w_codes, const void* w_scales, int64_t m,
                           int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s);
 hipError_t launch_mx4_dgrad(const void* dy, int64_t m, int64_t n, int64_t lddy, const void* w_codes,

@@ -187,7 +187,7 @@ int lq_mx4_linear(const lq_linear_desc* d, const void* x, const void* w_codes, c
                    (const void*)ws))
     return LQ_ERR_ALIGN;
   if (!ws || ws_bytes < lq_linear_workspace_bytes(d)) return LQ_ERR_WORKSPACE;
-  if (few_rows(d->m, d->k) && d->n > 0 && d->k > 0 && !ckpt_codes)
+  if (few_rows(d->m, d->n, d->k) && d->n > 0 && d->k > 0 && !ckpt_codes)
     return status_of(launch_mx4_few(d->in_dtype, x, d->ld_in, w_codes, w_scales, d->m, d->n, d->k, d->out_dtype, y,
                                     d->ld_out, (hipStream_t)stream));
   uint8_t *codes = (uint8_t*)ws, *scales = (uint8_t*)ws + operand_codes(d);
