@@ -289,12 +289,12 @@ hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const v
                               int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, void* planes,
                               hipStream_t s);
 // The forward product of a few rows straight from x: at most kFewBlocks blocks
-// of it (padded to whole groups), which each workgroup, of 16 columns, quantises
-// into its LDS. With more than one workgroup on a compute unit that work counts
-// more than once, and a launch of its own for it is sooner worth it (in place, or
-// apart; 11008 x 4096: 10 rows 8.7 or 8.9 us, 12 rows 9.9 or 9.3; 4096 x 4096: 12
-// rows 6.0 or 8.0, 16 rows 7.0 or 7.6).
-constexpr int64_t kFewRows = 16, kFewBlocks = 2048, kFewBlocksWide = 1280;
+// of it (padded to whole groups), which each workgroup, of 16 columns or more,
+// quantises into its LDS. With more than one workgroup on a compute unit that work
+// counts more than once, and a launch of its own for it is sooner worth it (in
+// place, or apart; 11008 x 4096: 8 rows 8.2 or 9.0 us, 12 rows 9.9 or 9.3; 4096 x
+// 4096: 12 rows 6.0 or 8.0, 16 rows 7.0 or 7.6).
+constexpr int64_t kFewRows = 16, kFewBlocks = 2048, kFewBlocksWide = 1024;
 inline bool few_rows(int64_t m, int64_t n, int64_t k) {
   return m <= kFewRows && m * mx4_groups(k) * 4 <= (n <= 16 * compute_units() ? kFewBlocks : kFewBlocksWide);
 }

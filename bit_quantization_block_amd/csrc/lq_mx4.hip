@@ -14,7 +14,8 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 // One wave per 4 rows x 128 columns, four side by side in a workgroup; a lane
 // holds 8 consecutive elements, so a block of 32 is the four lanes of a quad,
 // and the wave's codes are 256 bytes in one stretch. One read of x gives the
-// 4-bit operand and the 8-bit checkpoint.
+// 4-bit operand and the 8-bit checkpoint: bound by memory, 8192 x 4096 of bf16
+// 17 us (4.9 TB/s, a large copy's 5.1), with the checkpoint 20 us (5.9 TB/s).
 template <int DT, int F>
 __global__ __launch_bounds__(256) void k_mx4_quantize(const void* x, int64_t m, int64_t k, int64_t ldx,
                                                       uint8_t* codes, uint8_t* scales, uint8_t* ck, uint8_t* cks) {
@@ -53,6 +54,14 @@ __global__ __launch_bounds__(256) void k_mx4_quantize(const void* x, int64_t m, 
 // at a time into a ring of four stages, three of them in flight; the transfers
 // run on across the end of a tile, so the next tile starts with its first steps
 // in LDS, and a tile's results leave through a part of LDS of their own.
+//
+// 8192 x 4096 x 11008 163 us (4.5 PFLOP/s), 8192 x 8192 x 8192 271 us (4.1), 8192
+// x 11008 x 4096 185 to 203 us (3.6 to 4.0; 5.4 tiles a compute unit take 6 turns,
+// and each turn writes 32 MB). Power bounds the large ones: a loop of nothing but
+// these products on random operands reaches 5.8 PFLOP/s at 1.4 to 1.7 GHz, and
+// here, with the matrix cores busy half of the cycles, the clock is 1.9 of 2.4 GHz.
+// 256 x 256 tiles read each operand half as often as 128 x 128 ones; those, and 64
+// x 64, are for products of few tiles (2048 x 4096 x 4096: 23 us against 30).
 constexpr int kStages = 4;
 // A row's four 16-byte units are stored in the order u ^ (row / 4 & 3): the 16
 // lanes that the LDS serves at a time (0-3, 12-15, 20-27 and so on) then read
@@ -372,6 +381,9 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
 // a float type (up to kFewRows rows) every workgroup quantises x itself, a block
 // a thread, into LDS while its first reads of W are on their way: a launch of
 // its own for x would cost a quarter of the call. Otherwise x is an MX4 operand.
+//
+// 1 x 11008 x 4096 5.5 us (24 MB of W at 4.4 TB/s, the launch included), 1 x 16384
+// x 8192 13 us (5.4 TB/s), 16 x 4096 x 11008 9.1 us with x's own launch.
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint16_t v2u __attribute__((ext_vector_type(2)));
 constexpr int kOperand = -1;
@@ -542,7 +554,9 @@ hipError_t product_tiled(const void* a, const void* as, const void* w, const voi
 template <int SRC, int OUT, int CT>
 hipError_t few(const void* x, int64_t ldx, const void* xs, const void* w, const void* ws, int64_t m, int64_t n, int64_t k,
                void* y, int64_t ldy, hipStream_t s) {
-  if (n > 16 * 512) {
+  // 16 rows of W a workgroup while all of them run at once, three on a compute unit (1 x 8448 x 4096 4.9 or, with 32
+  // rows, 5.4 us; 1 x 11008 x 4096 5.5 or 5.7), 32 beyond (1 x 16384 x 8192 14.1 or 13.0 us, 4 x 16384 x 4096 9.1 or 7.4)
+  if (n > 16 * 3 * (int64_t)compute_units()) {
     hipLaunchKernelGGL((k_mx4_few<SRC, OUT, 2, CT>), dim3((unsigned)((n + 31) / 32)), dim3(64 * kFewWaves), 0, s, x, ldx,
                        (const uint8_t*)xs, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy);
   } else {
