@@ -382,8 +382,10 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
 // a thread, into LDS while its first reads of W are on their way: a launch of
 // its own for x would cost a quarter of the call. Otherwise x is an MX4 operand.
 //
-// 1 x 11008 x 4096 5.5 us (24 MB of W at 4.4 TB/s, the launch included), 1 x 16384
-// x 8192 13 us (5.4 TB/s), 16 x 4096 x 11008 9.1 us with x's own launch.
+// With W in memory, call after call in a graph: 1 x 4096 x 4096 4.9 us, 1 x 11008 x
+// 4096 7.7, 1 x 8192 x 8192 10.2: 3.2 us and W's bytes at 5.2 TB/s, the rate of a
+// large copy; the smallest call takes 2.55 us. Loads of twice as many groups in
+// flight cost the registers of a third of the waves: 8.6 instead of 7.7 us.
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint16_t v2u __attribute__((ext_vector_type(2)));
 constexpr int kOperand = -1;
@@ -554,9 +556,10 @@ hipError_t product_tiled(const void* a, const void* as, const void* w, const voi
 template <int SRC, int OUT, int CT>
 hipError_t few(const void* x, int64_t ldx, const void* xs, const void* w, const void* ws, int64_t m, int64_t n, int64_t k,
                void* y, int64_t ldy, hipStream_t s) {
-  // 16 rows of W a workgroup while all of them run at once, three on a compute unit (1 x 8448 x 4096 4.9 or, with 32
-  // rows, 5.4 us; 1 x 11008 x 4096 5.5 or 5.7), 32 beyond (1 x 16384 x 8192 14.1 or 13.0 us, 4 x 16384 x 4096 9.1 or 7.4)
-  if (n > 16 * 3 * (int64_t)compute_units()) {
+  // 32 rows of W a workgroup where that leaves one for each compute unit, else 16 (W read from memory, one call after
+  // another in a graph: 1 x 8192 x 8192 10.2 us, with 16 rows 10.8; 1 x 16384 x 4096 9.6 or 11.2; 8 x 11008 x 4096 10.5
+  // or 11.2; but 1 x 4096 x 11008 9.8 or 8.6)
+  if (n >= 32 * (int64_t)compute_units()) {
     hipLaunchKernelGGL((k_mx4_few<SRC, OUT, 2, CT>), dim3((unsigned)((n + 31) / 32)), dim3(64 * kFewWaves), 0, s, x, ldx,
                        (const uint8_t*)xs, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy);
   } else {
