@@ -391,19 +391,26 @@ typedef uint16_t v2u __attribute__((ext_vector_type(2)));
 constexpr int kOperand = -1;
 constexpr int kFewWaves = 8;
 
-// One block of x, `valid` of whose 32 elements exist: its codes and scale byte.
+// One block of x as it is stored, `valid` of whose 32 elements exist; its codes
+// and scale byte.
 template <int SRC>
-__device__ __forceinline__ v4i quantise_block(const typename El<SRC>::T* p, int valid, uint32_t& scale) {
-  float v[32];
+struct Block { typename El<SRC>::T t[32]; };
+template <int SRC>
+__device__ __forceinline__ Block<SRC> load_block(const typename El<SRC>::T* p, int valid) {
+  Block<SRC> b;
   if (valid >= 32) {
-    typename El<SRC>::T t[32];
-    __builtin_memcpy(t, p, sizeof(t));
-#pragma unroll
-    for (int i = 0; i < 32; i++) v[i] = widen<SRC>(t[i]);
+    __builtin_memcpy(b.t, p, sizeof(b.t));
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; i++) v[i] = i < valid ? widen<SRC>(p[i]) : 0.0f;
+    for (int i = 0; i < 32; i++) b.t[i] = i < valid ? p[i] : (typename El<SRC>::T)0;
   }
+  return b;
+}
+template <int SRC>
+__device__ __forceinline__ v4i quantise_block(const Block<SRC>& block, uint32_t& scale) {
+  float v[32];
+#pragma unroll
+  for (int i = 0; i < 32; i++) v[i] = widen<SRC>(block.t[i]);
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < 32; i++) {
@@ -462,17 +469,28 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64
     }
   };
   Reads a, b;
-  if (begin < end) load(a, begin);
   if constexpr (own) {
-    const int blocks = groups * 4;
-    for (int i = threadIdx.x; i < (int)m * blocks; i += 64 * kFewWaves) {
+    // loads return in the order they were asked for: a thread's first block of x, then W, whose way here hides the rest
+    const int blocks = groups * 4, all = (int)m * blocks;
+    auto block = [&](int i) {
       const int row = i / blocks, col = (i - row * blocks) * 32;
-      const int valid = k - col < 32 ? (int)(k - col) : 32;
+      return load_block<SRC>((const typename El<SRC>::T*)x + row * ldx + col, k - col < 32 ? (int)(k - col) : 32);
+    };
+    auto keep = [&](int i, const Block<SRC>& v) {
       uint32_t e;
-      xcodes[i] = quantise_block<SRC>((const typename El<SRC>::T*)x + row * ldx + col, valid, e);
+      xcodes[i] = quantise_block<SRC>(v, e);
       xscales[i] = (uint8_t)e;
-    }
+    };
+    int i = threadIdx.x;
+    Block<SRC> mine;
+    if (i < all) mine = block(i);
+    asm volatile("" ::: "memory");
+    if (begin < end) load(a, begin);
+    if (i < all) keep(i, mine);
+    for (i += 64 * kFewWaves; i < all; i += 64 * kFewWaves) keep(i, block(i));
     __syncthreads();
+  } else {
+    if (begin < end) load(a, begin);
   }
   v4f acc[R][CT];
 #pragma unroll
