@@ -382,10 +382,11 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
 // a thread, into LDS while its first reads of W are on their way: a launch of
 // its own for x would cost a quarter of the call. Otherwise x is an MX4 operand.
 //
-// With W in memory, call after call in a graph: 1 x 4096 x 4096 4.9 us, 1 x 11008 x
-// 4096 7.7, 1 x 8192 x 8192 10.2: 3.2 us and W's bytes at 5.2 TB/s, the rate of a
-// large copy; the smallest call takes 2.55 us. Loads of twice as many groups in
-// flight cost the registers of a third of the waves: 8.6 instead of 7.7 us.
+// With W in memory, call after call in a graph: 1 x 4096 x 4096 4.3 us, 1 x 11008 x
+// 4096 7.4, 1 x 8192 x 8192 9.9, 8 x 11008 x 4096 9.0: 2.6 us, which the smallest
+// call takes, and W's bytes at 5.1 TB/s, the rate of a large copy. Asked for after
+// W, x came behind all of it: 4.9, 7.7, 10.2 and 10.5 us. Loads of twice as many
+// groups in flight cost the registers of a third of the waves: 8.6 for the 7.7.
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint16_t v2u __attribute__((ext_vector_type(2)));
 constexpr int kOperand = -1;
@@ -470,7 +471,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64
   };
   Reads a, b;
   if constexpr (own) {
-    // loads return in the order they were asked for: a thread's first block of x, then W, whose way here hides the rest
+    // loads return in the order they were asked for: a thread's first two blocks of x, then W, whose way here hides the rest
     const int blocks = groups * 4, all = (int)m * blocks;
     auto block = [&](int i) {
       const int row = i / blocks, col = (i - row * blocks) * 32;
@@ -481,13 +482,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64
       xcodes[i] = quantise_block<SRC>(v, e);
       xscales[i] = (uint8_t)e;
     };
+    constexpr int kThreads = 64 * kFewWaves;
     int i = threadIdx.x;
-    Block<SRC> mine;
+    Block<SRC> mine, second;
     if (i < all) mine = block(i);
+    if (i + kThreads < all) second = block(i + kThreads);
     asm volatile("" ::: "memory");
     if (begin < end) load(a, begin);
     if (i < all) keep(i, mine);
-    for (i += 64 * kFewWaves; i < all; i += 64 * kFewWaves) keep(i, block(i));
+    if (i + kThreads < all) keep(i + kThreads, second);
+    for (i += 2 * kThreads; i < all; i += kThreads) keep(i, block(i));
     __syncthreads();
   } else {
     if (begin < end) load(a, begin);
@@ -575,8 +579,8 @@ template <int SRC, int OUT, int CT>
 hipError_t few(const void* x, int64_t ldx, const void* xs, const void* w, const void* ws, int64_t m, int64_t n, int64_t k,
                void* y, int64_t ldy, hipStream_t s) {
   // 32 rows of W a workgroup where that leaves one for each compute unit, else 16 (W read from memory, one call after
-  // another in a graph: 1 x 8192 x 8192 10.2 us, with 16 rows 10.8; 1 x 16384 x 4096 9.6 or 11.2; 8 x 11008 x 4096 10.5
-  // or 11.2; but 1 x 4096 x 11008 9.8 or 8.6)
+  // another in a graph, when x still came after it: 1 x 8192 x 8192 10.2 us, with 16 rows 10.8; 1 x 16384 x 4096 9.6 or
+  // 11.2; 8 x 11008 x 4096 10.5 or 11.2; but 1 x 4096 x 11008 9.8 or 8.6)
   if (n >= 32 * (int64_t)compute_units()) {
     hipLaunchKernelGGL((k_mx4_few<SRC, OUT, 2, CT>), dim3((unsigned)((n + 31) / 32)), dim3(64 * kFewWaves), 0, s, x, ldx,
                        (const uint8_t*)xs, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy);
