@@ -35,8 +35,8 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 // its products, a few instructions at a time, so that the matrix cores are
 // never without work; one barrier a step.
 //
-// dx 8192 x 11008 x 4096 534 to 620 us (1.2 to 1.4 PFLOP/s), dw from E4M3 592 us
-// (1.25), from INT8 689 us (1.07; twice the vector instructions to convert it). The
+// dx 8192 x 11008 x 4096 534 to 620 us (1.2 to 1.4 PFLOP/s), dw from E4M3 583 us
+// (1.27), from INT8 650 us (1.14; twice the vector instructions to convert it). The
 // library's bf16 product, all operands in memory at 2 bytes, takes 574 us for the
 // first and 836 us for dw's order of operands, and 8192^3 at 1.2 to 1.3 PFLOP/s.
 // Power bounds the large ones: 72% of the cycles are the matrix cores', at 1.8 of
@@ -90,13 +90,11 @@ __device__ __forceinline__ v4s read_columns(place_t p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
 }
 
-// Two INT8 codes times their scale as bfloat16: bytes `first` and first + 1 of w,
-// the codes with their top bit turned, which are code + 128 as unsigned bytes.
-// One conversion and one fused multiply-add (off = -128 s) give the exact
-// binary32 value, whose upper half is the bfloat16.
-__device__ __forceinline__ int widen_int8(uint32_t w, int first, float s, float off) {
-  const uint32_t a = __float_as_uint(__builtin_fmaf((float)(w >> 8 * first & 0xFFu), s, off));
-  const uint32_t b = __float_as_uint(__builtin_fmaf((float)(w >> 8 * (first + 1) & 0xFFu), s, off));
+// Two INT8 codes times their scale as bfloat16: bytes `first` and first + 1 of w.
+// The binary32 product is exact, and its upper half is the bfloat16.
+__device__ __forceinline__ int widen_int8(uint32_t w, int first, float s) {
+  const uint32_t a = __float_as_uint((float)(int8_t)(w >> 8 * first) * s);
+  const uint32_t b = __float_as_uint((float)(int8_t)(w >> 8 * (first + 1)) * s);
   return (int)__builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
@@ -256,8 +254,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
   // Unit i of the step's W or x8: 8 codes, converted in kBits bits and stored with the last.
   constexpr int kBits = KIND == kWgrad && F == LQ_INT8 ? 4 : 2;
   static_assert(kUnitsB == kLoadsA, "a thread has as many units of either operand");
-  float scale[kLoadsB], offset[kLoadsB];
-  uint32_t turned;
+  float scale[kLoadsB];
   v4i made;
   auto put_b = [&](int st, int set, int i, int bit) {
     const int l = i / kEach, u = i % kEach;
@@ -272,8 +269,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
         made[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
       }
     } else if (F == LQ_INT8) {
-      if (bit % 2 == 0) turned = (uint32_t)rb[set][l][2 * u + bit / 2] ^ 0x80808080u;
-      made[bit] = widen_int8(turned, bit % 2 * 2, s, offset[l]);
+      made[bit] = widen_int8((uint32_t)rb[set][l][2 * u + bit / 2], bit % 2 * 2, s);
     } else {
       const int w = rb[set][l][2 * u + bit];
       made[2 * bit] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
@@ -359,7 +355,6 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
   };
   auto take_scales = [&](int set, int i) {
     scale[i] = scale_value(rs[set][i]);
-    offset[i] = -128.0f * scale[i];
   };
   load(begin, 0);
   load(begin + 1, 1);

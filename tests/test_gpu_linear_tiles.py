@@ -174,6 +174,37 @@ def test_nothing_around_dy_is_used(m, n, k, ld):
     close(got[1][1], d.t() @ x8, d.abs().t() @ x8.abs(), m, "f32", "dw")
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("size", [3.3e38, 2.0 ** 126, 1e38, 2.0 ** -100])
+def test_checkpoints_at_the_ends_of_binary32(fmt, size):
+    """Scales up to 2^122: the codes' values are finite, and so are gradients of small dy. (But 3.3e38 in E4M3 is 248 * 2^120,
+    whose nearest code is 256: 2^128, an infinity in the binary32 that the gradients are computed from.)"""
+    say(f"[gpu] {fmt} checkpoint of {size}")
+    m, n, k = 70, 40, 96
+    x = (random(m, k, "f32", 0, 1).clamp(-1, 1) * size).contiguous()
+    x[::7] = size
+    kept = lq.Ckpt8(m, k, fmt)
+    kept.save(x)
+    x8 = kept_values(x, fmt)
+    over = x8.abs() >= 2.0 ** 128
+    assert over.any() == (fmt == "e4m3" and size == 3.3e38)
+    dy = random(m, n, "bf16", 0, 2) * 2.0 ** -60
+    layer = lq.Mx4Linear(torch.zeros(n, k, device="cuda"), rows=m)
+    d = dy.double()
+    got, cols = layer.wgrad(dy, kept), ~over.any(0)
+    close(got[:, cols], d.t() @ x8[:, cols], d.abs().t() @ x8[:, cols].abs() + 2.0 ** -126, m, "f32", "dw")
+    assert not got[:, ~cols].isfinite().any()
+    act = lq.SwigluCkpt8(m, k, "f32", fmt)
+    act.forward(torch.full_like(x, 0.5), x)
+    dg, du = act.backward(torch.full_like(x, 2.0 ** -60))
+    g8 = kept_values(torch.full_like(x, 0.5), fmt)
+    s = 1 / (1 + torch.exp(-g8))
+    want = 2.0 ** -60 * x8 * s * (1 + g8 * (1 - s))
+    bound = 17 * 2.0 ** -24 * 2.0 ** -60 * x8.abs() * s * (1 + g8) + 2.0 ** -120
+    assert ((dg.double() - want).abs() <= bound)[~over].all()
+    assert not dg[over].isfinite().any()
+
+
 def example():
     path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "gated_mlp.py")
     spec = importlib.util.spec_from_file_location("gated_mlp", path)
