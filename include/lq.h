@@ -294,9 +294,10 @@ LQ_API int lq_call_kernels(const lq_desc* desc, int64_t rows, int64_t cols, uint
  * last block of a row short if k is no multiple of 32. Codes are the rules
  * above (E2M1; INT8 in [-127,127], half to even; E4M3). A block that holds an
  * infinity or a NaN gets the NaN scale 0xFF and zero codes, and every result
- * computed from it is NaN. The products take the quantised values as they are (E2M1, INT8 and
- * E4M3 values times a power of two are exact in bfloat16) and add in binary32;
- * results are rounded once, to nearest even, to the output type. A repeated
+ * computed from it is NaN. The products take the quantised values as they are
+ * (E2M1, INT8 and E4M3 values times a power of two are exact in bfloat16; one
+ * that rounding took to 2^128 is infinite) and add in binary32; results are
+ * rounded once, to nearest even, to the output type. A repeated
  * call gives the same bits. silu(g) = g / (1 + exp(-g)), its derivative
  * s (1 + g (1 - s)) with s = 1 / (1 + exp(-g)), in binary32.
  *
@@ -313,8 +314,9 @@ LQ_API int lq_call_kernels(const lq_desc* desc, int64_t rows, int64_t cols, uint
  *           are lq_quantize's bytes for INT8 or E4M3, PER_BLOCK 32, UE8M0, and
  *           lq_dequantize reads them.
  *
- * Sides are 0 .. 2^31-1, n and k of a layer at most 2^21. Empty sides are no error: an empty contraction gives
- * zeros (or dw_in). Pointers, ownership, streams and errors as above; buffers
+ * Sides are 0 .. 2^31-1, n and k of a layer at most 2^21. Empty sides are no
+ * error: an empty contraction gives zeros (or dw_in). dy is read in words of 4
+ * bytes: after an odd number of elements also the rest of its last word. Pointers, ownership, streams and errors as above; buffers
  * of one call must not overlap, except that dw may be dw_in. Every call but the
  * quantisers and the activation needs a workspace of
  * lq_linear_workspace_bytes(), 16-byte aligned, not initialised, not shared
