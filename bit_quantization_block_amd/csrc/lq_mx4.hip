@@ -374,7 +374,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
 }
 
 // ---------------------------------------------------------------- a few rows
-// Up to 16 CT rows of x: the call is bound by reading W once. Eight waves of a
+// Up to 16 CT rows of x, 64 at most: the call is bound by reading W once. Eight waves of a
 // workgroup share 16 R rows of W, each taking a run of the contraction's groups
 // with v_mfma_scale_f32_16x16x128_f8f6f4, whose operand of 16 rows and 128
 // columns is one kilobyte of W as it is stored; their sums meet in LDS. With SRC
@@ -445,7 +445,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64
 #pragma unroll
   for (int i = 0; i < R; i++) wrow[i] = row0 + i * 16 + r < n ? row0 + i * 16 + r : n - 1;
 
-  constexpr int U = 4;   // groups whose reads are in flight together
+  constexpr int U = CT == 4 ? 2 : 4;   // groups whose reads are in flight together (4 of 64 rows' would leave one wave on a SIMD)
   struct Reads {
     v4i wc[U][R], xc[own ? 1 : U][CT];
     uint32_t we[U][R], xe[own ? 1 : U][CT];
@@ -581,8 +581,8 @@ hipError_t few(const void* x, int64_t ldx, const void* xs, const void* w, const 
   // 32 rows of W a workgroup where that leaves one for each compute unit, else 16 (W read from memory, one call after
   // another in a graph, when x still came after it: 1 x 8192 x 8192 10.2 us, with 16 rows 10.8; 1 x 16384 x 4096 9.6 or
   // 11.2; 8 x 11008 x 4096 10.5 or 11.2; but 1 x 4096 x 11008 9.8 or 8.6)
-  if (n >= 32 * (int64_t)compute_units()) {
-    hipLaunchKernelGGL((k_mx4_few<SRC, OUT, 2, CT>), dim3((unsigned)((n + 31) / 32)), dim3(64 * kFewWaves), 0, s, x, ldx,
+  if (CT < 4 && n >= 32 * (int64_t)compute_units()) {
+    hipLaunchKernelGGL((k_mx4_few<SRC, OUT, CT < 4 ? 2 : 1, CT>), dim3((unsigned)((n + 31) / 32)), dim3(64 * kFewWaves), 0, s, x, ldx,
                        (const uint8_t*)xs, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy);
   } else {
     hipLaunchKernelGGL((k_mx4_few<SRC, OUT, 1, CT>), dim3((unsigned)((n + 15) / 16)), dim3(64 * kFewWaves), 0, s, x, ldx,
@@ -613,6 +613,10 @@ hipError_t product_dt(const void* a, const void* as, const void* w, const void* 
   if (k == 0) return launch_constant(m, n, OUT, nullptr, y, ldy, s);
   if (m <= 16) return few<kOperand, OUT, 1>(a, 0, as, w, ws, m, n, k, y, ldy, s);
   if (m <= 32) return few<kOperand, OUT, 2>(a, 0, as, w, ws, m, n, k, y, ldy, s);
+  // Every workgroup reads all of x, 4 times its share of W at 64 rows: worth it with one on a compute unit and not too
+  // much of x (W in memory; 64 x 4096 x 4096 9.8 us, in tiles 12.9; 64 x 1024 x 4096 9.4 or 11.4; but 64 x 4096 x 11008
+  // 18.2 or 17.2, 64 x 8192 x 8192 24.6 or 19.5)
+  if (m <= 64 && n <= 16 * (int64_t)compute_units() && k <= 8192) return few<kOperand, OUT, 4>(a, 0, as, w, ws, m, n, k, y, ldy, s);
   const Split c = split_product(m, n, k, OUT);
   if (c.parts == 1) return product_tile<OUT>(c.tile, a, as, w, ws, m, n, k, 1, c.part, y, ldy, s);
   const hipError_t e = product_tile<LQ_F32>(c.tile, a, as, w, ws, m, n, k, c.parts, c.part, planes, plane_stride(n), s);

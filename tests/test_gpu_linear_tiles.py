@@ -123,6 +123,19 @@ def test_few_rows(m, k, dtype):
         assert (got[1] == 0).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(17, 70, 4096), (32, 8200, 300), (33, 70, 4096), (48, 300, 8192), (48, 300, 8193), (64, 4096, 1000),
+                                   (64, 4097, 1000), (63, 33, 129), (65, 100, 500)])
+@pytest.mark.parametrize("out", ["bf16", "f32", "f16"])
+def test_some_tens_of_rows(m, n, k, out):
+    say(f"[gpu] tens of rows {m}x{n}x{k} {out}")
+    x, w = random(m, k, "bf16", 3, m), random(n, k, "bf16", 0, 5, 0.02)
+    layer = lq.Mx4Linear(w, rows=m, out=out)
+    x4, w4 = kept_values(x, "e2m1"), kept_values(w, "e2m1")
+    y = torch.full((m, n + 5), 55.0, dtype=T[out], device="cuda")
+    close(layer.forward(x, out=y[:, :n]), x4 @ w4.t(), x4.abs() @ w4.abs().t(), k, out, "y")
+    assert (y[:, n:] == 55.0).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_activation_at_the_ends_of_its_range(dtype):
     """exp(-g) that overflows, a reciprocal below the normal numbers, infinities and NaN, against g u / (1 + exp(-g)) in
