@@ -370,6 +370,34 @@ def _matrix(t, rows, cols, dtype, what):
     return st[0] if rows > 1 else max(st[0], cols)
 
 
+def _share(a, b) -> bool:
+    """Whether two matrices with contiguous rows have a byte in common. (Two column ranges of one matrix interleave and
+    share none.)"""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    (pa, ma, wa, sa), (pb, mb, wb, sb) = ((t.data_ptr(), t.shape[0], t.shape[1] * t.element_size(),
+                                           t.stride(0) * t.element_size()) for t in (a, b))
+    if ma == 1:
+        sa = sb                              # a single row has any stride
+    elif mb == 1:
+        sb = sa
+    if sa == sb:
+        # row i of a and row i + t of b meet where -wb < pb - pa + t sa < wa
+        if ma == 1 and mb == 1:
+            return pa < pb + wb and pb < pa + wa
+        d = pb - pa
+        return max(-((wb + d - 1) // sa), 1 - ma) <= min((wa - d - 1) // sa, mb - 1)
+    # a row of a meets one of b that starts before the row's end and is the last such, or none
+    first = pa + sa * np.arange(ma, dtype=np.int64)
+    at = np.searchsorted(pb + sb * np.arange(mb, dtype=np.int64), first + wa) - 1
+    return bool(((at >= 0) & (pb + sb * at + wb > first)).any())
+
+
+def _reach(rows, ld, cols, size):
+    """Bytes from a matrix' first element to its last's end."""
+    return ((rows - 1) * ld + cols) * size if rows and cols else 0
+
+
 class Ckpt8:
     """An activation [rows, cols] kept in 8 bits for the backward pass: INT8
     or E4M3 codes (`fmt`), a power-of-two scale per 32 columns. A forward call
@@ -405,7 +433,8 @@ class Mx4Linear:
     gradients. `w` [n, k] is quantised once; `rows` is the most rows of x or
     dy a call may have, for which the results' buffers are allocated once (a
     call's result is a view of the layer's buffer, which the layer's next call
-    of that kind overwrites, unless the caller passes its own as `out`).
+    of that kind overwrites, unless the caller passes its own as `out`; a call
+    on that very result gets a second buffer, and the two take turns).
     `dtype`: of x; `out`: of y and dx; dy is bfloat16 and dw float32. Calls of
     one layer share its workspace: on two streams at a time, use two layers."""
 
@@ -469,8 +498,22 @@ class Mx4Linear:
         ws = self._workspace(need)
         if len(self._plans) >= 256:
             self._plans.clear()
-        plan = self._plans[key] = (ref, ctypes.c_void_p(ws.data_ptr()), ws.numel(), buffer)
+        sizes = _torch_dtype(in_dtype).itemsize, _torch_dtype(out_dtype).itemsize
+        plan = self._plans[key] = (ref, ctypes.c_void_p(ws.data_ptr()), ws.numel(), buffer,
+                                   _reach(m, ld_in, cols_in, sizes[0]), _reach(rows_out, ld_out, cols_out, sizes[1]))
         return plan
+
+    def _apart(self, kind, what, a, result, out):
+        """Where a call on `a` may write, whose bytes meet those of `result`: nothing that the call still reads may be
+        overwritten. The layer's second buffer, if the result is its own."""
+        if not _share(a, result):
+            return result
+        if out is not None:
+            raise ValueError(f"{what} and out share memory")
+        b = self._buffers.get(kind + " 2")
+        if b is None:
+            b = self._buffers[kind + " 2"] = self.torch.empty_like(self._buffers[kind])
+        return b[:result.shape[0]]
 
     def forward(self, x, ckpt: Ckpt8 | None = None, out=None, stream=None):
         """y = Q4(x) W^T; `ckpt` also receives x in 8 bits."""
@@ -484,7 +527,11 @@ class Mx4Linear:
             self._check_ckpt(ckpt, x.shape[0])
             cc, cs = ckpt.codes.data_ptr(), ckpt.scales.data_ptr()
         y = plan[3] if out is None else out
-        rc = self.lib.lq_mx4_linear(plan[0], x.data_ptr(), self._wc, self._ws, y.data_ptr(), cc, cs, plan[1], plan[2],
+        xp, yp = x.data_ptr(), y.data_ptr()
+        if xp < yp + plan[5] and yp < xp + plan[4]:
+            y = self._apart("y", "x", x, y, out)
+            yp = y.data_ptr()
+        rc = self.lib.lq_mx4_linear(plan[0], xp, self._wc, self._ws, yp, cc, cs, plan[1], plan[2],
                                     _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_mx4_linear", rc)
@@ -497,14 +544,18 @@ class Mx4Linear:
             key += _layout(out)
         plan = self._plans.get(key) or self._plan(key, "dx", dy, "dy", self.n, self.k, "bf16", self.out, "int8", out)
         dx = plan[3] if out is None else out
-        rc = self.lib.lq_mx4_dgrad(plan[0], dy.data_ptr(), self._wc, self._ws, dx.data_ptr(), plan[1], plan[2],
+        yp, xp = dy.data_ptr(), dx.data_ptr()
+        if yp < xp + plan[5] and xp < yp + plan[4]:
+            dx = self._apart("dx", "dy", dy, dx, out)
+            xp = dx.data_ptr()
+        rc = self.lib.lq_mx4_dgrad(plan[0], yp, self._wc, self._ws, xp, plan[1], plan[2],
                                    _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_mx4_dgrad", rc)
         return dx
 
     def wgrad(self, dy, ckpt: Ckpt8, dw_in=None, out=None, stream=None):
-        """dw = dw_in + dy^T x8, x8 the checkpoint that forward wrote; `out` may be dw_in."""
+        """dw = dw_in + dy^T x8, x8 the checkpoint that forward wrote; `out` may be dw_in, but not a part of it."""
         key = ("dw", ckpt.fmt) + _layout(dy, dw_in, out)
         plan = self._plans.get(key)
         if plan is None:
@@ -515,8 +566,13 @@ class Mx4Linear:
             plan = self._plan(key, "dw", dy, "dy", self.n, self.k, "bf16", "f32", ckpt.fmt, out)
         self._check_ckpt(ckpt, dy.shape[0])
         dw = plan[3] if out is None else out
-        rc = self.lib.lq_ckpt8_wgrad(plan[0], dy.data_ptr(), ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), _ptr(dw_in),
-                                     dw.data_ptr(), plan[1], plan[2], _stream_of(self._index, stream))
+        yp, wp, ap = dy.data_ptr(), dw.data_ptr(), _ptr(dw_in)
+        if yp < wp + plan[5] and wp < yp + plan[4] and _share(dy, dw):
+            raise ValueError("dy and the result share memory")
+        if ap is not None and ap != wp and abs(ap - wp) < plan[5] and _share(dw_in, dw):
+            raise ValueError("dw_in and the result share memory, but are not the same")
+        rc = self.lib.lq_ckpt8_wgrad(plan[0], yp, ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), ap, wp, plan[1], plan[2],
+                                     _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_ckpt8_wgrad", rc)
         return dw
@@ -529,7 +585,8 @@ class Mx4Linear:
 class SwigluCkpt8:
     """h = silu(gate) up over [rows, cols], keeping gate and up in 8 bits, and
     its backward pass from those. Results are the object's own buffers unless
-    the caller passes its own."""
+    the caller passes its own, and may be a call's inputs (h one of gate and up,
+    dgate or dup dh: the same rows), but no other part of them."""
 
     def __init__(self, rows: int, cols: int, dtype: str = "bf16", fmt: str = "int8", device="cuda", lib=None):
         import torch
@@ -564,8 +621,15 @@ class SwigluCkpt8:
         if len(self._plans) >= 256:
             self._plans.clear()
         d = SwigluDesc(DTYPE[self.dtype], FORMAT[self.fmt], self.rows, self.cols, ld, ld_h)
-        plan = self._plans[key] = (ctypes.byref(d), *own)
+        size = self._t.itemsize
+        plan = self._plans[key] = (ctypes.byref(d), _reach(self.rows, ld, self.cols, size),
+                                   _reach(self.rows, ld_h, self.cols, size), *own)
         return plan
+
+    def _refuse(self, a, result, what):
+        """An element is read and written by the same lane: in place is as good as apart, but nothing between."""
+        if _share(a, result) and not (a.data_ptr() == result.data_ptr() and (self.rows == 1 or a.stride(0) == result.stride(0))):
+            raise ValueError(f"{what} share memory, but are not the same")
 
     def forward(self, gate, up, out=None, stream=None):
         key = (gate.shape, gate.stride(), gate.dtype, gate.get_device(), up.shape, up.stride(), up.dtype, up.get_device())
@@ -579,9 +643,13 @@ class SwigluCkpt8:
             self._at_home(gate, up, *(() if out is None else (out,)))
             own, ldh = self._result("h", out)
             plan = self._remember(key, ld, ldh, own)
-        h = plan[1] if out is None else out
-        rc = self.lib.lq_swiglu_ckpt8(plan[0], gate.data_ptr(), up.data_ptr(), h.data_ptr(), *self._kept,
-                                      _stream_of(self._index, stream))
+        h = plan[3] if out is None else out
+        gp, up_, hp = gate.data_ptr(), up.data_ptr(), h.data_ptr()
+        if gp < hp + plan[2] and hp < gp + plan[1]:
+            self._refuse(gate, h, "gate and h")
+        if up_ < hp + plan[2] and hp < up_ + plan[1]:
+            self._refuse(up, h, "up and h")
+        rc = self.lib.lq_swiglu_ckpt8(plan[0], gp, up_, hp, *self._kept, _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_swiglu_ckpt8", rc)
         return h
@@ -600,9 +668,15 @@ class SwigluCkpt8:
                 raise ValueError("dgate and dup differ in their row strides")
             self._at_home(dh, *(out or ()))
             plan = self._remember(key, ld, ldh, own0, own1)
-        dg, du = (plan[1], plan[2]) if out is None else out
-        rc = self.lib.lq_swiglu_ckpt8_backward(plan[0], dh.data_ptr(), *self._kept, dg.data_ptr(), du.data_ptr(),
-                                               _stream_of(self._index, stream))
+        dg, du = (plan[3], plan[4]) if out is None else out
+        hp, gp, up = dh.data_ptr(), dg.data_ptr(), du.data_ptr()
+        if hp < gp + plan[1] and gp < hp + plan[2]:
+            self._refuse(dh, dg, "dh and dgate")
+        if hp < up + plan[1] and up < hp + plan[2]:
+            self._refuse(dh, du, "dh and dup")
+        if abs(gp - up) < plan[1] and _share(dg, du):
+            raise ValueError("dgate and dup share memory")
+        rc = self.lib.lq_swiglu_ckpt8_backward(plan[0], hp, *self._kept, gp, up, _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_swiglu_ckpt8_backward", rc)
         return dg, du

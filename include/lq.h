@@ -316,8 +316,10 @@ LQ_API int lq_call_kernels(const lq_desc* desc, int64_t rows, int64_t cols, uint
  *
  * Sides are 0 .. 2^31-1, n and k of a layer at most 2^21. Empty sides are no
  * error: an empty contraction gives zeros (or dw_in). dy is read in words of 4
- * bytes: after an odd number of elements also the rest of its last word. Pointers, ownership, streams and errors as above; buffers
- * of one call must not overlap, except that dw may be dw_in. Every call but the
+ * bytes: after an odd number of elements also the rest of its last word.
+ * Pointers, ownership, streams and errors as above; buffers of one call must
+ * not overlap, except that dw may be dw_in, and of the activation h may be gate
+ * or up, dgate or dup may be dh, all with one row stride. Every call but the
  * quantisers and the activation needs a workspace of
  * lq_linear_workspace_bytes(), 16-byte aligned, not initialised, not shared
  * by calls that overlap in time. */
