@@ -406,6 +406,8 @@ class Ckpt8:
     def __init__(self, rows: int, cols: int, fmt: str = "int8", device="cuda", lib=None):
         import torch
 
+        if torch.device(device).type != "cuda":
+            raise ValueError(f"a checkpoint on {device}: its kernels need it on a GPU")
         self.lib = lib or load()
         self.rows, self.cols, self.fmt = rows, cols, fmt
         u8 = dict(dtype=torch.uint8, device=device)
@@ -414,6 +416,8 @@ class Ckpt8:
 
     def save(self, x, stream=None):
         ld = _matrix(x, self.rows, self.cols, x.dtype, "x")
+        if x.device != self.codes.device:
+            raise ValueError(f"x is on {x.device}, the checkpoint on {self.codes.device}")
         d = LinearDesc(DTYPE[_dtype_name(x)], 0, FORMAT[self.fmt], 0, self.rows, 0, self.cols, ld, 0)
         _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(x), None, None, _ptr(self.codes),
                                                            _ptr(self.scales), _stream(stream)))
@@ -442,6 +446,7 @@ class Mx4Linear:
         import torch
 
         self.torch = torch
+        self._index = w.device.index
         self.lib = lib or load()
         self.n, self.k = w.shape
         self.rows, self.dtype, self.out = rows, dtype, out
@@ -451,7 +456,6 @@ class Mx4Linear:
         self.scales = torch.empty(max(16, self.lib.lq_mx4_scales_bytes(self.n, self.k)), **u8)
         self.load(w)
         self._wc, self._ws = ctypes.c_void_p(self.codes.data_ptr()), ctypes.c_void_p(self.scales.data_ptr())
-        self._index = w.device.index
         self._plans = {}
         self._buffers = {}
         self._workspaces = []
@@ -561,6 +565,8 @@ class Mx4Linear:
         if plan is None:
             if dw_in is not None:
                 ld = _matrix(dw_in, self.n, self.k, self.torch.float32, "dw_in")
+                if dw_in.device != self.device:
+                    raise ValueError(f"dw_in is on {dw_in.device}, the layer on {self.device}")
                 if ld != (self.k if out is None else _matrix(out, self.n, self.k, self.torch.float32, "out")):
                     raise ValueError("dw_in and the result differ in their row strides")
             plan = self._plan(key, "dw", dy, "dy", self.n, self.k, "bf16", "f32", ckpt.fmt, out)
@@ -580,6 +586,8 @@ class Mx4Linear:
     def _check_ckpt(self, ckpt, m):
         if ckpt.rows != m or ckpt.cols != self.k:
             raise ValueError(f"the checkpoint is {ckpt.rows} x {ckpt.cols}, the call's x {m} x {self.k}")
+        if ckpt.codes.device != self.device:
+            raise ValueError(f"the checkpoint is on {ckpt.codes.device}, the layer on {self.device}")
 
 
 class SwigluCkpt8:
@@ -592,7 +600,6 @@ class SwigluCkpt8:
         import torch
 
         self.torch = torch
-        self.lib = lib or load()
         self.rows, self.cols, self.dtype, self.fmt = rows, cols, dtype, fmt
         self._t = _torch_dtype(dtype)
         self.gate = Ckpt8(rows, cols, fmt, device, lib)
@@ -600,6 +607,7 @@ class SwigluCkpt8:
         self._kept = tuple(ctypes.c_void_p(t.data_ptr()) for c in (self.gate, self.up) for t in (c.codes, c.scales))
         self.device = self.gate.codes.device
         self._index = self.device.index
+        self.lib = lib or load()
         self._plans = {}
         self._buffers = {}
 

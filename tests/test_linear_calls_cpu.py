@@ -149,3 +149,29 @@ def test_the_gated_unit_in_place_or_apart():
         with pytest.raises(ValueError, match="share memory"):
             refused()
     assert len(act.lib.calls) == 6
+
+
+def elsewhere(*shape, dtype=torch.bfloat16):
+    """A tensor that says it is a GPU's, but another's."""
+    return torch.empty(*shape, dtype=dtype, device="meta").as_subclass(OnGpu)
+
+
+def test_every_tensor_of_a_call_is_on_the_objects_device(layer):
+    for device in ("cpu", torch.device("cpu"), "meta"):
+        with pytest.raises(ValueError, match="GPU"):
+            lq.Ckpt8(8, 64, device=device)
+        with pytest.raises(ValueError, match="GPU"):
+            lq.SwigluCkpt8(8, 64, device=device)
+    kept = lq.Ckpt8.__new__(lq.Ckpt8)
+    kept.rows, kept.cols, kept.fmt, kept.lib, kept._index = 8, 64, "int8", layer.lib, None
+    kept.codes = kept.scales = elsewhere(8 * 64, dtype=torch.uint8)
+    x, dy = device_tensor(8, 64), device_tensor(8, 64)
+    for refused in (lambda: layer.forward(x, ckpt=kept), lambda: layer.wgrad(dy, kept), lambda: kept.save(x),
+                    lambda: layer.load(elsewhere(64, 64)), lambda: layer.forward(elsewhere(7, 64)),
+                    lambda: layer.forward(x, out=elsewhere(8, 64)), lambda: layer.dgrad(elsewhere(7, 64))):
+        with pytest.raises(ValueError, match=" on "):
+            refused()
+    kept.codes = kept.scales = torch.empty(8 * 64, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="dw_in is on"):
+        layer.wgrad(dy, kept, dw_in=elsewhere(64, 64, dtype=torch.float32))
+    assert not layer.lib.calls
