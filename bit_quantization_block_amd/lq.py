@@ -157,6 +157,36 @@ def _stream_of(device: int, stream):
     return _raw_stream(device)
 
 
+class _Elsewhere:
+    """The library's functions, called with a device current that may not be: a launch goes to the current device
+    whatever the memory's is. (With one GPU there is no other, and calls go straight to the library.)"""
+
+    def __init__(self, lib, device):
+        self._lib, self._device = lib, device
+
+    def __getattr__(self, name):
+        import torch
+
+        fn = getattr(self._lib, name)
+
+        def call(*args):
+            if torch.cuda.current_device() == self._device:
+                return fn(*args)
+            with torch.cuda.device(self._device):
+                return fn(*args)
+
+        setattr(self, name, call)
+        return call
+
+
+def _library(lib, device):
+    """The library for memory on this device."""
+    import torch
+
+    lib = lib or load()
+    return _Elsewhere(lib, device) if torch.cuda.device_count() > 1 else lib
+
+
 def _check(fn, rc):
     if rc != LQ_OK:
         raise LQError(fn, rc)
@@ -408,11 +438,13 @@ class Ckpt8:
 
         if torch.device(device).type != "cuda":
             raise ValueError(f"a checkpoint on {device}: its kernels need it on a GPU")
-        self.lib = lib or load()
+        sizes = lib or load()
         self.rows, self.cols, self.fmt = rows, cols, fmt
         u8 = dict(dtype=torch.uint8, device=device)
-        self.codes = torch.empty(max(16, self.lib.lq_ckpt8_codes_bytes(rows, cols)), **u8)
-        self.scales = torch.empty(max(16, self.lib.lq_ckpt8_scales_bytes(rows, cols)), **u8)
+        self.codes = torch.empty(max(16, sizes.lq_ckpt8_codes_bytes(rows, cols)), **u8)
+        self.scales = torch.empty(max(16, sizes.lq_ckpt8_scales_bytes(rows, cols)), **u8)
+        self._index = self.codes.device.index
+        self.lib = _library(lib, self._index)
 
     def save(self, x, stream=None):
         ld = _matrix(x, self.rows, self.cols, x.dtype, "x")
@@ -420,7 +452,7 @@ class Ckpt8:
             raise ValueError(f"x is on {x.device}, the checkpoint on {self.codes.device}")
         d = LinearDesc(DTYPE[_dtype_name(x)], 0, FORMAT[self.fmt], 0, self.rows, 0, self.cols, ld, 0)
         _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(x), None, None, _ptr(self.codes),
-                                                           _ptr(self.scales), _stream(stream)))
+                                                           _ptr(self.scales), _stream_of(self._index, stream)))
 
 
 def _layout(*tensors):
@@ -447,7 +479,7 @@ class Mx4Linear:
 
         self.torch = torch
         self._index = w.device.index
-        self.lib = lib or load()
+        self.lib = _library(lib, self._index)
         self.n, self.k = w.shape
         self.rows, self.dtype, self.out = rows, dtype, out
         self.device = w.device
@@ -467,7 +499,8 @@ class Mx4Linear:
             raise ValueError(f"w is on {w.device}, the layer on {self.device}")
         d = LinearDesc(DTYPE[_dtype_name(w)], 0, 0, 0, self.n, 0, self.k, ld, 0)
         _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(w), _ptr(self.codes),
-                                                           _ptr(self.scales), None, None, _stream(stream)))
+                                                           _ptr(self.scales), None, None,
+                                                           _stream_of(self._index, stream)))
 
     def _workspace(self, need):
         """One of at least this size. Smaller ones stay alive: a captured graph may hold their addresses."""
@@ -607,7 +640,7 @@ class SwigluCkpt8:
         self._kept = tuple(ctypes.c_void_p(t.data_ptr()) for c in (self.gate, self.up) for t in (c.codes, c.scales))
         self.device = self.gate.codes.device
         self._index = self.device.index
-        self.lib = lib or load()
+        self.lib = _library(lib, self._index)
         self._plans = {}
         self._buffers = {}
 

@@ -175,3 +175,44 @@ def test_every_tensor_of_a_call_is_on_the_objects_device(layer):
     with pytest.raises(ValueError, match="dw_in is on"):
         layer.wgrad(dy, kept, dw_in=elsewhere(64, 64, dtype=torch.float32))
     assert not layer.lib.calls
+
+
+def test_calls_are_made_on_the_memorys_device(monkeypatch):
+    """With several GPUs, one that is not the current device becomes it for the call."""
+    now, seen = [0], []
+
+    class At:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.device
+
+        def __exit__(self, *exc):
+            now[0] = self.before
+
+    class Lib:
+        def lq_mx4_linear(self, *args):
+            seen.append((now[0], args))
+            return -3
+
+    monkeypatch.setattr(torch.cuda, "device", At)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    for device in (0, 1, 1):
+        assert lq._library(Lib(), device).lq_mx4_linear(5, 6) == -3
+    assert seen == [(0, (5, 6)), (1, (5, 6)), (1, (5, 6))] and now == [0]
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 1)
+    lib = Lib()
+    assert lq._library(lib, 0) is lib
+
+
+def test_weights_and_checkpoints_go_on_their_devices_stream(layer, monkeypatch):
+    monkeypatch.setattr(lq, "_stream_of", lambda device, stream: ("of", device, stream))
+    layer.load(device_tensor(64, 64))
+    kept = lq.Ckpt8.__new__(lq.Ckpt8)
+    kept.rows, kept.cols, kept.fmt, kept.lib, kept._index = 8, 64, "int8", layer.lib, 3
+    kept.codes = kept.scales = device_tensor(8 * 64, dtype=torch.uint8)
+    kept.save(device_tensor(8, 64))
+    kept.save(device_tensor(8, 64), stream=77)
+    assert [c[-1] for c in layer.lib.calls] == [("of", None, None), ("of", 3, None), ("of", 3, 77)]
