@@ -428,6 +428,17 @@ def _reach(rows, ld, cols, size):
     return ((rows - 1) * ld + cols) * size if rows and cols else 0
 
 
+def _empty_for(stream, *size, dtype, device):
+    """Memory for a call on this stream (None: the current one), from the stream's own pool: what the current stream's
+    pool hands out may still be in use by work that is queued there, which another stream does not wait for."""
+    import torch
+
+    if stream is None or stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)):
+        return torch.empty(size, dtype=dtype, device=device)
+
+
 class Ckpt8:
     """An activation [rows, cols] kept in 8 bits for the backward pass: INT8
     or E4M3 codes (`fmt`), a power-of-two scale per 32 columns. A forward call
@@ -472,7 +483,10 @@ class Mx4Linear:
     of that kind overwrites, unless the caller passes its own as `out`; a call
     on that very result gets a second buffer, and the two take turns).
     `dtype`: of x; `out`: of y and dx; dy is bfloat16 and dw float32. Calls of
-    one layer share its workspace: on two streams at a time, use two layers."""
+    one layer share its buffers and workspace: on two streams at a time, use two
+    layers; a stream other than the one on which the layer was made, or last
+    called, waits for that one first. `stream` is a stream's handle; tensors
+    given to a call on it are kept by the caller until it is done."""
 
     def __init__(self, w, rows: int, dtype: str = "bf16", out: str = "bf16", lib=None):
         import torch
@@ -502,13 +516,13 @@ class Mx4Linear:
                                                            _ptr(self.scales), None, None,
                                                            _stream_of(self._index, stream)))
 
-    def _workspace(self, need):
+    def _workspace(self, need, stream):
         """One of at least this size. Smaller ones stay alive: a captured graph may hold their addresses."""
         if not self._workspaces or self._workspaces[-1].numel() < need:
-            self._workspaces.append(self.torch.empty(need, dtype=self.torch.uint8, device=self.device))
+            self._workspaces.append(_empty_for(stream, need, dtype=self.torch.uint8, device=self.device))
         return self._workspaces[-1]
 
-    def _plan(self, key, kind, a, what, cols_in, cols_out, in_dtype, out_dtype, fmt, out):
+    def _plan(self, key, kind, a, what, cols_in, cols_out, in_dtype, out_dtype, fmt, out, stream):
         """The checked descriptor, the workspace and the result's buffer of a call with this layout."""
         m = a.shape[0]
         if m > self.rows:
@@ -524,15 +538,15 @@ class Mx4Linear:
             b = self._buffers.get(kind)
             if b is None:
                 most = self.n if kind == "dw" else self.rows
-                b = self._buffers[kind] = self.torch.empty(most, cols_out, dtype=_torch_dtype(out_dtype),
-                                                           device=self.device)
+                b = self._buffers[kind] = _empty_for(stream, most, cols_out, dtype=_torch_dtype(out_dtype),
+                                                     device=self.device)
             buffer, ld_out = b[:rows_out], cols_out
         d = LinearDesc(DTYPE[in_dtype], DTYPE[out_dtype], FORMAT[fmt], 0, m, self.n, self.k, ld_in, ld_out)
         ref = ctypes.byref(d)
         need = self.lib.lq_linear_workspace_bytes(ref)
         if need == 0:   # the descriptor is refused: by this call too, with the status
             _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ref, None, None, None, None, None, None))
-        ws = self._workspace(need)
+        ws = self._workspace(need, stream)
         if len(self._plans) >= 256:
             self._plans.clear()
         sizes = _torch_dtype(in_dtype).itemsize, _torch_dtype(out_dtype).itemsize
@@ -540,7 +554,7 @@ class Mx4Linear:
                                    _reach(m, ld_in, cols_in, sizes[0]), _reach(rows_out, ld_out, cols_out, sizes[1]))
         return plan
 
-    def _apart(self, kind, what, a, result, out):
+    def _apart(self, kind, what, a, result, out, stream):
         """Where a call on `a` may write, whose bytes meet those of `result`: nothing that the call still reads may be
         overwritten. The layer's second buffer, if the result is its own."""
         if not _share(a, result):
@@ -549,7 +563,8 @@ class Mx4Linear:
             raise ValueError(f"{what} and out share memory")
         b = self._buffers.get(kind + " 2")
         if b is None:
-            b = self._buffers[kind + " 2"] = self.torch.empty_like(self._buffers[kind])
+            like = self._buffers[kind]
+            b = self._buffers[kind + " 2"] = _empty_for(stream, *like.shape, dtype=like.dtype, device=self.device)
         return b[:result.shape[0]]
 
     def forward(self, x, ckpt: Ckpt8 | None = None, out=None, stream=None):
@@ -558,7 +573,7 @@ class Mx4Linear:
         key = ("y", fmt, x.shape, x.stride(), x.dtype, x.get_device())
         if out is not None:
             key += _layout(out)
-        plan = self._plans.get(key) or self._plan(key, "y", x, "x", self.k, self.n, self.dtype, self.out, fmt, out)
+        plan = self._plans.get(key) or self._plan(key, "y", x, "x", self.k, self.n, self.dtype, self.out, fmt, out, stream)
         cc = cs = None
         if ckpt is not None:
             self._check_ckpt(ckpt, x.shape[0])
@@ -566,7 +581,7 @@ class Mx4Linear:
         y = plan[3] if out is None else out
         xp, yp = x.data_ptr(), y.data_ptr()
         if xp < yp + plan[5] and yp < xp + plan[4]:
-            y = self._apart("y", "x", x, y, out)
+            y = self._apart("y", "x", x, y, out, stream)
             yp = y.data_ptr()
         rc = self.lib.lq_mx4_linear(plan[0], xp, self._wc, self._ws, yp, cc, cs, plan[1], plan[2],
                                     _stream_of(self._index, stream))
@@ -579,11 +594,11 @@ class Mx4Linear:
         key = ("dx", dy.shape, dy.stride(), dy.dtype, dy.get_device())
         if out is not None:
             key += _layout(out)
-        plan = self._plans.get(key) or self._plan(key, "dx", dy, "dy", self.n, self.k, "bf16", self.out, "int8", out)
+        plan = self._plans.get(key) or self._plan(key, "dx", dy, "dy", self.n, self.k, "bf16", self.out, "int8", out, stream)
         dx = plan[3] if out is None else out
         yp, xp = dy.data_ptr(), dx.data_ptr()
         if yp < xp + plan[5] and xp < yp + plan[4]:
-            dx = self._apart("dx", "dy", dy, dx, out)
+            dx = self._apart("dx", "dy", dy, dx, out, stream)
             xp = dx.data_ptr()
         rc = self.lib.lq_mx4_dgrad(plan[0], yp, self._wc, self._ws, xp, plan[1], plan[2],
                                    _stream_of(self._index, stream))
@@ -602,7 +617,7 @@ class Mx4Linear:
                     raise ValueError(f"dw_in is on {dw_in.device}, the layer on {self.device}")
                 if ld != (self.k if out is None else _matrix(out, self.n, self.k, self.torch.float32, "out")):
                     raise ValueError("dw_in and the result differ in their row strides")
-            plan = self._plan(key, "dw", dy, "dy", self.n, self.k, "bf16", "f32", ckpt.fmt, out)
+            plan = self._plan(key, "dw", dy, "dy", self.n, self.k, "bf16", "f32", ckpt.fmt, out, stream)
         self._check_ckpt(ckpt, dy.shape[0])
         dw = plan[3] if out is None else out
         yp, wp, ap = dy.data_ptr(), dw.data_ptr(), _ptr(dw_in)
@@ -649,13 +664,13 @@ class SwigluCkpt8:
             if t.device != self.device:
                 raise ValueError(f"a tensor is on {t.device}, the checkpoints on {self.device}")
 
-    def _result(self, kind, out):
+    def _result(self, kind, out, stream):
         """The result's tensor if it is the object's own, and its row stride."""
         if out is not None:
             return None, _matrix(out, self.rows, self.cols, self._t, "out")
         b = self._buffers.get(kind)
         if b is None:
-            b = self._buffers[kind] = self.torch.empty(self.rows, self.cols, dtype=self._t, device=self.device)
+            b = self._buffers[kind] = _empty_for(stream, self.rows, self.cols, dtype=self._t, device=self.device)
         return b, self.cols
 
     def _remember(self, key, ld, ld_h, *own):
@@ -682,7 +697,7 @@ class SwigluCkpt8:
             if _matrix(up, self.rows, self.cols, self._t, "up") != ld:
                 raise ValueError("gate and up differ in their row strides")
             self._at_home(gate, up, *(() if out is None else (out,)))
-            own, ldh = self._result("h", out)
+            own, ldh = self._result("h", out, stream)
             plan = self._remember(key, ld, ldh, own)
         h = plan[3] if out is None else out
         gp, up_, hp = gate.data_ptr(), up.data_ptr(), h.data_ptr()
@@ -703,8 +718,8 @@ class SwigluCkpt8:
         plan = self._plans.get(key)
         if plan is None:
             ldh = _matrix(dh, self.rows, self.cols, self._t, "dh")
-            own0, ld = self._result("dgate", out[0] if out else None)
-            own1, ld1 = self._result("dup", out[1] if out else None)
+            own0, ld = self._result("dgate", out[0] if out else None, stream)
+            own1, ld1 = self._result("dup", out[1] if out else None, stream)
             if ld != ld1:
                 raise ValueError("dgate and dup differ in their row strides")
             self._at_home(dh, *(out or ()))

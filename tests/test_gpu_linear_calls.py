@@ -51,3 +51,30 @@ def test_gated_unit_in_place(rows, cols, dtype):
         out = (d, e) if where == 0 else (e, d)
         act.backward(d, out=out)
         assert torch.equal(out[0], dg) and torch.equal(out[1], du)
+
+
+def pool_of(t):
+    """The stream whose pool a tensor's memory is from."""
+    at = t.data_ptr()
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= at < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+def test_a_call_on_a_stream_takes_memory_from_its_pool():
+    n = 256
+    layer, act = lq.Mx4Linear(random(n, n, "f32", 1), rows=40), lq.SwigluCkpt8(40, n)
+    want = layer.forward(random(40, n, "bf16", 2)).clone()
+    x = random(40, n, "bf16", 2)
+    s = torch.cuda.Stream()
+    other, act2 = lq.Mx4Linear(random(n, n, "f32", 1), rows=40), lq.SwigluCkpt8(40, n)
+    s.wait_stream(torch.cuda.current_stream())
+    y = other.forward(x, stream=s.cuda_stream)
+    h = act2.forward(y, y, stream=s.cuda_stream)
+    s.synchronize()
+    assert pool_of(y) == pool_of(h) == pool_of(other._workspaces[0]) == s.cuda_stream
+    assert pool_of(want) == torch.cuda.current_stream().cuda_stream
+    assert torch.equal(y, want) and torch.equal(h, act.forward(want, want))
+    z = other.forward(x, stream=0)
+    torch.cuda.synchronize()
+    assert z.data_ptr() == y.data_ptr() and torch.equal(z, want)

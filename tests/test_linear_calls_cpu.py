@@ -216,3 +216,46 @@ def test_weights_and_checkpoints_go_on_their_devices_stream(layer, monkeypatch):
     kept.save(device_tensor(8, 64))
     kept.save(device_tensor(8, 64), stream=77)
     assert [c[-1] for c in layer.lib.calls] == [("of", None, None), ("of", 3, None), ("of", 3, 77)]
+
+
+def test_memory_comes_from_the_calls_streams_pool(layer, monkeypatch):
+    """Buffers and workspaces of a call on a stream of its own are not taken from the current stream's pool."""
+    now, taken, empty = [5], [], torch.empty
+
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.cuda_stream = handle
+
+    class At:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.s.cuda_stream
+
+        def __exit__(self, *exc):
+            now[0] = self.before
+
+    def took(*args, **kw):
+        taken.append(now[0])
+        return empty(*args, **kw)
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(now[0]))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(0))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", At)
+    monkeypatch.setattr(torch, "empty", took)
+    x = device_tensor(8, 64)
+    y = layer.forward(x, stream=9).as_subclass(OnGpu)
+    layer.forward(y, stream=9)
+    assert set(taken) == {9} and len(taken) == 3                    # result, workspace, the second buffer
+    taken.clear()
+    layer.dgrad(device_tensor(8, 64), stream=0)
+    assert set(taken) == {0} and now == [5]
+    taken.clear()
+    act = unit(8, 64)
+    act.forward(x, y, stream=9)
+    assert taken == [9]
+    act.backward(x, stream=5)
+    act.backward(device_tensor(8, 64)[:, :64])
+    assert taken == [9, 5, 5]
