@@ -428,6 +428,17 @@ def _reach(rows, ld, cols, size):
     return ((rows - 1) * ld + cols) * size if rows and cols else 0
 
 
+def _refuse_grad(**tensors):
+    """No result is part of autograd's graph: a tensor that waits for a gradient would never get one, without a word."""
+    import torch
+
+    if torch.is_grad_enabled():
+        for what, t in tensors.items():
+            if t.requires_grad:
+                raise ValueError(f"{what} requires a gradient, which autograd does not get from this call: detach it "
+                                 "(or call under no_grad) and use the layer's own backward calls")
+
+
 def _empty_for(stream, *size, dtype, device):
     """Memory for a call on this stream (None: the current one), from the stream's own pool: what the current stream's
     pool hands out may still be in use by work that is queued there, which another stream does not wait for."""
@@ -458,6 +469,7 @@ class Ckpt8:
         self.lib = _library(lib, self._index)
 
     def save(self, x, stream=None):
+        _refuse_grad(x=x)
         ld = _matrix(x, self.rows, self.cols, x.dtype, "x")
         if x.device != self.codes.device:
             raise ValueError(f"x is on {x.device}, the checkpoint on {self.codes.device}")
@@ -477,7 +489,8 @@ def _layout(*tensors):
 
 class Mx4Linear:
     """A linear layer y = x W^T with W held in 4 bits (MXFP4), and its
-    gradients. `w` [n, k] is quantised once; `rows` is the most rows of x or
+    gradients, as calls of their own: autograd sees none of them, and inputs
+    that require a gradient are refused (w may: load() reads its values). `w` [n, k] is quantised once; `rows` is the most rows of x or
     dy a call may have, for which the results' buffers are allocated once (a
     call's result is a view of the layer's buffer, which the layer's next call
     of that kind overwrites, unless the caller passes its own as `out`; a call
@@ -569,6 +582,8 @@ class Mx4Linear:
 
     def forward(self, x, ckpt: Ckpt8 | None = None, out=None, stream=None):
         """y = Q4(x) W^T; `ckpt` also receives x in 8 bits."""
+        if x.requires_grad:
+            _refuse_grad(x=x)
         fmt = "int8" if ckpt is None else ckpt.fmt
         key = ("y", fmt, x.shape, x.stride(), x.dtype, x.get_device())
         if out is not None:
@@ -591,6 +606,8 @@ class Mx4Linear:
 
     def dgrad(self, dy, out=None, stream=None):
         """dx = dy W."""
+        if dy.requires_grad:
+            _refuse_grad(dy=dy)
         key = ("dx", dy.shape, dy.stride(), dy.dtype, dy.get_device())
         if out is not None:
             key += _layout(out)
@@ -608,6 +625,8 @@ class Mx4Linear:
 
     def wgrad(self, dy, ckpt: Ckpt8, dw_in=None, out=None, stream=None):
         """dw = dw_in + dy^T x8, x8 the checkpoint that forward wrote; `out` may be dw_in, but not a part of it."""
+        if dy.requires_grad:
+            _refuse_grad(dy=dy)
         key = ("dw", ckpt.fmt) + _layout(dy, dw_in, out)
         plan = self._plans.get(key)
         if plan is None:
@@ -688,6 +707,8 @@ class SwigluCkpt8:
             raise ValueError(f"{what} share memory, but are not the same")
 
     def forward(self, gate, up, out=None, stream=None):
+        if gate.requires_grad or up.requires_grad:
+            _refuse_grad(gate=gate, up=up)
         key = (gate.shape, gate.stride(), gate.dtype, gate.get_device(), up.shape, up.stride(), up.dtype, up.get_device())
         if out is not None:
             key += _layout(out)
@@ -712,6 +733,8 @@ class SwigluCkpt8:
 
     def backward(self, dh, out=None, stream=None):
         """(dgate, dup); `out`: a pair of tensors for them."""
+        if dh.requires_grad:
+            _refuse_grad(dh=dh)
         key = ("dh", dh.shape, dh.stride(), dh.dtype, dh.get_device())
         if out is not None:
             key += _layout(out[0], out[1])

@@ -259,3 +259,23 @@ def test_memory_comes_from_the_calls_streams_pool(layer, monkeypatch):
     act.backward(x, stream=5)
     act.backward(device_tensor(8, 64)[:, :64])
     assert taken == [9, 5, 5]
+
+
+def test_inputs_that_wait_for_a_gradient_are_refused(layer):
+    x = torch.zeros(8, 64, dtype=torch.bfloat16, requires_grad=True).as_subclass(OnGpu)
+    plain = device_tensor(8, 64)
+    act = unit(8, 64)
+    kept = lq.Ckpt8.__new__(lq.Ckpt8)
+    kept.rows, kept.cols, kept.fmt, kept.lib, kept._index = 8, 64, "int8", layer.lib, None
+    kept.codes = kept.scales = torch.empty(8 * 64, dtype=torch.uint8)
+    calls = [lambda: layer.forward(x), lambda: layer.dgrad(x), lambda: layer.wgrad(x, kept), lambda: kept.save(x),
+             lambda: act.forward(x, plain), lambda: act.forward(plain, x), lambda: act.backward(x)]
+    for call in calls:
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+    assert not layer.lib.calls and not act.lib.calls
+    with torch.no_grad():
+        for call in calls:
+            call()
+    layer.load(torch.nn.Parameter(torch.zeros(64, 64)).as_subclass(OnGpu))
+    assert len(layer.lib.calls) == 5 and len(act.lib.calls) == 3
