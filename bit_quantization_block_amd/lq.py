@@ -487,14 +487,18 @@ def _layout(*tensors):
     return key
 
 
+_CALL = {"y": "lq_mx4_linear", "dx": "lq_mx4_dgrad", "dw": "lq_ckpt8_wgrad"}
+
+
 class Mx4Linear:
     """A linear layer y = x W^T with W held in 4 bits (MXFP4), and its
     gradients, as calls of their own: autograd sees none of them, and inputs
-    that require a gradient are refused (w may: load() reads its values). `w` [n, k] is quantised once; `rows` is the most rows of x or
-    dy a call may have, for which the results' buffers are allocated once (a
-    call's result is a view of the layer's buffer, which the layer's next call
-    of that kind overwrites, unless the caller passes its own as `out`; a call
-    on that very result gets a second buffer, and the two take turns).
+    that require a gradient are refused (w may: load() reads its values).
+    `w` [n, k] is quantised once; `rows` is the most rows of x or dy a call may
+    have, for which the results' buffers are allocated once (a call's result is
+    a view of the layer's buffer, which the layer's next call of that kind
+    overwrites, unless the caller passes its own as `out`; a call on that very
+    result gets a second buffer, and the two take turns).
     `dtype`: of x; `out`: of y and dx; dy is bfloat16 and dw float32. Calls of
     one layer share its buffers and workspace: on two streams at a time, use two
     layers; a stream other than the one on which the layer was made, or last
@@ -536,7 +540,8 @@ class Mx4Linear:
         return self._workspaces[-1]
 
     def _plan(self, key, kind, a, what, cols_in, cols_out, in_dtype, out_dtype, fmt, out, stream):
-        """The checked descriptor, the workspace and the result's buffer of a call with this layout."""
+        """A call's function, checked descriptor and workspace for this layout, the result's buffer and its address
+        (none and 0 if it is the caller's), and between which addresses from there on an input's meets the result."""
         m = a.shape[0]
         if m > self.rows:
             raise ValueError(f"{m} rows in a layer planned for {self.rows}")
@@ -562,9 +567,10 @@ class Mx4Linear:
         ws = self._workspace(need, stream)
         if len(self._plans) >= 256:
             self._plans.clear()
-        sizes = _torch_dtype(in_dtype).itemsize, _torch_dtype(out_dtype).itemsize
-        plan = self._plans[key] = (ref, ctypes.c_void_p(ws.data_ptr()), ws.numel(), buffer,
-                                   _reach(m, ld_in, cols_in, sizes[0]), _reach(rows_out, ld_out, cols_out, sizes[1]))
+        at = 0 if buffer is None else buffer.data_ptr()
+        plan = self._plans[key] = (getattr(self.lib, _CALL[kind]), ref, ctypes.c_void_p(ws.data_ptr()), ws.numel(), buffer, at,
+                                   at - _reach(m, ld_in, cols_in, _torch_dtype(in_dtype).itemsize),
+                                   at + _reach(rows_out, ld_out, cols_out, _torch_dtype(out_dtype).itemsize))
         return plan
 
     def _apart(self, kind, what, a, result, out, stream):
@@ -593,13 +599,15 @@ class Mx4Linear:
         if ckpt is not None:
             self._check_ckpt(ckpt, x.shape[0])
             cc, cs = ckpt.codes.data_ptr(), ckpt.scales.data_ptr()
-        y = plan[3] if out is None else out
-        xp, yp = x.data_ptr(), y.data_ptr()
-        if xp < yp + plan[5] and yp < xp + plan[4]:
+        call, ref, ws, ws_bytes, y, yp, low, high = plan
+        if out is not None:
+            y, yp = out, out.data_ptr()
+            low, high = low + yp, high + yp
+        xp = x.data_ptr()
+        if low < xp < high:
             y = self._apart("y", "x", x, y, out, stream)
             yp = y.data_ptr()
-        rc = self.lib.lq_mx4_linear(plan[0], xp, self._wc, self._ws, yp, cc, cs, plan[1], plan[2],
-                                    _stream_of(self._index, stream))
+        rc = call(ref, xp, self._wc, self._ws, yp, cc, cs, ws, ws_bytes, _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_mx4_linear", rc)
         return y
@@ -612,13 +620,15 @@ class Mx4Linear:
         if out is not None:
             key += _layout(out)
         plan = self._plans.get(key) or self._plan(key, "dx", dy, "dy", self.n, self.k, "bf16", self.out, "int8", out, stream)
-        dx = plan[3] if out is None else out
-        yp, xp = dy.data_ptr(), dx.data_ptr()
-        if yp < xp + plan[5] and xp < yp + plan[4]:
+        call, ref, ws, ws_bytes, dx, xp, low, high = plan
+        if out is not None:
+            dx, xp = out, out.data_ptr()
+            low, high = low + xp, high + xp
+        yp = dy.data_ptr()
+        if low < yp < high:
             dx = self._apart("dx", "dy", dy, dx, out, stream)
             xp = dx.data_ptr()
-        rc = self.lib.lq_mx4_dgrad(plan[0], yp, self._wc, self._ws, xp, plan[1], plan[2],
-                                   _stream_of(self._index, stream))
+        rc = call(ref, yp, self._wc, self._ws, xp, ws, ws_bytes, _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_mx4_dgrad", rc)
         return dx
@@ -638,14 +648,19 @@ class Mx4Linear:
                     raise ValueError("dw_in and the result differ in their row strides")
             plan = self._plan(key, "dw", dy, "dy", self.n, self.k, "bf16", "f32", ckpt.fmt, out, stream)
         self._check_ckpt(ckpt, dy.shape[0])
-        dw = plan[3] if out is None else out
-        yp, wp, ap = dy.data_ptr(), dw.data_ptr(), _ptr(dw_in)
-        if yp < wp + plan[5] and wp < yp + plan[4] and _share(dy, dw):
+        call, ref, ws, ws_bytes, dw, wp, low, high = plan
+        if out is not None:
+            dw, wp = out, out.data_ptr()
+            low, high = low + wp, high + wp
+        yp, ap = dy.data_ptr(), None
+        if low < yp < high and _share(dy, dw):
             raise ValueError("dy and the result share memory")
-        if ap is not None and ap != wp and abs(ap - wp) < plan[5] and _share(dw_in, dw):
-            raise ValueError("dw_in and the result share memory, but are not the same")
-        rc = self.lib.lq_ckpt8_wgrad(plan[0], yp, ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), ap, wp, plan[1], plan[2],
-                                     _stream_of(self._index, stream))
+        if dw_in is not None:
+            ap = dw_in.data_ptr()
+            if ap != wp and abs(ap - wp) < high - wp and _share(dw_in, dw):
+                raise ValueError("dw_in and the result share memory, but are not the same")
+        rc = call(ref, yp, ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), ap, wp, ws, ws_bytes,
+                  _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_ckpt8_wgrad", rc)
         return dw
@@ -692,13 +707,15 @@ class SwigluCkpt8:
             b = self._buffers[kind] = _empty_for(stream, self.rows, self.cols, dtype=self._t, device=self.device)
         return b, self.cols
 
-    def _remember(self, key, ld, ld_h, *own):
+    def _remember(self, key, name, ld, ld_h, ld_in, ld_out, *own):
+        """A call's function and descriptor for this layout, how far below and above a result's address an input's meets
+        it, and the results that are the object's own, with their addresses."""
         if len(self._plans) >= 256:
             self._plans.clear()
         d = SwigluDesc(DTYPE[self.dtype], FORMAT[self.fmt], self.rows, self.cols, ld, ld_h)
-        size = self._t.itemsize
-        plan = self._plans[key] = (ctypes.byref(d), _reach(self.rows, ld, self.cols, size),
-                                   _reach(self.rows, ld_h, self.cols, size), *own)
+        low, high = (_reach(self.rows, ld, self.cols, self._t.itemsize) for ld in (ld_in, ld_out))
+        plan = self._plans[key] = (getattr(self.lib, name), ctypes.byref(d), -low, high, *own,
+                                   *(0 if t is None else t.data_ptr() for t in own))
         return plan
 
     def _refuse(self, a, result, what):
@@ -719,14 +736,17 @@ class SwigluCkpt8:
                 raise ValueError("gate and up differ in their row strides")
             self._at_home(gate, up, *(() if out is None else (out,)))
             own, ldh = self._result("h", out, stream)
-            plan = self._remember(key, ld, ldh, own)
-        h = plan[3] if out is None else out
-        gp, up_, hp = gate.data_ptr(), up.data_ptr(), h.data_ptr()
-        if gp < hp + plan[2] and hp < gp + plan[1]:
+            plan = self._remember(key, "lq_swiglu_ckpt8", ld, ldh, ld, ldh, own)
+        call, ref, low, high, h, hp = plan
+        if out is not None:
+            h, hp = out, out.data_ptr()
+        gp, up_ = gate.data_ptr(), up.data_ptr()
+        if low < gp - hp < high:
             self._refuse(gate, h, "gate and h")
-        if up_ < hp + plan[2] and hp < up_ + plan[1]:
+        if low < up_ - hp < high:
             self._refuse(up, h, "up and h")
-        rc = self.lib.lq_swiglu_ckpt8(plan[0], gp, up_, hp, *self._kept, _stream_of(self._index, stream))
+        gc, gs, uc, us = self._kept
+        rc = call(ref, gp, up_, hp, gc, gs, uc, us, _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_swiglu_ckpt8", rc)
         return h
@@ -746,16 +766,20 @@ class SwigluCkpt8:
             if ld != ld1:
                 raise ValueError("dgate and dup differ in their row strides")
             self._at_home(dh, *(out or ()))
-            plan = self._remember(key, ld, ldh, own0, own1)
-        dg, du = (plan[3], plan[4]) if out is None else out
-        hp, gp, up = dh.data_ptr(), dg.data_ptr(), du.data_ptr()
-        if hp < gp + plan[1] and gp < hp + plan[2]:
+            plan = self._remember(key, "lq_swiglu_ckpt8_backward", ld, ldh, ldh, ld, own0, own1)
+        call, ref, low, high, dg, du, gp, up = plan
+        if out is not None:
+            dg, du = out
+            gp, up = dg.data_ptr(), du.data_ptr()
+            if abs(gp - up) < high and _share(dg, du):
+                raise ValueError("dgate and dup share memory")
+        hp = dh.data_ptr()
+        if low < hp - gp < high:
             self._refuse(dh, dg, "dh and dgate")
-        if hp < up + plan[1] and up < hp + plan[2]:
+        if low < hp - up < high:
             self._refuse(dh, du, "dh and dup")
-        if abs(gp - up) < plan[1] and _share(dg, du):
-            raise ValueError("dgate and dup share memory")
-        rc = self.lib.lq_swiglu_ckpt8_backward(plan[0], hp, *self._kept, gp, up, _stream_of(self._index, stream))
+        gc, gs, uc, us = self._kept
+        rc = call(ref, hp, gc, gs, uc, us, gp, up, _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_swiglu_ckpt8_backward", rc)
         return dg, du
