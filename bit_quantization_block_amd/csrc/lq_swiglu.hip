@@ -10,20 +10,27 @@
 // is written goes past the caches. Vector work was the bound before it was cut:
 // codes decoded by sub-word converts, rounded by one fused multiply-add, 16-bit
 // maxima two at a time, and no division to find a place (184 us backward with
-// 64-bit places, the library's exp and a divided sigmoid).
+// 64-bit places, the library's exp and a divided sigmoid). At 8192 x 11008 of
+// binary32: 237 us forward and 262 us backward, 5.3 and 4.8 TB/s (14.06 bytes an
+// element).
 #include "lq_linear.h"
 
 namespace lql {
 namespace {
 
-// 1 / (1 + exp(-g)), in binary32, short enough for the kernels to stay bound by
-// memory: exp(-g) = 2^t (1 + ln2 rest), with t = -g log2(e) rounded and its
-// remainder exact by fused multiply-adds over log2(e) in two parts. v_exp_f32 and
-// v_rcp_f32 are good to a unit in the last place, which with the sum's and the
-// products' roundings makes at most 7 * 2^-24 relative: two or three times the
-// library exp's and an IEEE division's, at a third of their instructions. An exp
-// that overflows gives 0.
+// 1 / (1 + exp(-g)), in binary32; an exp that overflows gives 0.
+// For 32-bit matrices the library's exp and an IEEE division: off by a unit in
+// exp's last place and the roundings of the sum and the quotient; the memory's time
+// hides them (237 and 262 us, and with the short form below too).
+// For 16-bit matrices, whose results keep 11 bits at most, a third of the
+// instructions, without which vector work would be the bound: exp(-g) = 2^t
+// (1 + ln2 rest), with t = -g log2(e) rounded and its remainder exact by fused
+// multiply-adds over log2(e) in two parts. v_exp_f32 and v_rcp_f32 are good to a
+// unit in the last place, which with the sum's and the products' roundings makes
+// at most 7 * 2^-24 relative.
+template <int DT>
 __device__ __forceinline__ float sigmoid(float g) {
+  if constexpr (DT == LQ_F32) return 1.0f / (1.0f + expf(-g));
   constexpr float hi = -1.4426950216293335f, lo = -1.925963e-08f, ln2 = 0.6931471805599453f;
   const float t = g * hi, rest = __builtin_fmaf(g, lo, __builtin_fmaf(g, hi, -t));
   const float e = __builtin_amdgcn_exp2f(t);
@@ -65,7 +72,7 @@ __global__ __launch_bounds__(256) void k_swiglu(const void* gate, const void* up
     }
     if (h) {
 #pragma unroll
-      for (int i = 0; i < 8; i++) g[i] = g[i] * sigmoid(g[i]) * u[i];
+      for (int i = 0; i < 8; i++) g[i] = g[i] * sigmoid<DT>(g[i]) * u[i];
       store8<DT>((T*)h + row * ldh, col, valid, g);
     }
   }
@@ -91,7 +98,7 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(const void* dh, int64_t
     decode4<F>(wu.y, su, u + 4);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const float s = sigmoid(g[i]);
+      const float s = sigmoid<DT>(g[i]);
       u[i] = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
       g[i] = d[i] * (g[i] * s);
     }

@@ -78,3 +78,38 @@ def test_a_call_on_a_stream_takes_memory_from_its_pool():
     z = other.forward(x, stream=0)
     torch.cuda.synchronize()
     assert z.data_ptr() == y.data_ptr() and torch.equal(z, want)
+
+
+def unit_in_last_place(t):
+    """Of binary32 numbers of the magnitudes in t (float64, normal as binary32)."""
+    return ((t.abs().view(torch.int64) >> 52) - 23 << 52).view(torch.float64)
+
+
+def silu_bound(g):
+    """What g / (1 + exp(-g)) in binary32 may be off: exp by a unit in its last place, the sum, the quotient and the product
+    with g by half of one each (evaluated at the exact values; 1% for the binades' edges being those of rounded ones)."""
+    e = torch.exp(-g)
+    s = 1 / (1 + e)
+    off = (unit_in_last_place(e) + 0.5 * unit_in_last_place(1 + e)) / (1 + e) * s + 0.5 * unit_in_last_place(s)
+    return (off * g.abs() + 0.5 * unit_in_last_place(g * s)) * 1.01
+
+
+@pytest.mark.parametrize("low,high", [(-80, -8), (-8, -1), (-1, 1), (1, 8), (8, 80)])
+def test_32_bit_activations_keep_32_bits(low, high):
+    """h with up = 1, and dup with dh = 1, of float32 matrices: as good as the library's exp and a division make them."""
+    say(f"[gpu] float32 silu {low}..{high}")
+    gen = torch.Generator(device="cuda").manual_seed(high)
+    g = torch.rand(4096, 4096, generator=gen, device="cuda") * (high - low) + low
+    g = torch.where(g.abs() < 2.0 ** -20, torch.ones_like(g), g)
+    one = torch.ones_like(g)
+    act = lq.SwigluCkpt8(4096, 4096, "f32")
+    h = act.forward(g, one).double()
+    gd = g.double()
+    assert ((h - gd / (1 + torch.exp(-gd))).abs() <= silu_bound(gd)).all()
+    act.backward(one)
+    _, du = act.backward(one)
+    codes, scales = act.gate.codes.view(4096, 4096), act.gate.scales.view(4096, 128).long()
+    g8 = codes.view(torch.int8).double() * ((scales - 127 + 1023) << 52).view(torch.float64).repeat_interleave(32, 1)
+    g8 = torch.where(g8 == 0, torch.full_like(g8, 2.0 ** -30), g8)       # du is 0 there
+    want = g8 / (1 + torch.exp(-g8))
+    assert ((du.double() - want).abs() <= silu_bound(g8) + (g8 == 2.0 ** -30) * 2.0 ** -30).all()
