@@ -19,7 +19,10 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 // Both gradients are matrix products A B over bfloat16 operands: E2M1 and INT8
 // values times a power of two have at most 7 significant bits, E4M3 values 4,
 // so the stored operand is exact in bfloat16 (8 bits; its exponents are
-// binary32's) and is converted once, on its way into LDS.
+// binary32's) and is converted once, on its way into LDS. (But below 2^-126
+// bfloat16 holds multiples of 2^-133 only. The scales end at 2^-127: E2M1's unit of
+// 2^-1 and INT8's of 1 stay above, E4M3's of 2^-9 does not for scales below
+// 2^-124, whose values the conversion rounds, half to even.)
 //   dgrad: A = dy [m, n], B = W [n, k]; the contraction runs along dy's rows
 //          and down W's columns
 //   wgrad: A = dy^T, B = x8 [m, k]; it runs down the columns of both

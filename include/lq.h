@@ -295,8 +295,11 @@ LQ_API int lq_call_kernels(const lq_desc* desc, int64_t rows, int64_t cols, uint
  * above (E2M1; INT8 in [-127,127], half to even; E4M3). A block that holds an
  * infinity or a NaN gets the NaN scale 0xFF and zero codes, and every result
  * computed from it is NaN. The products take the quantised values as they are
- * (E2M1, INT8 and E4M3 values times a power of two are exact in bfloat16; one
- * that rounding took to 2^128 is infinite) and add in binary32; results are
+ * (E2M1 and INT8 values times their scale are exact in bfloat16, in which the
+ * gradients take them, and so are E4M3 values with a scale of 2^-124 or more;
+ * with a smaller one they are rounded to bfloat16's subnormal numbers, multiples
+ * of 2^-133, half to even. A value that rounding took to 2^128 is infinite) and
+ * add in binary32; results are
  * rounded once, to nearest even, to the output type. A repeated
  * call gives the same bits. silu(g) = g / (1 + exp(-g)), its derivative
  * s (1 + g (1 - s)) with s = 1 / (1 + exp(-g)), in binary32.

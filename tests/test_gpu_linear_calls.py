@@ -1,10 +1,13 @@
 """Calls of the low-bit linear layer's classes as programs make them: a result as the next call's input, the gated unit in
-place."""
+place, streams; and the numbers at the ends of what they hold: float32 activations, the smallest scales."""
+import numpy as np
 import pytest
 import torch
 
 from bit_quantization_block_amd import lq
+from tests import linear_ref as R
 from tests.gpu_helpers import say
+from tests.test_linear_numbers_cpu import bfloat16
 
 pytestmark = pytest.mark.gpu
 T = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
@@ -113,3 +116,33 @@ def test_32_bit_activations_keep_32_bits(low, high):
     g8 = torch.where(g8 == 0, torch.full_like(g8, 2.0 ** -30), g8)       # du is 0 there
     want = g8 / (1 + torch.exp(-g8))
     assert ((du.double() - want).abs() <= silu_bound(g8) + (g8 == 2.0 ** -30) * 2.0 ** -30).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("e", [-110, -115, -117, -120, -126, -130, -135])
+def test_checkpoints_of_tiny_numbers(fmt, e):
+    """Scales at their lowest and a large dy: dw is 2^100 times each value as bfloat16 holds it, for E4M3 rounded to multiples
+    of 2^-133."""
+    m = k = 64
+    x = ((torch.rand(m, k, generator=torch.Generator().manual_seed(-e)) * 2 - 1) * 2.0 ** (e + 100)).double() * 2.0 ** -100
+    kept = lq.Ckpt8(m, k, fmt)
+    kept.save(x.float().cuda())
+    layer = lq.Mx4Linear(torch.zeros(m, k, device="cuda"), rows=m)
+    dw = layer.wgrad((torch.eye(m) * 2.0 ** 100).bfloat16().cuda(), kept).double().cpu().numpy()
+    x8 = R.quantise(x.float().numpy(), fmt)[2]
+    held = bfloat16(x8)
+    assert np.array_equal(held, x8) or (fmt == "e4m3" and e < -115)
+    assert np.array_equal(dw, held * 2.0 ** 100)
+
+
+def test_weights_of_tiny_numbers():
+    """E2M1 weights are exact down to the smallest scale, in both directions."""
+    n = 64
+    for e in (-110, -120, -126, -128):
+        w = ((torch.rand(n, n, generator=torch.Generator().manual_seed(-e)) * 2 - 1) * 2.0 ** (e + 100)).double() * 2.0 ** -100
+        w4 = R.quantise(w.float().numpy(), "e2m1")[2]
+        layer = lq.Mx4Linear(w.float().cuda(), rows=n, out="f32")
+        big = (torch.eye(n) * 2.0 ** 100).bfloat16().cuda()
+        assert np.array_equal(layer.dgrad(big).double().cpu().numpy(), w4 * 2.0 ** 100)
+        for rows in (1, 20, n):
+            assert np.array_equal(layer.forward(big[:rows]).double().cpu().numpy(), (w4 * 2.0 ** 100).T[:rows])
