@@ -542,20 +542,6 @@ void* scratch_for_current_device() {
   return g_scratch_ptr[dev];
 }
 
-// Installs a launch-plan recorder on this thread for the lifetime of the object.
-struct PlanScope {
-  PlanRecorder rec;
-  explicit PlanScope(char* buf, size_t bytes) {
-    rec.buf = (buf && bytes) ? buf : nullptr;
-    rec.cap = bytes;
-    rec.len = 0;
-    rec.count = 0;
-    if (rec.buf) rec.buf[0] = '\0';
-    g_plan = &rec;
-  }
-  ~PlanScope() { g_plan = nullptr; }
-};
-
 // Integer-vs-float pairs of the sweep table: (INT8, E4M3), (INT8, E5M2), (INT4, E2M1).
 constexpr int kPairInt[3] = {LQ_INT8, LQ_INT8, LQ_INT4};
 constexpr int kPairFp[3] = {LQ_E4M3, LQ_E5M2, LQ_E2M1};

@@ -515,6 +515,7 @@ hipError_t grad_tiled(GradArgs& g, hipStream_t s) {
   g.tm = (uint32_t)((rows + 64 * FM - 1) / (64 * FM));
   g.tn = (uint32_t)((g.k + 64 * FN - 1) / (64 * FN));
   const dim3 grid(g.tm * g.tn * g.parts);
+  if (lqd::g_plan) return plan(grid, 256, "k_grad<%d, %d, %d, %d, %d, %s>", KIND, F, OUT, FM, FN, lqd::tf(kMayBe && g.row % 8 != 0));
   if (kMayBe && g.row % 8 != 0) hipLaunchKernelGGL((k_grad<KIND, F, OUT, FM, FN, kMayBe>), grid, dim3(256), 0, s, g);
   else hipLaunchKernelGGL((k_grad<KIND, F, OUT, FM, FN, false>), grid, dim3(256), 0, s, g);
   return hipGetLastError();
@@ -528,8 +529,13 @@ hipError_t grad(GradArgs g, void* ws, hipStream_t s) {
   uint8_t* planes = (uint8_t*)ws;
   if (!reads_in_place(g.m, g.n, g.k, g.lddy)) {
     const int64_t ld = padded_columns(g.n);
-    hipLaunchKernelGGL(k_pad_rows, matrix_grid((ld + 511) / 512, g.m), dim3(256), 0, s, g.dy, g.m, g.n, g.lddy, (uint16_t*)ws, ld);
-    if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+    const dim3 grid = matrix_grid((ld + 511) / 512, g.m);
+    if (lqd::g_plan) {
+      plan(grid, 256, "k_pad_rows");
+    } else {
+      hipLaunchKernelGGL(k_pad_rows, grid, dim3(256), 0, s, g.dy, g.m, g.n, g.lddy, (uint16_t*)ws, ld);
+      if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+    }
     g.dy = (const uint16_t*)ws;
     g.lddy = g.row = ld;
     planes += (g.m * ld * 2 + 255) / 256 * 256;

@@ -6,13 +6,12 @@
 // every wave reads and writes contiguous runs and every block of
 // 16..256 elements lives in 1..16 neighbouring lanes.
 #pragma once
-#include <stdarg.h>
-#include <stdio.h>
 #include <string.h>
 
 #include <utility>
 
 #include "lq_device.h"
+#include "lq_plan.h"
 
 namespace lqd {
 
@@ -1051,40 +1050,7 @@ static __global__ void k_empty_result(lq_result* res) {
 }
 
 // ---------------------------------------------------------------- launchers
-// Launch plans: while a host thread has a PlanRecorder installed, every
-// launch wrapper appends the name of the kernel it would launch (as the HIP
-// runtime's demangler prints it, the name profilers report) and the grid
-// and block sizes, instead of launching. lq_call_kernels uses it to report the kernels
-// of a call from this dispatch code itself.
-struct PlanRecorder {
-  char* buf;      // may be null (count only)
-  size_t cap;     // bytes at buf
-  size_t len;     // bytes written, without the terminating NUL
-  int count;      // kernels recorded
-};
-extern thread_local PlanRecorder* g_plan;
-
-__attribute__((format(printf, 3, 4))) inline hipError_t plan_add(int nwg, int nthreads, const char* fmt, ...) {
-  PlanRecorder* r = g_plan;
-  char line[256];
-  va_list ap;
-  va_start(ap, fmt);
-  int n = vsnprintf(line, sizeof line, fmt, ap);
-  va_end(ap);
-  if (n < 0) n = 0;
-  char grid[32];
-  const int g = snprintf(grid, sizeof grid, "\t%d\t%d\n", nwg, nthreads);
-  if (r->buf && r->len + (size_t)n + (size_t)g < r->cap) {
-    memcpy(r->buf + r->len, line, (size_t)n);
-    memcpy(r->buf + r->len + n, grid, (size_t)g);
-    r->len += (size_t)n + (size_t)g;
-    r->buf[r->len] = '\0';
-  }
-  r->count++;
-  return hipSuccess;
-}
-inline const char* tf(bool b) { return b ? "true" : "false"; }
-
+// (with a plan being recorded, lq_plan.h, each appends its kernel instead of launching it)
 template <int DT, int F, int ODT, int MODE>
 hipError_t launch_flat(const Args& a, int nwg, hipStream_t s) {
   if (g_plan) return plan_add(nwg, kThreads, "void lqd::k_flat<%d, %d, %d, %d>(lqd::Args)", DT, F, ODT, MODE);

@@ -229,6 +229,22 @@ int lq_ckpt8_wgrad(const lq_linear_desc* d, const void* dy, const void* ckpt_cod
                                       (const float*)dw_in, (float*)dw, d->ld_out, ws, (hipStream_t)stream));
 }
 
+int lq_linear_kernels(const lq_linear_desc* d, int call, int also, char* names, size_t bytes) {
+  // (no buffer is touched: any aligned address stands for one)
+  void *const b = (void*)(uintptr_t)256, *const opt = also ? b : nullptr;
+  const size_t ws = ~(size_t)0;
+  lqd::PlanScope scope(names, bytes);
+  int rc = LQ_ERR_BAD_DESC;
+  switch (call) {
+    case LQ_CALL_QUANTIZE: rc = lq_mx4_quantize(d, b, b, b, opt, opt, nullptr); break;
+    case LQ_CALL_PRODUCT: rc = lq_mx4_product(d, b, b, b, b, b, b, ws, nullptr); break;
+    case LQ_CALL_LINEAR: rc = lq_mx4_linear(d, b, b, b, b, opt, opt, b, ws, nullptr); break;
+    case LQ_CALL_DGRAD: rc = lq_mx4_dgrad(d, b, b, b, b, b, ws, nullptr); break;
+    case LQ_CALL_WGRAD: rc = lq_ckpt8_wgrad(d, b, b, b, opt, b, b, ws, nullptr); break;
+  }
+  return rc < 0 ? rc : scope.rec.count;
+}
+
 static int check_swiglu(const lq_swiglu_desc* d) {
   if (!d) return LQ_ERR_NULL;
   if (!is_dtype(d->dtype) || d->ckpt_format < LQ_INT8 || d->ckpt_format > LQ_E3M2) return LQ_ERR_BAD_DESC;

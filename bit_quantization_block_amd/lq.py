@@ -29,7 +29,8 @@ EXPORTS = ("lq_quantize", "lq_dequantize", "lq_fake_quant_qsnr", "lq_hadamard_qu
            "lq_call_kernels", "lq_set_grid_limit", "lq_status_string", "lq_fake_quant_qsnr_static",
            "lq_mx4_codes_bytes", "lq_mx4_scales_bytes", "lq_ckpt8_codes_bytes", "lq_ckpt8_scales_bytes",
            "lq_linear_workspace_bytes", "lq_mx4_quantize", "lq_mx4_product", "lq_mx4_linear", "lq_mx4_dgrad",
-           "lq_ckpt8_wgrad", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward")
+           "lq_ckpt8_wgrad", "lq_linear_kernels", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward")
+LINEAR_CALL = {"quantize": 0, "product": 1, "linear": 2, "dgrad": 3, "wgrad": 4}
 # output bits of lq_call_kernels
 OUT = {"codes": 1, "scales": 2, "zeros": 4, "y": 8, "res": 16}
 
@@ -106,8 +107,9 @@ def load(path: str | None = None):
     L.lq_ckpt8_wgrad.argtypes = [lp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.lq_swiglu_ckpt8.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.lq_swiglu_ckpt8_backward.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.lq_linear_kernels.argtypes = [lp, ctypes.c_int, ctypes.c_int, ctypes.c_char_p, sz]
     for f in ("lq_mx4_quantize", "lq_mx4_product", "lq_mx4_linear", "lq_mx4_dgrad", "lq_ckpt8_wgrad",
-              "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward"):
+              "lq_linear_kernels", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward"):
         getattr(L, f).restype = ctypes.c_int
     L.lq_status_string.argtypes = [ctypes.c_int]
     L.lq_status_string.restype = ctypes.c_char_p
@@ -448,6 +450,22 @@ def _empty_for(stream, *size, dtype, device):
         return torch.empty(size, dtype=dtype, device=device)
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)):
         return torch.empty(size, dtype=dtype, device=device)
+
+
+def linear_kernels(call: str, m: int, n: int, k: int, in_dtype: str = "bf16", out_dtype: str = "bf16", fmt: str = "int8",
+                   also: bool = False, ld_in: int | None = None, lib=None) -> list:
+    """[(kernel, workgroups, threads per workgroup)] that a call of the linear layer would launch, in order. `call`: of
+    LINEAR_CALL; `also`: with a checkpoint, or a dw_in; `ld_in`: its input's row stride, if rows are apart."""
+    lib = lib or load()
+    ins, outs = {"dgrad": (n, k), "wgrad": (n, k)}.get(call, (k, n))
+    d = LinearDesc(DTYPE[in_dtype], DTYPE[out_dtype], FORMAT[fmt], 0, m, n, k, ins if ld_in is None else ld_in, outs)
+    buf = ctypes.create_string_buffer(4096)
+    count = lib.lq_linear_kernels(ctypes.byref(d), LINEAR_CALL[call], int(also), buf, len(buf))
+    if count < 0:
+        raise LQError("lq_linear_kernels", count)
+    lines = [line.rsplit("\t", 2) for line in buf.value.decode().splitlines()]
+    assert len(lines) == count
+    return [(name, int(groups), int(threads)) for name, groups, threads in lines]
 
 
 class Ckpt8:

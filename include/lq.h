@@ -366,6 +366,21 @@ LQ_API int lq_mx4_dgrad(const lq_linear_desc* desc, const void* dy, const void* 
 LQ_API int lq_ckpt8_wgrad(const lq_linear_desc* desc, const void* dy, const void* ckpt_codes, const void* ckpt_scales,
                           const void* dw_in, void* dw, void* ws, size_t ws_bytes, void* stream);
 
+/* The kernels that a call with this descriptor would launch, as
+ * lq_call_kernels reports them: one line each, the name with its template
+ * arguments, a tab, the number of workgroups, a tab, the threads of one. `also`:
+ * the call keeps a checkpoint (LQ_CALL_QUANTIZE, LQ_CALL_LINEAR) or has a dw_in
+ * (LQ_CALL_WGRAD). Returns their number, or the call's LQ_ERR_*
+ * (LQ_ERR_BAD_DESC for an unknown call). */
+typedef enum {
+  LQ_CALL_QUANTIZE = 0, /* lq_mx4_quantize */
+  LQ_CALL_PRODUCT = 1,  /* lq_mx4_product */
+  LQ_CALL_LINEAR = 2,   /* lq_mx4_linear */
+  LQ_CALL_DGRAD = 3,    /* lq_mx4_dgrad */
+  LQ_CALL_WGRAD = 4     /* lq_ckpt8_wgrad */
+} lq_linear_call;
+LQ_API int lq_linear_kernels(const lq_linear_desc* desc, int call, int also, char* names, size_t bytes);
+
 typedef struct {
   int32_t dtype;       /* lq_dtype of every matrix */
   int32_t ckpt_format; /* LQ_INT8 or LQ_E4M3 */
