@@ -515,7 +515,7 @@ hipError_t grad_tiled(GradArgs& g, hipStream_t s) {
   g.tm = (uint32_t)((rows + 64 * FM - 1) / (64 * FM));
   g.tn = (uint32_t)((g.k + 64 * FN - 1) / (64 * FN));
   const dim3 grid(g.tm * g.tn * g.parts);
-  if (lqd::g_plan) return plan(grid, 256, "k_grad<%d, %d, %d, %d, %d, %s>", KIND, F, OUT, FM, FN, lqd::tf(kMayBe && g.row % 8 != 0));
+  if (lqd::g_plan) return LQ_PLAN(grid, 256, "k_grad<%d, %d, %d, %d, %d, %s>", KIND, F, OUT, FM, FN, lqd::tf(kMayBe && g.row % 8 != 0));
   if (kMayBe && g.row % 8 != 0) hipLaunchKernelGGL((k_grad<KIND, F, OUT, FM, FN, kMayBe>), grid, dim3(256), 0, s, g);
   else hipLaunchKernelGGL((k_grad<KIND, F, OUT, FM, FN, false>), grid, dim3(256), 0, s, g);
   return hipGetLastError();
@@ -531,7 +531,7 @@ hipError_t grad(GradArgs g, void* ws, hipStream_t s) {
     const int64_t ld = padded_columns(g.n);
     const dim3 grid = matrix_grid((ld + 511) / 512, g.m);
     if (lqd::g_plan) {
-      plan(grid, 256, "k_pad_rows");
+      (void)LQ_PLAN(grid, 256, "k_pad_rows");
     } else {
       hipLaunchKernelGGL(k_pad_rows, grid, dim3(256), 0, s, g.dy, g.m, g.n, g.lddy, (uint16_t*)ws, ld);
       if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;

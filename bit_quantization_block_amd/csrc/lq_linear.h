@@ -281,10 +281,7 @@ inline size_t planes_bytes(const Split& c, int64_t rows, int64_t cols) {
 
 // ------------------------------------------------------------ launchers
 // Instead of launching, the kernel's name and its template arguments for a plan being recorded (lq_plan.h).
-template <class... A>
-hipError_t plan(dim3 grid, int threads, const char* name, A... args) {
-  return lqd::plan_add((int64_t)grid.x * grid.y, threads, name, args...);
-}
+#define LQ_PLAN(grid, threads, ...) lqd::plan_add((int64_t)(grid).x * (grid).y, threads, __VA_ARGS__)
 // (lq_mx4.hip, lq_grad.hip, lq_swiglu.hip; arguments checked by lq_linear.hip)
 hipError_t launch_mx4_quantize(int in_dtype, int ckpt_format, const void* x, int64_t m, int64_t k, int64_t ldx,
                                void* codes, void* scales, void* ckpt_codes, void* ckpt_scales, hipStream_t s);

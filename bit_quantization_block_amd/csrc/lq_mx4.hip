@@ -554,7 +554,7 @@ template <int DT>
 hipError_t quantize_dt(int format, const void* x, int64_t m, int64_t k, int64_t ldx, void* codes, void* scales,
                        void* ck, void* cks, hipStream_t s) {
   const dim3 g = matrix_grid((mx4_groups(k) + 3) / 4, m);
-  if (lqd::g_plan) return plan(g, 256, "k_mx4_quantize<%d, %d>", DT, format);
+  if (lqd::g_plan) return LQ_PLAN(g, 256, "k_mx4_quantize<%d, %d>", DT, format);
   if (format == LQ_INT8)
     hipLaunchKernelGGL((k_mx4_quantize<DT, LQ_INT8>), g, dim3(256), 0, s, x, m, k, ldx, (uint8_t*)codes,
                        (uint8_t*)scales, (uint8_t*)ck, (uint8_t*)cks);
@@ -572,7 +572,7 @@ hipError_t product_tiled(const void* a, const void* as, const void* w, const voi
   const int64_t tm = (m + 64 * FM - 1) / (64 * FM), tn = (n + 64 * FN - 1) / (64 * FN), tiles = tm * tn * parts;
   const int64_t most = (int64_t)compute_units() * (int)(163840 / sizeof(ProductLds<FM, FN>));
   const dim3 grid((unsigned)(tiles < most ? tiles : most));
-  if (lqd::g_plan) return plan(grid, 256, "k_mx4_product<%d, %d, %d>", OUT, FM, FN);
+  if (lqd::g_plan) return LQ_PLAN(grid, 256, "k_mx4_product<%d, %d, %d>", OUT, FM, FN);
   hipLaunchKernelGGL((k_mx4_product<OUT, FM, FN>), grid, dim3(256), 0, s,
                      (const uint8_t*)a, (const uint8_t*)as, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy,
                      (uint32_t)tm, (uint32_t)tn, (uint32_t)parts, part_groups);
@@ -586,7 +586,7 @@ hipError_t few(const void* x, int64_t ldx, const void* xs, const void* w, const 
   // 11.2; 8 x 11008 x 4096 10.5 or 11.2; but 1 x 4096 x 11008 9.8 or 8.6)
   const int r = CT < 4 && n >= 32 * (int64_t)compute_units() ? 2 : 1;
   const dim3 grid((unsigned)((n + 16 * r - 1) / (16 * r)));
-  if (lqd::g_plan) return plan(grid, 64 * kFewWaves, "k_mx4_few<%d, %d, %d, %d>", SRC, OUT, r, CT);
+  if (lqd::g_plan) return LQ_PLAN(grid, 64 * kFewWaves, "k_mx4_few<%d, %d, %d, %d>", SRC, OUT, r, CT);
   if (r == 2) {
     hipLaunchKernelGGL((k_mx4_few<SRC, OUT, CT < 4 ? 2 : 1, CT>), grid, dim3(64 * kFewWaves), 0, s, x, ldx,
                        (const uint8_t*)xs, (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy);
@@ -677,7 +677,7 @@ __global__ __launch_bounds__(256) void k_join(int64_t rows, int64_t cols, int pa
 hipError_t launch_join(int64_t rows, int64_t cols, int dtype, int parts, const float* planes, const float* in, void* y,
                        int64_t ldy, hipStream_t s) {
   const dim3 g = matrix_grid((cols + 255) / 256, rows);
-  if (lqd::g_plan) return plan(g, 256, "k_join<%d>", dtype);
+  if (lqd::g_plan) return LQ_PLAN(g, 256, "k_join<%d>", dtype);
   if (dtype == LQ_F32) hipLaunchKernelGGL((k_join<LQ_F32>), g, dim3(256), 0, s, rows, cols, parts, planes, in, y, ldy);
   else if (dtype == LQ_BF16) hipLaunchKernelGGL((k_join<LQ_BF16>), g, dim3(256), 0, s, rows, cols, parts, planes, in, y, ldy);
   else hipLaunchKernelGGL((k_join<LQ_F16>), g, dim3(256), 0, s, rows, cols, parts, planes, in, y, ldy);
@@ -686,7 +686,7 @@ hipError_t launch_join(int64_t rows, int64_t cols, int dtype, int parts, const f
 
 hipError_t launch_constant(int64_t rows, int64_t cols, int dtype, const void* in, void* y, int64_t ldy, hipStream_t s) {
   const dim3 g = matrix_grid((cols + 63) / 64, rows);
-  if (lqd::g_plan) return plan(g, 256, "k_constant<%s>", dtype == LQ_F32 ? "float" : "unsigned short");
+  if (lqd::g_plan) return LQ_PLAN(g, 256, "k_constant<%s>", dtype == LQ_F32 ? "float" : "unsigned short");
   if (dtype == LQ_F32)
     hipLaunchKernelGGL((k_constant<float>), g, dim3(256), 0, s, rows, cols, (const float*)in, (float*)y, ldy);
   else

@@ -59,7 +59,8 @@ class GatedMlp:
             g.zero_()
 
     def call(self, x, act):
-        """y for any number of rows, keeping nothing; `act` is a SwigluCkpt8 of that many rows."""
+        """y for any number of rows, which leaves what forward() kept as it is; `act` is a SwigluCkpt8 of that many rows,
+        whose own checkpoints it fills."""
         return self.down.forward(act.forward(self.gate.forward(x), self.up.forward(x)))
 
 

@@ -1,5 +1,7 @@
 """Calls of the low-bit linear layer's classes as programs make them: a result as the next call's input, the gated unit in
 place, streams; and the numbers at the ends of what they hold: float32 activations, the smallest scales."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -7,6 +9,7 @@ import torch
 from bit_quantization_block_amd import lq
 from tests import linear_ref as R
 from tests.gpu_helpers import say
+from tests.test_gpu_linear_tiles import example
 from tests.test_linear_numbers_cpu import bfloat16
 
 pytestmark = pytest.mark.gpu
@@ -146,3 +149,42 @@ def test_weights_of_tiny_numbers():
         assert np.array_equal(layer.dgrad(big).double().cpu().numpy(), w4 * 2.0 ** 100)
         for rows in (1, 20, n):
             assert np.array_equal(layer.forward(big[:rows]).double().cpu().numpy(), (w4 * 2.0 ** 100).T[:rows])
+
+
+def test_gated_unit_that_writes_h_or_checkpoints_only():
+    """The C call without checkpoints (inference) and without h: what it does write is what the whole call writes."""
+    lib = lq.load()
+    for dtype in ("bf16", "f16", "f32"):
+        for fmt in ("int8", "e4m3"):
+            for rows, cols in ((1, 40), (5, 33), (130, 2050)):
+                g, u = (random(rows, cols, dtype, s) for s in (1, 2))
+                act = lq.SwigluCkpt8(rows, cols, dtype, fmt)
+                h = act.forward(g, u)
+                d = lq.SwigluDesc(lq.DTYPE[dtype], lq.FORMAT[fmt], rows, cols, cols, cols + 1)
+                alone = torch.full((rows, cols + 1), 55.0, dtype=T[dtype], device="cuda")
+                args = [ctypes.byref(d), g.data_ptr(), u.data_ptr()]
+                assert lib.lq_swiglu_ckpt8(*args, alone.data_ptr(), None, None, None, None, lq._stream(None)) == 0
+                assert torch.equal(alone[:, :cols], h) and (alone[:, cols:] == 55).all()
+                kept = [torch.zeros_like(t) for c in (act.gate, act.up) for t in (c.codes, c.scales)]
+                assert lib.lq_swiglu_ckpt8(*args, None, *[t.data_ptr() for t in kept], lq._stream(None)) == 0
+                sizes = [lib.lq_ckpt8_codes_bytes(rows, cols), lib.lq_ckpt8_scales_bytes(rows, cols)] * 2
+                whole = [t for c in (act.gate, act.up) for t in (c.codes, c.scales)]
+                assert all(torch.equal(a[:n], b[:n]) for a, b, n in zip(kept, whole, sizes))
+
+
+def test_a_call_of_the_example_leaves_what_forward_kept():
+    """One token between forward() and backward(): the gradients are those without it. The call's own unit does keep its
+    gate and up."""
+    ex = example()
+    x, dy = random(40, 128, "bf16", 1), random(40, 128, "bf16", 2, 0.1)
+    got = []
+    for between in (False, True):
+        mlp = ex.GatedMlp(ex.weights(128, 256, 1), 40)
+        mlp.forward(x)
+        if between:
+            act = lq.SwigluCkpt8(1, 256)
+            before = act.gate.codes.clone()
+            mlp.call(x[:1], act)
+            assert not torch.equal(act.gate.codes, before)
+        got.append([mlp.backward(dy).clone(), *mlp.grads])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
