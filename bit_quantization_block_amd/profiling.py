@@ -33,15 +33,39 @@ def _code_only(text: str) -> str:
     return " ".join(text.split())
 
 
-def kernel_source_digest() -> str:
-    """Digest of everything that decides the kernels' code (comments aside)."""
+# Sources of the linear layer's kernels; every other file in csrc/ is the fake-quant path's or the ceilings'.
+LINEAR_SOURCES = ("lq_linear.h", "lq_linear.hip", "lq_mx4.hip", "lq_grad.hip", "lq_swiglu.hip")
+SHARED_SOURCES = ("lq_device.h", "lq_plan.h")
+
+
+def _header_types(text: str, path: str) -> str:
+    """The constants and types of lq.h that a path's kernels are compiled with: a new function or another path's
+    descriptor changes none of them."""
+    text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
+    out = re.findall(r"^#define LQ_\w+ .*$", text, flags=re.M)
+    for body, name in re.findall(r"typedef (?:struct|enum)\s*\{([^}]*)\}\s*(\w+);", text):
+        if name.startswith(("lq_linear", "lq_swiglu")) <= (path == "linear"):
+            out.append(name + " " + body)
+    return _code_only("\n".join(out))
+
+
+def kernel_source_digest(path: str = "fake_quant", root: str = ROOT) -> str:
+    """Digest of everything that decides the code of a path's kernels (comments aside): its sources, the header's types, the
+    compiler's flags. Paths: fake_quant (with the ceilings) and linear. What one path's sources become leaves the other's
+    digest, and the profiles that carry it, as they are."""
+    from . import build
+
     h = hashlib.sha256()
-    files = sorted(glob.glob(os.path.join(ROOT, "bit_quantization_block_amd", "csrc", "*")))
-    files += [os.path.join(ROOT, "bit_quantization_block_amd", "build.py"), os.path.join(ROOT, "include", "lq.h")]
-    for p in files:
-        with open(p, encoding="utf-8") as f:
-            h.update(os.path.basename(p).encode())
-            h.update(_code_only(f.read()).encode())
+    csrc = os.path.join(root, "bit_quantization_block_amd", "csrc")
+    for p in sorted(glob.glob(os.path.join(csrc, "*"))):
+        name = os.path.basename(p)
+        if name in SHARED_SOURCES or (name in LINEAR_SOURCES) == (path == "linear"):
+            with open(p, encoding="utf-8") as f:
+                h.update(name.encode())
+                h.update(_code_only(f.read()).encode())
+    with open(os.path.join(root, "include", "lq.h"), encoding="utf-8") as f:
+        h.update(_header_types(f.read(), path).encode())
+    h.update(" ".join(build.FLAGS).encode())
     return h.hexdigest()[:16]
 
 
