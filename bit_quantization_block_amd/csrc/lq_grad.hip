@@ -11,7 +11,6 @@ namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
@@ -527,7 +526,7 @@ hipError_t grad_tile(int tile, GradArgs& g, hipStream_t s) {
 template <int KIND, int F, int OUT>
 hipError_t grad(GradArgs g, void* ws, hipStream_t s) {
   uint8_t* planes = (uint8_t*)ws;
-  if (!reads_in_place(g.m, g.n, g.k, g.lddy)) {
+  if (!reads_in_place(g.m, g.n, g.lddy)) {
     const int64_t ld = padded_columns(g.n);
     const dim3 grid = matrix_grid((ld + 511) / 512, g.m);
     if (lqd::g_plan) {

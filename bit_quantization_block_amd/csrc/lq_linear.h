@@ -246,7 +246,7 @@ inline dim3 matrix_grid(int64_t across, int64_t rows) {
 //    that ends the last row's loads (n odd) and the second half of one of memory:
 //    the load's word would reach past the matrix, perhaps into a page that is not
 //    there.
-inline bool reads_in_place(int64_t m, int64_t n, int64_t k, int64_t lddy) {
+inline bool reads_in_place(int64_t m, int64_t n, int64_t lddy) {
   if (lddy > 1 << 21) return false;
   if (n % 8 == 0 && lddy % 8 == 0) return true;
   if (n % 2 != 0 && ((m - 1) * lddy + n) % 2 == 0) return false;

@@ -141,7 +141,7 @@ size_t lq_linear_workspace_bytes(const lq_linear_desc* d) {
   // the most of: the forward call's operand and its parts' sums; a gradient
   // call's padded dy and its parts' sums
   const size_t forward = operand_bytes(d) + planes_bytes(split_product(d->m, d->n, d->k, d->out_dtype), d->m, d->n);
-  const size_t dy = !reads_in_place(d->m, d->n, d->k, d->ld_in) ? round256((size_t)(d->m * padded_columns(d->n)) * 2) : 0;
+  const size_t dy = !reads_in_place(d->m, d->n, d->ld_in) ? round256((size_t)(d->m * padded_columns(d->n)) * 2) : 0;
   const size_t dx = planes_bytes(split_dgrad(d->m, d->n, d->k), d->m, d->k);
   const size_t dw0 = planes_bytes(split_wgrad(d->m, d->n, d->k, false), d->n, d->k);
   const size_t dw1 = planes_bytes(split_wgrad(d->m, d->n, d->k, true), d->n, d->k);

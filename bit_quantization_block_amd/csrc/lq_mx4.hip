@@ -388,7 +388,6 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
 // W, x came behind all of it: 4.9, 7.7, 10.2 and 10.5 us. Loads of twice as many
 // groups in flight cost the registers of a third of the waves: 8.6 for the 7.7.
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef uint16_t v2u __attribute__((ext_vector_type(2)));
 constexpr int kOperand = -1;
 constexpr int kFewWaves = 8;
 
@@ -582,8 +581,9 @@ template <int SRC, int OUT, int CT>
 hipError_t few(const void* x, int64_t ldx, const void* xs, const void* w, const void* ws, int64_t m, int64_t n, int64_t k,
                void* y, int64_t ldy, hipStream_t s) {
   // 32 rows of W a workgroup where that leaves one for each compute unit, else 16 (W read from memory, one call after
-  // another in a graph, when x still came after it: 1 x 8192 x 8192 10.2 us, with 16 rows 10.8; 1 x 16384 x 4096 9.6 or
-  // 11.2; 8 x 11008 x 4096 10.5 or 11.2; but 1 x 4096 x 11008 9.8 or 8.6)
+  // another in a graph: 1 x 8192 x 4096 5.6 us, with 16 rows 6.2; 1 x 11008 x 4096 7.7 or 8.5; 8 x 11008 x 4096 9.2 or
+  // 11.5; 24 x 8192 x 4096 9.4 or 11.7; but 1 x 4096 x 4096 4.6 or 4.3, 1 x 4096 x 11008 9.3 or 7.6, 24 x 4096 x 4096
+  // 8.7 or 7.8)
   const int r = CT < 4 && n >= 32 * (int64_t)compute_units() ? 2 : 1;
   const dim3 grid((unsigned)((n + 16 * r - 1) / (16 * r)));
   if (lqd::g_plan) return LQ_PLAN(grid, 64 * kFewWaves, "k_mx4_few<%d, %d, %d, %d>", SRC, OUT, r, CT);
