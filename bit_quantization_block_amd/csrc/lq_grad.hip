@@ -37,13 +37,15 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 // its products, a few instructions at a time, so that the matrix cores are
 // never without work; one barrier a step.
 //
-// dx 8192 x 11008 x 4096 534 to 620 us (1.2 to 1.4 PFLOP/s), dw from E4M3 583 us
+// dx 8192 x 11008 x 4096 506 to 620 us (1.2 to 1.5 PFLOP/s), dw from E4M3 582 us
 // (1.27), from INT8 650 us (1.14; twice the vector instructions to convert it). The
 // library's bf16 product, all operands in memory at 2 bytes, takes 574 us for the
 // first and 836 us for dw's order of operands, and 8192^3 at 1.2 to 1.3 PFLOP/s.
-// Power bounds the large ones: 72% of the cycles are the matrix cores', at 1.8 of
-// 2.4 GHz. The 128 x 128 tile is bound by LDS and by what one wave on a SIMD can
-// issue between its products: 1024 x 4096 x 4096 38 us, where the library takes 42.
+// The large dx keeps the matrix cores busy 72% of the cycles, at 1.8 of 2.4 GHz. The
+// 128 x 128 tile with one workgroup a compute unit keeps them busy 31%, LDS 40% and
+// vector issue 8%: one wave on a SIMD has no other's work for its waits. 1024 x 4096
+// x 4096 35 us, where the library takes 42; dw of those sizes, in 256 x 256 tiles,
+// 41 us (23% busy: 16 steps, and then 256 KB of results a compute unit).
 enum Kind { kDgrad, kWgrad };
 constexpr int kStep = 64;
 

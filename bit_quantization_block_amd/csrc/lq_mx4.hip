@@ -56,10 +56,11 @@ __global__ __launch_bounds__(256) void k_mx4_quantize(const void* x, int64_t m, 
 // in LDS, and a tile's results leave through a part of LDS of their own.
 //
 // 8192 x 4096 x 11008 163 us (4.5 PFLOP/s), 8192 x 8192 x 8192 271 us (4.1), 8192
-// x 11008 x 4096 185 to 203 us (3.6 to 4.0; 5.4 tiles a compute unit take 6 turns,
-// and each turn writes 32 MB). Power bounds the large ones: a loop of nothing but
-// these products on random operands reaches 5.8 PFLOP/s at 1.4 to 1.7 GHz, and
-// here, with the matrix cores busy half of the cycles, the clock is 1.9 of 2.4 GHz.
+// x 11008 x 4096 177 to 200 us (3.7 to 4.2; 5.4 tiles a compute unit take 6 turns,
+// and each turn writes 32 MB). A loop of nothing but these products on random
+// operands reaches 5.8 PFLOP/s at 1.4 to 1.7 GHz, where power holds it; here the
+// matrix cores are busy 46% of the cycles at 1.9 GHz: what is missing is the last
+// turn, and work beside a tile's end (6 of its 33 us).
 // 256 x 256 tiles read each operand half as often as 128 x 128 ones; those, and 64
 // x 64, are for products of few tiles (2048 x 4096 x 4096: 23 us against 30).
 constexpr int kStages = 4;

@@ -521,7 +521,8 @@ class Mx4Linear:
     one layer share its buffers and workspace: on two streams at a time, use two
     layers; a stream other than the one on which the layer was made, or last
     called, waits for that one first. `stream` is a stream's handle; tensors
-    given to a call on it are kept by the caller until it is done."""
+    given to a call on it are kept by the caller until it is done. Tensors have
+    contiguous rows of any stride and start at a multiple of 16 bytes."""
 
     def __init__(self, w, rows: int, dtype: str = "bf16", out: str = "bf16", lib=None):
         import torch
