@@ -1,0 +1,103 @@
+// lq_layers.hip — C ABI of the norm with an 8-bit checkpoint (declared in
+// include/lq.h): argument checks and workspace sizes. Every check runs before the
+// first launch, so a call that fails writes nothing.
+#include <stddef.h>
+#include <stdint.h>
+
+#include "lq_linear.h"
+
+using namespace lql;
+
+namespace {
+
+bool aligned(const void* p) { return ((uintptr_t)p & 15u) == 0u; }
+template <class... P>
+bool all_aligned(P... p) {
+  return (aligned(p) && ...);
+}
+bool is_dtype(int d) { return d == LQ_F32 || d == LQ_BF16 || d == LQ_F16; }
+bool is_ckpt_format(int f) { return f == LQ_INT8 || f == LQ_E4M3; }
+bool is_side(int64_t v) { return v >= 0 && v <= 0x7FFFFFFF; }
+bool is_stride(int64_t ld, int64_t cols) { return ld >= cols && ld <= (int64_t)1 << 31; }
+int status_of(hipError_t e) { return e == hipSuccess ? LQ_OK : LQ_ERR_HIP; }
+
+// ------------------------------------------------------------ the norm
+int check_norm(const lq_norm_desc* d) {
+  if (!d) return LQ_ERR_NULL;
+  if (!is_dtype(d->dtype) || !is_dtype(d->weight_dtype) || d->ckpt_format < LQ_INT8 || d->ckpt_format > LQ_E3M2)
+    return LQ_ERR_BAD_DESC;
+  if (!(d->eps >= 0.0f) || d->eps > 3.4e38f) return LQ_ERR_BAD_DESC;
+  if (!is_ckpt_format(d->ckpt_format) || (d->weight_dtype != d->dtype && d->weight_dtype != LQ_F32))
+    return LQ_ERR_UNSUPPORTED;
+  if (!is_side(d->rows) || !is_side(d->cols)) return LQ_ERR_SHAPE;
+  if (!is_stride(d->ld_x, d->cols) || !is_stride(d->ld_residual, d->cols) || !is_stride(d->ld_h, d->cols) ||
+      !is_stride(d->ld_y, d->cols))
+    return LQ_ERR_SHAPE;
+  if (d->cols > kNormColumns) return LQ_ERR_UNSUPPORTED;
+  return LQ_OK;
+}
+NormArgs norm_args(const lq_norm_desc* d) {
+  NormArgs a = {};
+  a.rows = d->rows;
+  a.cols = d->cols;
+  a.ldx = d->ld_x;
+  a.ldr = d->ld_residual;
+  a.ldh = d->ld_h;
+  a.ldy = d->ld_y;
+  a.eps = d->eps;
+  a.wide = d->weight_dtype == LQ_F32;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lq_rmsnorm(const lq_norm_desc* d, const void* x, const void* residual, const void* weight, void* h, void* y,
+               void* ckpt_codes, void* ckpt_scales, void* rs, void* stream) {
+  const int rc = check_norm(d);
+  if (rc) return rc;
+  if (!ckpt_codes != !ckpt_scales) return LQ_ERR_NULL;
+  if (d->rows == 0 || d->cols == 0) return LQ_OK;
+  if (!x || !weight || (!h && !y && !ckpt_codes && !rs)) return LQ_ERR_NULL;
+  if (!all_aligned(x, residual, weight, (const void*)h, (const void*)y, (const void*)ckpt_codes,
+                   (const void*)ckpt_scales, (const void*)rs))
+    return LQ_ERR_ALIGN;
+  NormArgs a = norm_args(d);
+  a.x = x;
+  a.r = residual;
+  a.w = weight;
+  a.h = h;
+  a.y = y;
+  a.codes = (uint8_t*)ckpt_codes;
+  a.scales = (uint8_t*)ckpt_scales;
+  a.rs = (float*)rs;
+  return status_of(launch_rmsnorm(d->dtype, d->ckpt_format, a, (hipStream_t)stream));
+}
+
+size_t lq_rmsnorm_workspace_bytes(const lq_norm_desc* d) {
+  if (check_norm(d)) return 0;
+  const size_t b = d->rows > 0 ? (size_t)(norm_planes(d->rows, d->cols) * plane_stride(d->cols)) * 4 : 0;
+  return b ? b : 256;
+}
+
+int lq_rmsnorm_backward(const lq_norm_desc* d, const void* dy, const void* dh, const void* h, const void* weight,
+                        const void* rs, void* dx, const void* dw_in, void* dw, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_norm(d);
+  if (rc) return rc;
+  if (d->cols == 0 || (d->rows == 0 && !dw)) return LQ_OK;
+  if (d->rows > 0 && (!dy || !h || !weight || !rs || !dx)) return LQ_ERR_NULL;
+  if (!all_aligned(dy, dh, h, weight, rs, (const void*)dx, dw_in, (const void*)dw, (const void*)ws)) return LQ_ERR_ALIGN;
+  if (dw && (!ws || ws_bytes < lq_rmsnorm_workspace_bytes(d))) return LQ_ERR_WORKSPACE;
+  NormArgs a = norm_args(d);
+  a.x = dy;
+  a.r = dh;
+  a.h = const_cast<void*>(h);
+  a.w = weight;
+  a.rs = (float*)const_cast<void*>(rs);
+  a.y = dx;
+  a.planes = dw ? (float*)ws : nullptr;
+  return status_of(launch_rmsnorm_backward(d->dtype, a, (const float*)dw_in, (float*)dw, (hipStream_t)stream));
+}
+
+}  // extern "C"

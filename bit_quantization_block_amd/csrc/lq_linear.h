@@ -315,4 +315,20 @@ hipError_t launch_swiglu_backward(int dtype, int format, const void* dh, int64_t
                                   const void* gc, const void* gs, const void* uc, const void* us, void* dgate,
                                   void* dup, int64_t ld, hipStream_t s);
 
+// The norm (lq_rmsnorm.hip; arguments checked by lq_layers.hip). Backward, x is dy, r is dh and y is dx, and without
+// dw there are no planes.
+struct NormArgs {
+  const void *x, *r, *w;
+  void *h, *y;
+  uint8_t *codes, *scales;
+  float *rs, *planes;
+  int64_t rows, cols, ldx, ldr, ldh, ldy;
+  float eps;
+  bool wide;   // w is binary32
+};
+constexpr int64_t kNormColumns = 16384;
+int64_t norm_planes(int64_t rows, int64_t cols);
+hipError_t launch_rmsnorm(int dtype, int format, const NormArgs& a, hipStream_t s);
+hipError_t launch_rmsnorm_backward(int dtype, const NormArgs& a, const float* dw_in, float* dw, hipStream_t s);
+
 }  // namespace lql

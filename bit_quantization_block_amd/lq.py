@@ -29,7 +29,8 @@ EXPORTS = ("lq_quantize", "lq_dequantize", "lq_fake_quant_qsnr", "lq_hadamard_qu
            "lq_call_kernels", "lq_set_grid_limit", "lq_status_string", "lq_fake_quant_qsnr_static",
            "lq_mx4_codes_bytes", "lq_mx4_scales_bytes", "lq_ckpt8_codes_bytes", "lq_ckpt8_scales_bytes",
            "lq_linear_workspace_bytes", "lq_mx4_quantize", "lq_mx4_product", "lq_mx4_linear", "lq_mx4_dgrad",
-           "lq_ckpt8_wgrad", "lq_linear_kernels", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward")
+           "lq_ckpt8_wgrad", "lq_linear_kernels", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward",
+           "lq_rmsnorm", "lq_rmsnorm_workspace_bytes", "lq_rmsnorm_backward")
 LINEAR_CALL = {"quantize": 0, "product": 1, "linear": 2, "dgrad": 3, "wgrad": 4}
 # output bits of lq_call_kernels
 OUT = {"codes": 1, "scales": 2, "zeros": 4, "y": 8, "res": 16}
@@ -60,6 +61,11 @@ class LinearDesc(ctypes.Structure):
 class SwigluDesc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("ckpt_format", ctypes.c_int32)] + \
                [(n, ctypes.c_int64) for n in ("rows", "cols", "ld", "ld_h")]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "weight_dtype", "ckpt_format")] + [("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("rows", "cols", "ld_x", "ld_residual", "ld_h", "ld_y")]
 
 
 _lib = None
@@ -107,6 +113,13 @@ def load(path: str | None = None):
     L.lq_ckpt8_wgrad.argtypes = [lp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.lq_swiglu_ckpt8.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.lq_swiglu_ckpt8_backward.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp]
+    np_ = ctypes.POINTER(NormDesc)
+    L.lq_rmsnorm.argtypes = [np_, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.lq_rmsnorm.restype = ctypes.c_int
+    L.lq_rmsnorm_workspace_bytes.argtypes = [np_]
+    L.lq_rmsnorm_workspace_bytes.restype = sz
+    L.lq_rmsnorm_backward.argtypes = [np_, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.lq_rmsnorm_backward.restype = ctypes.c_int
     L.lq_linear_kernels.argtypes = [lp, ctypes.c_int, ctypes.c_int, ctypes.c_char_p, sz]
     for f in ("lq_mx4_quantize", "lq_mx4_product", "lq_mx4_linear", "lq_mx4_dgrad", "lq_ckpt8_wgrad",
               "lq_linear_kernels", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward"):
@@ -485,6 +498,7 @@ class Ckpt8:
         self.scales = torch.empty(max(16, sizes.lq_ckpt8_scales_bytes(rows, cols)), **u8)
         self._index = self.codes.device.index
         self.lib = _library(lib, self._index)
+        self._d = self._values = None
 
     def save(self, x, stream=None):
         _refuse_grad(x=x)
@@ -494,6 +508,31 @@ class Ckpt8:
         d = LinearDesc(DTYPE[_dtype_name(x)], 0, FORMAT[self.fmt], 0, self.rows, 0, self.cols, ld, 0)
         _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(x), None, None, _ptr(self.codes),
                                                            _ptr(self.scales), _stream_of(self._index, stream)))
+
+
+    def values(self, out=None, stream=None):
+        """What the codes stand for, [rows, cols] in bfloat16 (exact but for E4M3 values of scales below 2^-124). The
+        result is a view of the object's own buffer, which its next call overwrites, unless the caller passes its own."""
+        import torch
+
+        pitch = -(-self.cols // 32) * 32
+        if self._d is None:
+            self._d = Desc(FORMAT[self.fmt], GRAN["block"], 32, SCALE_FMT["ue8m0"], 1, 0, DTYPE["bf16"], DTYPE["bf16"])
+        if out is not None:
+            if _matrix(out, self.rows, self.cols, torch.bfloat16, "out") != self.cols or pitch != self.cols:
+                raise ValueError("out has rows of a multiple of 32 elements, one after the other")
+            if out.device != self.codes.device:
+                raise ValueError(f"out is on {out.device}, the checkpoint on {self.codes.device}")
+        elif self._values is None:
+            self._values = _empty_for(stream, self.rows, pitch, dtype=torch.bfloat16, device=self.codes.device)
+        y = self._values if out is None else out
+        if self.rows == 0 or self.cols == 0:
+            return y[:, :self.cols]
+        rc = self.lib.lq_dequantize(ctypes.byref(self._d), self.codes.data_ptr(), self.scales.data_ptr(), None, self.rows,
+                                    pitch, y.data_ptr(), _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_dequantize", rc)
+        return y[:, :self.cols]
 
 
 def _layout(*tensors):
@@ -802,6 +841,139 @@ class SwigluCkpt8:
         if rc != LQ_OK:
             raise LQError("lq_swiglu_ckpt8_backward", rc)
         return dg, du
+
+
+class RmsNormCkpt8:
+    """y = h / sqrt(mean(h^2) + eps) * weight over the rows of [rows, cols], h = x + residual, keeping y in 8 bits
+    (`kept`, a Ckpt8: for the layer behind it, whose weight gradient takes it) and each row's factor, and its backward
+    pass from h. `weight` [cols] is of the matrices' dtype or float32. Results are the object's own buffers, which its
+    next call of that kind overwrites, unless the caller passes its own; h and y may be x or the residual, dx may be dy,
+    dh or h (the same rows), but no other part of them. Calls of one object share its buffers: on two streams at a time,
+    use two objects. As the linear layer's, its calls are no part of autograd's graph."""
+
+    def __init__(self, rows: int, cols: int, dtype: str = "bf16", fmt: str = "int8", eps: float = 1e-6, device="cuda",
+                 lib=None):
+        import torch
+
+        self.torch = torch
+        self.rows, self.cols, self.dtype, self.fmt, self.eps = rows, cols, dtype, fmt, eps
+        self._t = _torch_dtype(dtype)
+        self.kept = Ckpt8(rows, cols, fmt, device, lib)
+        self.device = self.kept.codes.device
+        self._index = self.device.index
+        self.lib = _library(lib, self._index)
+        self.rs = torch.empty(max(4, rows), dtype=torch.float32, device=self.device)
+        self._kept = (self.kept.codes.data_ptr(), self.kept.scales.data_ptr(), self.rs.data_ptr())
+        self._plans = {}
+        self._buffers = {}
+        self._ws = None
+
+    def _weight(self, w, what="weight", dtypes=None):
+        if w.dim() != 1 or w.shape[0] != self.cols or (self.cols > 1 and w.stride(0) != 1):
+            raise ValueError(f"{what} has shape {tuple(w.shape)} and strides {w.stride()}, expected {(self.cols,)}, contiguous")
+        if w.dtype not in (dtypes or (self._t, self.torch.float32)):
+            raise TypeError(f"{what} is {w.dtype}")
+        if not w.is_cuda:
+            raise ValueError(f"{what} is not on the GPU")
+
+    def _at_home(self, *tensors):
+        for t in tensors:
+            if t is not None and t.device != self.device:
+                raise ValueError(f"a tensor is on {t.device}, the norm on {self.device}")
+
+    def _stride(self, t, what):
+        return self.cols if t is None else _matrix(t, self.rows, self.cols, self._t, what)
+
+    def _own(self, kind, stream, shape=None, dtype=None):
+        b = self._buffers.get(kind)
+        if b is None:
+            b = self._buffers[kind] = _empty_for(stream, *(shape or (self.rows, self.cols)), dtype=dtype or self._t,
+                                                 device=self.device)
+        return b
+
+    def _remember(self, key, w, *strides):
+        if len(self._plans) >= 256:
+            self._plans.clear()
+        d = NormDesc(DTYPE[self.dtype], DTYPE[_dtype_name(w)], FORMAT[self.fmt], self.eps, self.rows, self.cols, *strides)
+        size = self._t.itemsize
+        plan = self._plans[key] = (ctypes.byref(d), tuple(_reach(self.rows, ld, self.cols, size) for ld in strides))
+        return plan
+
+    @staticmethod
+    def _refuse(a, ra, b, rb, what, same=True):
+        """An element is read and written by the same lane: in place is as good as apart, but nothing between."""
+        if a is None or b is None:
+            return
+        pa, pb = a.data_ptr(), b.data_ptr()
+        if pa < pb + rb and pb < pa + ra and _share(a, b):
+            if not (same and pa == pb and (a.shape[0] == 1 or a.stride(0) == b.stride(0))):
+                raise ValueError(f"{what} share memory" + (", but are not the same" if same else ""))
+
+    def forward(self, x, weight, residual=None, y=True, out=None, h_out=None, stream=None):
+        """(y, h): h is x itself without a residual; y is None if it is not asked for (`y` false), `kept` alone then
+        holds it. `out`: a tensor for y, `h_out`: for h."""
+        if x.requires_grad or weight.requires_grad or (residual is not None and residual.requires_grad):
+            _refuse_grad(x=x, weight=weight, **({} if residual is None else {"residual": residual}))
+        key = ("y",) + _layout(x, weight, residual, out, h_out)
+        plan = self._plans.get(key)
+        if plan is None:
+            if h_out is not None and residual is None:
+                raise ValueError("h_out without a residual: h is x itself")
+            self._weight(weight)
+            self._at_home(x, weight, residual, out, h_out)
+            plan = self._remember(key, weight, self._stride(x, "x"), self._stride(residual, "residual"),
+                                  self._stride(h_out, "h_out"), self._stride(out, "out"))
+        ref, (rx, rr, rh, ry) = plan
+        h = x if residual is None else h_out if h_out is not None else self._own("h", stream)
+        if not y and out is not None:
+            raise ValueError("out is for y, which is not asked for")
+        y = (out if out is not None else self._own("y", stream)) if y else None
+        self._refuse(x, rx, y, ry, "x and y")
+        if residual is not None:
+            self._refuse(residual, rr, y, ry, "the residual and y")
+            self._refuse(x, rx, h, rh, "x and h")
+            self._refuse(residual, rr, h, rh, "the residual and h")
+            self._refuse(h, rh, y, ry, "h and y", same=False)
+        rc = self.lib.lq_rmsnorm(ref, x.data_ptr(), _ptr(residual), weight.data_ptr(), None if residual is None else
+                                 h.data_ptr(), _ptr(y), *self._kept, _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_rmsnorm", rc)
+        return y, h
+
+    def backward(self, dy, h, weight, dh=None, dw_in=None, out=None, dw_out=None, stream=None):
+        """(dx, dw) of the last forward call, whose h is given back: dx = dh + dy's share, for x and the residual
+        alike; dw = dw_in + the rows' sum, in float32. `out`: a tensor for dx, `dw_out`: for dw (it may be dw_in)."""
+        if dy.requires_grad or h.requires_grad or weight.requires_grad or (dh is not None and dh.requires_grad):
+            _refuse_grad(dy=dy, h=h, weight=weight, **({} if dh is None else {"dh": dh}))
+        key = ("dx",) + _layout(dy, h, weight, dh, dw_in, out, dw_out)
+        plan = self._plans.get(key)
+        if plan is None:
+            self._weight(weight)
+            for t, what in ((dw_in, "dw_in"), (dw_out, "dw_out")):
+                if t is not None:
+                    self._weight(t, what, (self.torch.float32,))
+            self._at_home(dy, h, weight, dh, dw_in, out, dw_out)
+            plan = self._remember(key, weight, self._stride(dy, "dy"), self._stride(dh, "dh"), self._stride(h, "h"),
+                                  self._stride(out, "out"))
+        ref, (ry, rd, rh, rx) = plan
+        dx = out if out is not None else self._own("dx", stream)
+        dw = dw_out if dw_out is not None else self._own("dw", stream, (max(4, self.cols),), self.torch.float32)[:self.cols]
+        self._refuse(dy, ry, dx, rx, "dy and dx")
+        self._refuse(dh, rd, dx, rx, "dh and dx")
+        self._refuse(h, rh, dx, rx, "h and dx")
+        if dw_in is not None:
+            far = abs(dw_in.data_ptr() - dw.data_ptr())
+            if 0 < far < 4 * self.cols:
+                raise ValueError("dw_in and dw share memory, but are not the same")
+        if self._ws is None:
+            self._ws = _empty_for(stream, max(16, self.lib.lq_rmsnorm_workspace_bytes(ref)), dtype=self.torch.uint8,
+                                  device=self.device)
+        rc = self.lib.lq_rmsnorm_backward(ref, dy.data_ptr(), _ptr(dh), h.data_ptr(), weight.data_ptr(),
+                                          self.rs.data_ptr(), dx.data_ptr(), _ptr(dw_in), dw.data_ptr(),
+                                          self._ws.data_ptr(), self._ws.numel(), _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_rmsnorm_backward", rc)
+        return dx, dw
 
 
 # ------------------------------------------------------------------ ceilings

@@ -398,6 +398,48 @@ LQ_API int lq_swiglu_ckpt8_backward(const lq_swiglu_desc* desc, const void* dh, 
                                     const void* gate_scales, const void* up_codes, const void* up_scales, void* dgate,
                                     void* dup, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Root-mean-square norm before a layer, with the residual's addition and an 8-bit
+ * checkpoint of its result.
+ *
+ *   h = x + residual (x itself without one), rounded to the matrices' type
+ *   rs = 1 / sqrt(mean(h^2) + eps) per row, y = h rs weight, rounded to it too
+ *   checkpoint of the rounded y, written or not: the bytes that lq_mx4_quantize
+ *   writes for it
+ * backward, from h and rs, with g = dy weight and n = h rs:
+ *   dx = dh + rs (g - n mean(g n)), the gradient of x and of the residual alike
+ *   dw = dw_in + sum over the rows of dy n
+ * Additions, squares and sums are in binary32 (|h| up to 2^63); a repeated call
+ * gives the same bits. A row that holds an infinity or a NaN is NaN, and so is a
+ * row of zeros with eps 0. Rows are of at most 16384 elements
+ * (LQ_ERR_UNSUPPORTED beyond). Matrices have a row stride each and start at a
+ * multiple of 16 bytes; layouts, ownership, streams and errors as above. Buffers
+ * of one call must not overlap, except that h or y may be x or the residual, and
+ * dx may be dy, dh or h, with the same row stride, and dw may be dw_in. */
+typedef struct {
+  int32_t dtype;        /* lq_dtype of every matrix */
+  int32_t weight_dtype; /* the same, or LQ_F32 */
+  int32_t ckpt_format;  /* LQ_INT8 or LQ_E4M3 */
+  float eps;            /* 0 or more, finite */
+  int64_t rows, cols;
+  int64_t ld_x;         /* row stride of x; backward, of dy */
+  int64_t ld_residual;  /* of the residual; backward, of dh (without one, any valid stride) */
+  int64_t ld_h;         /* of h */
+  int64_t ld_y;         /* of y; backward, of dx */
+} lq_norm_desc;
+
+/* Any of residual, h, y, the checkpoint (both its parts) and rs [rows] (fp32) may
+ * be NULL: not read, not written. */
+LQ_API int lq_rmsnorm(const lq_norm_desc* desc, const void* x, const void* residual, const void* weight, void* h,
+                      void* y, void* ckpt_codes, void* ckpt_scales, void* rs, void* stream);
+
+/* dh, dw_in (fp32 [cols]) and dw (fp32 [cols]; then no workspace is needed) may be
+ * NULL. ws: lq_rmsnorm_workspace_bytes() (0 on a bad descriptor), as above. */
+LQ_API size_t lq_rmsnorm_workspace_bytes(const lq_norm_desc* desc);
+LQ_API int lq_rmsnorm_backward(const lq_norm_desc* desc, const void* dy, const void* dh, const void* h,
+                               const void* weight, const void* rs, void* dx, const void* dw_in, void* dw, void* ws,
+                               size_t ws_bytes, void* stream);
+
 /* Text for a status code (static storage). */
 LQ_API const char* lq_status_string(int status);
 
