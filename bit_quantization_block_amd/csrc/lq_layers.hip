@@ -1,5 +1,5 @@
-// lq_layers.hip — C ABI of the norm with an 8-bit checkpoint (declared in
-// include/lq.h): argument checks and workspace sizes. Every check runs before the
+// lq_layers.hip — C ABI of the norm with an 8-bit checkpoint and of the 4-bit integer
+// layer (declared in include/lq.h): argument checks and workspace sizes. Every check runs before the
 // first launch, so a call that fails writes nothing.
 #include <stddef.h>
 #include <stdint.h>
@@ -18,6 +18,7 @@ bool all_aligned(P... p) {
 bool is_dtype(int d) { return d == LQ_F32 || d == LQ_BF16 || d == LQ_F16; }
 bool is_ckpt_format(int f) { return f == LQ_INT8 || f == LQ_E4M3; }
 bool is_side(int64_t v) { return v >= 0 && v <= 0x7FFFFFFF; }
+bool is_width(int64_t v) { return v >= 0 && v <= 1 << 21; }
 bool is_stride(int64_t ld, int64_t cols) { return ld >= cols && ld <= (int64_t)1 << 31; }
 int status_of(hipError_t e) { return e == hipSuccess ? LQ_OK : LQ_ERR_HIP; }
 
@@ -47,6 +48,20 @@ NormArgs norm_args(const lq_norm_desc* d) {
   a.eps = d->eps;
   a.wide = d->weight_dtype == LQ_F32;
   return a;
+}
+
+
+// ------------------------------------------------------------ the 4-bit integer layer
+int check_int4(const lq_int4_desc* d) {
+  if (!d) return LQ_ERR_NULL;
+  if (!is_dtype(d->in_dtype) || !is_dtype(d->out_dtype) || d->zero_points < 0 || d->zero_points > 1 ||
+      d->reserved != 0) return LQ_ERR_BAD_DESC;
+  if (d->x_format < -1 || d->x_format > LQ_E3M2) return LQ_ERR_BAD_DESC;
+  if (d->x_format != -1 && !is_ckpt_format(d->x_format)) return LQ_ERR_UNSUPPORTED;
+  if (d->group != 32 && d->group != 64 && d->group != 128) return LQ_ERR_UNSUPPORTED;
+  if (!is_side(d->m) || !is_width(d->n) || !is_width(d->k) || d->k % d->group != 0) return LQ_ERR_SHAPE;
+  if (d->m > 65535 * (int64_t)16) return LQ_ERR_UNSUPPORTED;
+  return LQ_OK;
 }
 
 }  // namespace
@@ -98,6 +113,39 @@ int lq_rmsnorm_backward(const lq_norm_desc* d, const void* dy, const void* dh, c
   a.y = dx;
   a.planes = dw ? (float*)ws : nullptr;
   return status_of(launch_rmsnorm_backward(d->dtype, a, (const float*)dw_in, (float*)dw, (hipStream_t)stream));
+}
+
+size_t lq_int4_packed_bytes(const lq_int4_desc* d) {
+  if (check_int4(d)) return 0;
+  return int4_codes_bytes(d->n, d->k) + int4_scales_bytes(d->n, d->k, d->group) * (d->zero_points ? 2 : 1);
+}
+
+int lq_int4_pack(const lq_int4_desc* d, const void* codes, const void* scales, const void* zeros, void* packed,
+                 void* stream) {
+  const int rc = check_int4(d);
+  if (rc) return rc;
+  if (d->n == 0 || d->k == 0) return LQ_OK;
+  if (!codes || !scales || !packed || !zeros != !d->zero_points) return LQ_ERR_NULL;
+  if (!all_aligned(codes, scales, zeros, (const void*)packed)) return LQ_ERR_ALIGN;
+  return status_of(launch_int4_pack(d, codes, scales, zeros, packed, (hipStream_t)stream));
+}
+
+size_t lq_int4_workspace_bytes(const lq_int4_desc* d) {
+  if (check_int4(d)) return 0;
+  const size_t b = int4_rows_bytes(d);
+  return b ? b : 16;
+}
+
+int lq_int4_linear(const lq_int4_desc* d, const void* x, const void* x_scales, const void* packed, void* y, void* ws,
+                   size_t ws_bytes, void* stream) {
+  const int rc = check_int4(d);
+  if (rc) return rc;
+  if ((d->x_format == -1 && !is_stride(d->ld_in, d->k)) || !is_stride(d->ld_out, d->n)) return LQ_ERR_SHAPE;
+  if (d->m == 0 || d->n == 0) return LQ_OK;
+  if (!y || (d->k > 0 && (!x || !packed || !x_scales != (d->x_format == -1)))) return LQ_ERR_NULL;
+  if (!all_aligned(x, x_scales, packed, (const void*)y, (const void*)ws)) return LQ_ERR_ALIGN;
+  if (!ws || ws_bytes < lq_int4_workspace_bytes(d)) return LQ_ERR_WORKSPACE;
+  return status_of(launch_int4_linear(d, x, x_scales, packed, y, ws, (hipStream_t)stream));
 }
 
 }  // extern "C"

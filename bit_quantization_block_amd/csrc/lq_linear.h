@@ -331,4 +331,13 @@ int64_t norm_planes(int64_t rows, int64_t cols);
 hipError_t launch_rmsnorm(int dtype, int format, const NormArgs& a, hipStream_t s);
 hipError_t launch_rmsnorm_backward(int dtype, const NormArgs& a, const float* dw_in, float* dw, hipStream_t s);
 
+// The 4-bit integer layer (lq_int4.hip): a packed layer is codes, then scales, then zero points.
+size_t int4_codes_bytes(int64_t n, int64_t k);
+size_t int4_scales_bytes(int64_t n, int64_t k, int group);
+size_t int4_rows_bytes(const lq_int4_desc* d);
+hipError_t launch_int4_pack(const lq_int4_desc* d, const void* codes, const void* scales, const void* zeros, void* packed,
+                            hipStream_t s);
+hipError_t launch_int4_linear(const lq_int4_desc* d, const void* x, const void* x_scales, const void* packed, void* y,
+                              void* ws, hipStream_t s);
+
 }  // namespace lql

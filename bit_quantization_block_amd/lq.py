@@ -30,7 +30,8 @@ EXPORTS = ("lq_quantize", "lq_dequantize", "lq_fake_quant_qsnr", "lq_hadamard_qu
            "lq_mx4_codes_bytes", "lq_mx4_scales_bytes", "lq_ckpt8_codes_bytes", "lq_ckpt8_scales_bytes",
            "lq_linear_workspace_bytes", "lq_mx4_quantize", "lq_mx4_product", "lq_mx4_linear", "lq_mx4_dgrad",
            "lq_ckpt8_wgrad", "lq_linear_kernels", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward",
-           "lq_rmsnorm", "lq_rmsnorm_workspace_bytes", "lq_rmsnorm_backward")
+           "lq_rmsnorm", "lq_rmsnorm_workspace_bytes", "lq_rmsnorm_backward", "lq_int4_packed_bytes",
+           "lq_int4_pack", "lq_int4_workspace_bytes", "lq_int4_linear")
 LINEAR_CALL = {"quantize": 0, "product": 1, "linear": 2, "dgrad": 3, "wgrad": 4}
 # output bits of lq_call_kernels
 OUT = {"codes": 1, "scales": 2, "zeros": 4, "y": 8, "res": 16}
@@ -66,6 +67,11 @@ class SwigluDesc(ctypes.Structure):
 class NormDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "weight_dtype", "ckpt_format")] + [("eps", ctypes.c_float)] + \
                [(n, ctypes.c_int64) for n in ("rows", "cols", "ld_x", "ld_residual", "ld_h", "ld_y")]
+
+
+class Int4Desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_dtype", "x_format", "out_dtype", "group", "zero_points", "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("m", "n", "k", "ld_in", "ld_out")]
 
 
 _lib = None
@@ -120,6 +126,13 @@ def load(path: str | None = None):
     L.lq_rmsnorm_workspace_bytes.restype = sz
     L.lq_rmsnorm_backward.argtypes = [np_, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.lq_rmsnorm_backward.restype = ctypes.c_int
+    ip = ctypes.POINTER(Int4Desc)
+    for f in ("lq_int4_packed_bytes", "lq_int4_workspace_bytes"):
+        getattr(L, f).argtypes = [ip]
+        getattr(L, f).restype = sz
+    L.lq_int4_pack.argtypes = [ip, vp, vp, vp, vp, vp]
+    L.lq_int4_linear.argtypes = [ip, vp, vp, vp, vp, vp, sz, vp]
+    L.lq_int4_pack.restype = L.lq_int4_linear.restype = ctypes.c_int
     L.lq_linear_kernels.argtypes = [lp, ctypes.c_int, ctypes.c_int, ctypes.c_char_p, sz]
     for f in ("lq_mx4_quantize", "lq_mx4_product", "lq_mx4_linear", "lq_mx4_dgrad", "lq_ckpt8_wgrad",
               "lq_linear_kernels", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward"):
@@ -974,6 +987,154 @@ class RmsNormCkpt8:
         if rc != LQ_OK:
             raise LQError("lq_rmsnorm_backward", rc)
         return dx, dw
+
+
+class Int4Linear:
+    """y = x W^T with W held as 4-bit integers with an fp16 scale, and a zero point unless `symmetric`, for each `group`
+    (32, 64 or 128) of columns: for serving, a few rows of x at a time. `w` [n, k] is quantised (lq_quantize's INT4 rules)
+    and laid out once; from_codes() takes stored weights. x is a matrix of `dtype`, or a Ckpt8 of either format (as the
+    norm's `kept`), taken at the values it holds. `rows` is the most rows a call may have, for which the result's buffer is
+    allocated once (a call's result is a view of it, which the next call overwrites, unless the caller passes its own as
+    `out`; a call on that very result gets a second buffer). Calls of one layer share its buffers and workspace: on two
+    streams at a time, use two layers; a stream other than the one on which the layer was made, or last called, waits for
+    that one first. `stream` is a stream's handle. No part of autograd's graph: inputs that require a gradient are
+    refused."""
+
+    def __init__(self, w, rows: int, group: int = 64, symmetric: bool = True, dtype: str = "bf16", out: str = "bf16",
+                 lib=None):
+        self._start(w.shape[0], w.shape[1], group, not symmetric, rows, dtype, out, w.device, lib)
+        self.load(w)
+
+    @classmethod
+    def from_codes(cls, codes, scales, zeros=None, rows: int = 1, dtype: str = "bf16", out: str = "bf16", lib=None):
+        """A layer of stored weights: codes [n, k / 2] uint8 (two's complement nibbles, the even column's low), scales and
+        zeros [n, groups] float16, contiguous."""
+        n, k, groups = codes.shape[0], codes.shape[1] * 2, scales.shape[1]
+        if groups == 0 or k % groups:
+            raise ValueError(f"{k} columns in {groups} groups")
+        made = cls.__new__(cls)
+        made._start(n, k, k // groups, zeros is not None, rows, dtype, out, codes.device, lib)
+        made.load_codes(codes, scales, zeros)
+        return made
+
+    def _start(self, n, k, group, zero_points, rows, dtype, out, device, lib):
+        import torch
+
+        self.torch = torch
+        self._index = device.index
+        self.lib = _library(lib, self._index)
+        self.n, self.k, self.group, self.zero_points = n, k, group, zero_points
+        self.rows, self.dtype, self.out, self.device = rows, dtype, out, device
+        d = Int4Desc(DTYPE[dtype], -1, DTYPE[out], group, int(zero_points), 0, 0, n, k, 0, 0)
+        size = self.lib.lq_int4_packed_bytes(ctypes.byref(d))
+        if size == 0 and n > 0 and k > 0:   # the descriptor is refused: by this call too, with the status
+            _check("lq_int4_pack", self.lib.lq_int4_pack(ctypes.byref(d), None, None, None, None, None))
+        self.packed = torch.empty(max(16, size), dtype=torch.uint8, device=device)
+        self._pw = ctypes.c_void_p(self.packed.data_ptr())
+        self._plans = {}
+        self._buffers = {}
+        self._workspaces = []
+
+    _workspace = Mx4Linear._workspace
+
+    def load(self, w, stream=None):
+        """Quantises w into the layer: its weights from the next call on."""
+        torch = self.torch
+        if _matrix(w, self.n, self.k, w.dtype, "w") != self.k:
+            raise ValueError("w's rows must lie one after the other")
+        groups = self.k // self.group
+        codes = _empty_for(stream, self.n, self.k // 2, dtype=torch.uint8, device=self.device)
+        scales, zeros = (_empty_for(stream, self.n, groups, dtype=torch.float16, device=self.device) for _ in range(2))
+        if w.device != self.device:
+            raise ValueError(f"w is on {w.device}, the layer on {self.device}")
+        d = Desc(FORMAT["int4"], GRAN["block"], self.group, SCALE_FMT["f16"], int(not self.zero_points), 0,
+                 DTYPE[_dtype_name(w)], DTYPE["bf16"])
+        if self.n and self.k:
+            _check("lq_quantize", self.lib.lq_quantize(ctypes.byref(d), _ptr(w), self.n, self.k, _ptr(codes), _ptr(scales),
+                                                       _ptr(zeros) if self.zero_points else None, None, 0,
+                                                       _stream_of(self._index, stream)))
+        self.load_codes(codes, scales, zeros if self.zero_points else None, stream)
+
+    def load_codes(self, codes, scales, zeros=None, stream=None):
+        """Lays stored weights out in the layer, as from_codes() does."""
+        groups = self.k // self.group
+        if (zeros is not None) != self.zero_points:
+            raise ValueError("zero points and a layer without" if zeros is not None else "no zero points for the layer's")
+        for t, shape, dtype, what in ((codes, (self.n, self.k // 2), self.torch.uint8, "codes"),
+                                      (scales, (self.n, groups), self.torch.float16, "scales"),
+                                      (zeros, (self.n, groups), self.torch.float16, "zeros")):
+            if t is None:
+                continue
+            if _matrix(t, *shape, dtype, what) != shape[1]:
+                raise ValueError(f"{what} must be contiguous")
+            if t.device != self.device:
+                raise ValueError(f"{what} are on {t.device}, the layer on {self.device}")
+        d = Int4Desc(0, -1, 0, self.group, int(self.zero_points), 0, 0, self.n, self.k, 0, 0)
+        _check("lq_int4_pack", self.lib.lq_int4_pack(ctypes.byref(d), _ptr(codes), _ptr(scales), _ptr(zeros),
+                                                     _ptr(self.packed), _stream_of(self._index, stream)))
+
+    def _plan(self, key, x, kept, out, stream):
+        m = x.rows if kept else x.shape[0]
+        if m > self.rows:
+            raise ValueError(f"{m} rows in a layer planned for {self.rows}")
+        if kept:
+            if x.cols != self.k:
+                raise ValueError(f"the checkpoint has {x.cols} columns, the layer {self.k}")
+            where, ld_in, reach = x.codes.device, self.k, 0
+        else:
+            where, ld_in = x.device, _matrix(x, m, self.k, _torch_dtype(self.dtype), "x")
+            reach = _reach(m, ld_in, self.k, x.element_size())
+        for device in (where, self.device if out is None else out.device):
+            if device != self.device:
+                raise ValueError(f"a tensor is on {device}, the layer on {self.device}")
+        if out is None:
+            b = self._buffers.get("y")
+            if b is None:
+                b = self._buffers["y"] = _empty_for(stream, self.rows, self.n, dtype=_torch_dtype(self.out),
+                                                    device=self.device)
+            buffer, ld_out = b[:m], self.n
+        else:
+            buffer, ld_out = None, _matrix(out, m, self.n, _torch_dtype(self.out), "out")
+        d = Int4Desc(DTYPE[self.dtype], FORMAT[x.fmt] if kept else -1, DTYPE[self.out], self.group, int(self.zero_points), 0,
+                     m, self.n, self.k, ld_in, ld_out)
+        ref = ctypes.byref(d)
+        ws = self._workspace(max(16, self.lib.lq_int4_workspace_bytes(ref)), stream)
+        if len(self._plans) >= 256:
+            self._plans.clear()
+        at = 0 if buffer is None else buffer.data_ptr()
+        plan = self._plans[key] = (ref, ctypes.c_void_p(ws.data_ptr()), ws.numel(), buffer, at, at - reach,
+                                   at + _reach(m, ld_out, self.n, _torch_dtype(self.out).itemsize))
+        return plan
+
+    _apart = Mx4Linear._apart
+
+    def forward(self, x, out=None, stream=None):
+        """y = x W^T; x a matrix [m, k], or a Ckpt8 of it."""
+        kept = isinstance(x, Ckpt8)
+        if kept:
+            key = (x.rows, x.cols, x.fmt, x._index)
+        else:
+            if x.requires_grad:
+                _refuse_grad(x=x)
+            key = (x.shape, x.stride(), x.dtype, x.get_device())
+        if out is not None:
+            key += _layout(out)
+        plan = self._plans.get(key) or self._plan(key, x, kept, out, stream)
+        ref, ws, ws_bytes, y, yp, low, high = plan
+        if out is not None:
+            y, yp = out, out.data_ptr()
+            low, high = low + yp, high + yp
+        if kept:
+            xp, sp = x.codes.data_ptr(), x.scales.data_ptr()
+        else:
+            xp, sp = x.data_ptr(), None
+            if low < xp < high:
+                y = self._apart("y", "x", x, y, out, stream)
+                yp = y.data_ptr()
+        rc = self.lib.lq_int4_linear(ref, xp, sp, self._pw, yp, ws, ws_bytes, _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_int4_linear", rc)
+        return y
 
 
 # ------------------------------------------------------------------ ceilings

@@ -35,7 +35,7 @@ def _code_only(text: str) -> str:
 
 # Sources of the linear layer's kernels; every other file in csrc/ is the fake-quant path's or the ceilings'.
 LINEAR_SOURCES = ("lq_linear.h", "lq_linear.hip", "lq_mx4.hip", "lq_grad.hip", "lq_swiglu.hip", "lq_layers.hip",
-                  "lq_rmsnorm.hip")
+                  "lq_rmsnorm.hip", "lq_int4.hip")
 SHARED_SOURCES = ("lq_device.h", "lq_plan.h")
 
 
@@ -45,7 +45,7 @@ def _header_types(text: str, path: str) -> str:
     text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
     out = re.findall(r"^#define LQ_\w+ .*$", text, flags=re.M)
     for body, name in re.findall(r"typedef (?:struct|enum)\s*\{([^}]*)\}\s*(\w+);", text):
-        if name.startswith(("lq_linear", "lq_swiglu", "lq_norm")) <= (path == "linear"):
+        if name.startswith(("lq_linear", "lq_swiglu", "lq_norm", "lq_int4")) <= (path == "linear"):
             out.append(name + " " + body)
     return _code_only("\n".join(out))
 

@@ -440,6 +440,47 @@ LQ_API int lq_rmsnorm_backward(const lq_norm_desc* desc, const void* dy, const v
                                const void* weight, const void* rs, void* dx, const void* dw_in, void* dw, void* ws,
                                size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A linear layer for serving whose weights are 4-bit integers with a scale, and a
+ * zero point or none, for each group of columns, as lq_quantize writes them (INT4,
+ * PER_BLOCK of 32, 64 or 128, LQ_SCALE_F16):
+ *
+ *   y[m, n] = sum over groups g of s[n, g] * sum over k in g of (q[n, k] - z[n, g]) x[m, k]
+ *
+ * for few rows of x (from one up to some dozens at a time: more are taken in bands of
+ * 64, each of which reads W again). x is a matrix, or an 8-bit checkpoint as the norm,
+ * the gated unit or lq_mx4_quantize leave it, taken at the values it holds. Products
+ * are exact and added in binary32 (values of x up to 2^120 in magnitude), groups are
+ * scaled and added in binary32, and y is rounded once, to nearest even. A repeated call
+ * gives the same bits. An infinity or a NaN in a row of x makes the row of y NaN.
+ *
+ * W is laid out once for the kernels by lq_int4_pack, into lq_int4_packed_bytes() (0 on
+ * a bad descriptor) of device memory. k is a multiple of the group; n and k are at most
+ * 2^21, m at most 65535 * 16. Layouts, ownership, streams and errors as above; every
+ * product call needs a workspace of lq_int4_workspace_bytes(), 16-byte aligned, not
+ * initialised, not shared by calls that overlap in time. */
+typedef struct {
+  int32_t in_dtype;    /* lq_dtype of x, if it is a matrix */
+  int32_t x_format;    /* -1: x is a matrix; LQ_INT8 or LQ_E4M3: x is a checkpoint */
+  int32_t out_dtype;   /* lq_dtype of y */
+  int32_t group;       /* columns of a group: 32, 64 or 128 */
+  int32_t zero_points; /* 1: each group has a zero point, 0: none has */
+  int32_t reserved;    /* 0 */
+  int64_t m, n, k;     /* rows of x and y; rows of W; columns of x and W */
+  int64_t ld_in;       /* row stride of x, if it is a matrix */
+  int64_t ld_out;      /* row stride of y */
+} lq_int4_desc;
+
+LQ_API size_t lq_int4_packed_bytes(const lq_int4_desc* desc);
+/* codes [n, k / 2], scales and zeros (NULL without) [n, k / group] fp16. in_dtype, x_format, out_dtype, m and the
+ * strides are not used. */
+LQ_API int lq_int4_pack(const lq_int4_desc* desc, const void* codes, const void* scales, const void* zeros, void* packed,
+                        void* stream);
+LQ_API size_t lq_int4_workspace_bytes(const lq_int4_desc* desc);
+/* x_scales: the checkpoint's, NULL for a matrix. */
+LQ_API int lq_int4_linear(const lq_int4_desc* desc, const void* x, const void* x_scales, const void* packed, void* y,
+                          void* ws, size_t ws_bytes, void* stream);
+
 /* Text for a status code (static storage). */
 LQ_API const char* lq_status_string(int status);
 
