@@ -112,12 +112,15 @@ struct GradArgs {
   int64_t ldo;
   uint32_t tm, tn;
   int parts, part;         // of the contraction: steps of each; with parts > 1, out is `parts` planes
+  Experts experts;         // with rows by expert: m is all of them, and W and dw are one expert's after another's
 };
 
 // F: the checkpoint's format (wgrad); OUT: the result's type; RAGGED (dgrad): dy's
 // rows end inside a unit of 8 elements, of whose last the rest is cut off.
-template <int KIND, int F, int OUT, int FM, int FN, bool RAGGED>
-__global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradArgs g) {
+// BY_EXPERT: the rows of dy (and x8) lie by expert: a tile of dx is one expert's rows
+// times its n rows of W; a tile of dw, one expert's, is contracted over its rows alone.
+template <int KIND, int F, int OUT, int FM, int FN, bool RAGGED, bool BY_EXPERT>
+__device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
   typedef typename El<OUT>::T T;
   typedef GradLds<KIND, FM, FN> Lds;
   constexpr int BM = 64 * FM, BN = 64 * FN;
@@ -125,17 +128,46 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
 
-  // The XCD's share of the tiles is a contiguous run in bands of 4 rows of tiles (as in the 4-bit product).
-  const uint32_t tiles = g.tm * g.tn, total = tiles * g.parts, xcd = blockIdx.x % 8, per8 = total / 8, more = total % 8;
-  const uint32_t mine8 = xcd * per8 + (xcd < more ? xcd : more) + blockIdx.x / 8;
-  const uint32_t part = __builtin_amdgcn_readfirstlane(mine8 / tiles), t0 = mine8 - part * tiles;
-  const uint32_t band = t0 / (4 * g.tn), first = band * 4, high = g.tm - first < 4 ? g.tm - first : 4, in = t0 - band * 4 * g.tn;
-  const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane(first + in % high) * BM;
+  // The XCD's share of the tiles is a contiguous run in bands of 4 rows of tiles (as in the 4-bit product). Of dw's by
+  // expert, it is such a run of each expert's, whose tiles take as long as that one has rows.
+  uint32_t tm = g.tm, part = 0, expert = 0, t0;
+  int64_t from = 0, until = KIND == kDgrad ? g.m : g.n;   // rows of A that the expert's are (dgrad); dw's rows
+  int64_t depth0 = 0, depth = KIND == kDgrad ? g.n : g.m; // the contraction's: first, and how many
+  const uint32_t xcd = blockIdx.x % 8;
+  if constexpr (BY_EXPERT && KIND == kDgrad) {
+    ExpertTable table;
+    table.scan(g.experts, g.m, BM);
+    const uint32_t total = table.tiles_to(g.experts.count - 1) * g.tn, per8 = total / 8, more = total % 8;
+    if (blockIdx.x / 8 >= per8 + (xcd < more ? 1 : 0)) return;
+    const uint32_t mine8 = xcd * per8 + (xcd < more ? xcd : more) + blockIdx.x / 8;
+    expert = uniform(table.at(mine8 / g.tn, g.experts.count));
+    const uint32_t before = table.tiles_before(expert);
+    t0 = mine8 - before * g.tn;
+    tm = table.tiles_to(expert) - before;
+    from = table.row_begin(expert);
+    until = table.row_end(expert);
+  } else if constexpr (BY_EXPERT) {
+    const uint32_t tiles = g.tm * g.tn, share = (tiles + 7) / 8, mine = blockIdx.x / 8;
+    expert = uniform(mine / share);
+    t0 = xcd * share + mine - expert * share;
+    if (t0 >= tiles) return;
+    int64_t end;
+    expert_rows(g.experts, g.m, (int)expert, depth0, end);
+    depth = end - depth0;
+  } else {
+    const uint32_t tiles = g.tm * g.tn, total = tiles * g.parts, per8 = total / 8, more = total % 8;
+    const uint32_t mine8 = xcd * per8 + (xcd < more ? xcd : more) + blockIdx.x / 8;
+    part = __builtin_amdgcn_readfirstlane(mine8 / tiles);
+    t0 = mine8 - part * tiles;
+  }
+  const uint32_t band = t0 / (4 * g.tn), first = band * 4, high = tm - first < 4 ? tm - first : 4, in = t0 - band * 4 * g.tn;
+  const int64_t row0 = from + (int64_t)__builtin_amdgcn_readfirstlane(first + in % high) * BM;
   const int64_t col0 = (int64_t)__builtin_amdgcn_readfirstlane(in / high) * BN;
 
-  const int64_t rows = KIND == kDgrad ? g.m : g.n, depth = KIND == kDgrad ? g.n : g.m;   // of A
+  const int64_t rows = until;   // of A
+  const int64_t w_rows = BY_EXPERT ? g.experts.count * g.n : g.n, w_first = expert * g.n;   // dgrad: rows of W as it is stored, and the expert's first
   const int all = (int)((depth + kStep - 1) / kStep), begin = (int)part * g.part;
-  const int steps = begin + g.part < all ? begin + g.part : all;
+  const int steps = BY_EXPERT || begin + g.part >= all ? all : begin + g.part;
 
   // ---- A: 16 bytes a load, 2 FM loads a step
   constexpr int kLoadsA = 2 * FM;
@@ -172,17 +204,21 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
   uint32_t wstep = (uint32_t)start * 64, wsstep = (uint32_t)start * 4;
   // wgrad: all three move down the rows, 64 at a time, the part's last step with what is left
   int to_come = steps - begin;
-  const uint8_t *pa8 = (const uint8_t*)(KIND == kDgrad ? g.dy + row0 * g.lddy + start : g.dy + start * g.lddy + row0);
-  const uint8_t *pc8 = g.b + start * pitch + col0, *ps8 = g.bs + start * spitch + col0 / 32;
+  const uint8_t *pa8 = (const uint8_t*)(KIND == kDgrad ? g.dy + row0 * g.lddy + start : g.dy + (depth0 + start) * g.lddy + row0);
+  const uint8_t *pc8 = g.b + (depth0 + start) * pitch + col0, *ps8 = g.bs + (depth0 + start) * spitch + col0 / 32;
+  // (an expert's rows may begin in the middle of a word: the stretch begins with the word, and the places in it later)
+  const uint32_t shift = BY_EXPERT ? uniform((uint32_t)(uintptr_t)pa8 & 3u) : 0;
+  pa8 -= shift;
+  ao += shift;
   const int64_t tail = end - start - (to_come - 1) * (int64_t)kStep;   // rows of the last step
   // (a load's every 4 bytes have to end before the stretch does: of rows of odd length, 2 more are let in, which the
   // rules of reads_in_place() keep inside the matrix or its last 4 bytes)
   const int64_t row_bytes = (g.row + (g.row & 1)) * 2;
-  auto size_a = [&](int64_t rows_left) { return (uint32_t)((rows_left - 1) * g.lddy * 2 + row_bytes - row0 * 2); };   // (below 2^31)
+  auto size_a = [&](int64_t rows_left) { return (uint32_t)((rows_left - 1) * g.lddy * 2 + row_bytes - row0 * 2 + shift); };   // (below 2^31)
   auto size_c = [&](int64_t rows_left) { return (uint32_t)(rows_left * pitch - col0); };
   auto size_s = [&](int64_t rows_left) { return (uint32_t)(rows_left * spitch - col0 / 32); };
   const uint32_t last_a = uniform(size_a(tail)), last_c = uniform(size_c(tail)), last_s = uniform(size_s(tail));
-  uint32_t bytes_a = uniform(KIND == kDgrad ? (uint32_t)((left - 1) * g.lddy * 2 + row_bytes - start * 2) : size_a(kStep));
+  uint32_t bytes_a = uniform(KIND == kDgrad ? (uint32_t)((left - 1) * g.lddy * 2 + row_bytes - start * 2 + shift) : size_a(kStep));
   uint32_t bytes_c = uniform(size_c(kStep)), bytes_s = uniform(size_s(kStep));
   const uint32_t move_a = uniform((uint32_t)(KIND == kDgrad ? kStep * 2 : kStep * 2 * g.lddy)), move_c = uniform((uint32_t)(kStep * pitch)), move_s = uniform((uint32_t)(kStep * spitch));
   __amdgpu_buffer_rsrc_t sa, sc[kPieces], ss[kPieces];
@@ -191,8 +227,8 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
     for (int i = 0; i < kPieces; i++) {
       const int64_t panel = col0 / 128 + i;
       const bool real = panel < mx4_groups(g.k);
-      sc[i] = stretch(g.b + panel * g.n * 64, real ? end * 64 : 0);
-      ss[i] = stretch(g.bs + panel * mx4_scale_rows(g.n) * 4, real ? end * 4 : 0);
+      sc[i] = stretch(g.b + (panel * w_rows + w_first) * 64, real ? end * 64 : 0);
+      ss[i] = stretch(g.bs + (panel * mx4_scale_rows(w_rows) + w_first) * 4, real ? end * 4 : 0);
     }
   }
   auto point = [&] {
@@ -436,6 +472,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
   // What dw is added to, of 32 rows: asked for a block of rows ahead (a load may not pass a store that might be to the
   // same place: one by one, 154 x 11008 x 4096 took 123 us, and with 8 at a time 20 us more in 256 x 256 tiles).
   constexpr int kStores = units / 2;
+  const int64_t dw0 = BY_EXPERT && KIND == kWgrad ? expert * g.n : part * rows;   // of out: the expert's, or the plane's
   v4f base[2][kStores];
   auto load_base = [&](int i) {
     if (KIND == kWgrad && g.in) {
@@ -443,7 +480,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
       for (int b = 0; b < kStores; b++) {
         const int u = b * 64 + lane;
         const int64_t row = r0 + i * 32 + u / units, col = c0 + u % units * V;
-        if (row < rows && g.k - col >= V) __builtin_memcpy(&base[i % 2][b], g.in + row * g.ldo + col, 16);
+        if (row < rows && g.k - col >= V) __builtin_memcpy(&base[i % 2][b], g.in + (dw0 + row) * g.ldo + col, 16);
       }
     }
   };
@@ -468,7 +505,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
       T v[V];
       __builtin_memcpy(v, __builtin_assume_aligned(mine + rr * kRow + cc * (int)sizeof(T), 16), 16);
       if (row < rows && col < g.k) {
-        T* o = (T*)g.out + (part * rows + row) * g.ldo + col;
+        T* o = (T*)g.out + (dw0 + row) * g.ldo + col;
         if (g.k - col >= V) {
           if constexpr (KIND == kWgrad) {
             if (g.in) {
@@ -481,7 +518,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
 #pragma unroll
           for (int e = 0; e < V; e++)
             if (col + e < g.k) {
-              if constexpr (KIND == kWgrad) o[e] = v[e] + (g.in ? g.in[row * g.ldo + col + e] : 0.0f);
+              if constexpr (KIND == kWgrad) o[e] = v[e] + (g.in ? g.in[(dw0 + row) * g.ldo + col + e] : 0.0f);
               else o[e] = v[e];
             }
         }
@@ -489,6 +526,15 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
     }
     asm volatile("" ::: "memory");
   }
+}
+
+template <int KIND, int F, int OUT, int FM, int FN, bool RAGGED>
+__global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradArgs g) {
+  grad_tile_of<KIND, F, OUT, FM, FN, RAGGED, false>(g);
+}
+template <int KIND, int F, int OUT, int FM, int FN, bool RAGGED>
+__global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad_experts(const GradArgs g) {
+  grad_tile_of<KIND, F, OUT, FM, FN, RAGGED, true>(g);
 }
 
 // dy with rows of a multiple of 64 elements, zeros past n.
@@ -525,22 +571,27 @@ template <int KIND, int F, int OUT>
 hipError_t grad_tile(int tile, GradArgs& g, hipStream_t s) {
   return tile == 4 ? grad_tiled<KIND, F, OUT, 4, 4>(g, s) : grad_tiled<KIND, F, OUT, 2, 2>(g, s);
 }
+// dy where it can be read in place, or its copy at the workspace's start; the rest of the workspace.
+hipError_t place_dy(GradArgs& g, void* ws, uint8_t*& rest, hipStream_t s) {
+  rest = (uint8_t*)ws;
+  if (reads_in_place(g.m, g.n, g.lddy)) return hipSuccess;
+  const int64_t ld = padded_columns(g.n);
+  const dim3 grid = matrix_grid((ld + 511) / 512, g.m);
+  if (lqd::g_plan) {
+    (void)LQ_PLAN(grid, 256, "k_pad_rows");
+  } else {
+    hipLaunchKernelGGL(k_pad_rows, grid, dim3(256), 0, s, g.dy, g.m, g.n, g.lddy, (uint16_t*)ws, ld);
+    if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+  }
+  g.dy = (const uint16_t*)ws;
+  g.lddy = g.row = ld;
+  rest += (g.m * ld * 2 + 255) / 256 * 256;
+  return hipSuccess;
+}
 template <int KIND, int F, int OUT>
 hipError_t grad(GradArgs g, void* ws, hipStream_t s) {
-  uint8_t* planes = (uint8_t*)ws;
-  if (!reads_in_place(g.m, g.n, g.lddy)) {
-    const int64_t ld = padded_columns(g.n);
-    const dim3 grid = matrix_grid((ld + 511) / 512, g.m);
-    if (lqd::g_plan) {
-      (void)LQ_PLAN(grid, 256, "k_pad_rows");
-    } else {
-      hipLaunchKernelGGL(k_pad_rows, grid, dim3(256), 0, s, g.dy, g.m, g.n, g.lddy, (uint16_t*)ws, ld);
-      if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
-    }
-    g.dy = (const uint16_t*)ws;
-    g.lddy = g.row = ld;
-    planes += (g.m * ld * 2 + 255) / 256 * 256;
-  }
+  uint8_t* planes;
+  if (place_dy(g, ws, planes, s) != hipSuccess) return hipErrorLaunchFailure;
   const int64_t rows = KIND == kDgrad ? g.m : g.n;
   const Split c = KIND == kDgrad ? split_dgrad(g.m, g.n, g.k) : split_wgrad(g.m, g.n, g.k, g.in != nullptr);
   g.parts = c.parts;
@@ -562,7 +613,7 @@ hipError_t launch_mx4_dgrad(const void* dy, int64_t m, int64_t n, int64_t lddy, 
                             const void* w_scales, int64_t k, int out_dtype, void* dx, int64_t lddx, void* ws,
                             hipStream_t s) {
   if (n == 0) return launch_constant(m, k, out_dtype, nullptr, dx, lddx, s);
-  const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)w_codes, (const uint8_t*)w_scales, nullptr, dx, lddx, 0, 0, 1, 0};
+  const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)w_codes, (const uint8_t*)w_scales, nullptr, dx, lddx, 0, 0, 1, 0, {}};
   switch (out_dtype) {
     case LQ_F32: return grad<kDgrad, LQ_E2M1, LQ_F32>(g, ws, s);
     case LQ_BF16: return grad<kDgrad, LQ_E2M1, LQ_BF16>(g, ws, s);
@@ -574,9 +625,56 @@ hipError_t launch_ckpt8_wgrad(int format, const void* dy, int64_t m, int64_t n, 
                               const void* x_scales, int64_t k, const float* dw_in, float* dw, int64_t lddw, void* ws,
                               hipStream_t s) {
   if (m == 0) return launch_constant(n, k, LQ_F32, dw_in, dw, lddw, s);
-  const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)x_codes, (const uint8_t*)x_scales, dw_in, dw, lddw, 0, 0, 1, 0};
+  const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)x_codes, (const uint8_t*)x_scales, dw_in, dw, lddw, 0, 0, 1, 0, {}};
   if (format == LQ_INT8) return grad<kWgrad, LQ_INT8, LQ_F32>(g, ws, s);
   return grad<kWgrad, LQ_E4M3, LQ_F32>(g, ws, s);
+}
+
+namespace {
+
+template <int KIND, int F, int OUT, int FM, int FN>
+hipError_t grad_experts_tiled(GradArgs& g, hipStream_t s) {
+  constexpr bool kMayBe = KIND == kDgrad;
+  const int64_t rows = KIND == kDgrad ? g.m : g.n;
+  g.tm = (uint32_t)((rows + 64 * FM - 1) / (64 * FM));
+  g.tn = (uint32_t)((g.k + 64 * FN - 1) / (64 * FN));
+  // dgrad: at most one tile of rows an expert more than if the rows were one's, and an eighth of them for an XCD;
+  // wgrad: an eighth of each expert's
+  const int64_t tiles = KIND == kDgrad ? ((int64_t)g.m / (64 * FM) + g.experts.count) * g.tn : (int64_t)g.tm * g.tn;
+  const int64_t eighth = (tiles + 7) / 8 * (KIND == kDgrad ? 1 : g.experts.count);
+  const dim3 grid((unsigned)(eighth * 8));
+  if (kMayBe && g.row % 8 != 0) hipLaunchKernelGGL((k_grad_experts<KIND, F, OUT, FM, FN, kMayBe>), grid, dim3(256), 0, s, g);
+  else hipLaunchKernelGGL((k_grad_experts<KIND, F, OUT, FM, FN, false>), grid, dim3(256), 0, s, g);
+  return hipGetLastError();
+}
+template <int KIND, int F, int OUT>
+hipError_t grad_experts(GradArgs g, int tile, void* ws, hipStream_t s) {
+  uint8_t* rest;
+  if (place_dy(g, ws, rest, s) != hipSuccess) return hipErrorLaunchFailure;
+  return tile == 4 ? grad_experts_tiled<KIND, F, OUT, 4, 4>(g, s) : grad_experts_tiled<KIND, F, OUT, 2, 2>(g, s);
+}
+
+}  // namespace
+
+hipError_t launch_mx4_experts_dgrad(const void* dy, const Experts& e, int64_t m, int64_t n, int64_t lddy,
+                                    const void* w_codes, const void* w_scales, int64_t k, int out_dtype, void* dx,
+                                    int64_t lddx, void* ws, hipStream_t s) {
+  const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)w_codes, (const uint8_t*)w_scales, nullptr, dx, lddx, 0, 0, 1, 0, e};
+  const int tile = expert_dgrad_tile(m, n, k, e.count);
+  switch (out_dtype) {
+    case LQ_F32: return grad_experts<kDgrad, LQ_E2M1, LQ_F32>(g, tile, ws, s);
+    case LQ_BF16: return grad_experts<kDgrad, LQ_E2M1, LQ_BF16>(g, tile, ws, s);
+    default: return grad_experts<kDgrad, LQ_E2M1, LQ_F16>(g, tile, ws, s);
+  }
+}
+
+hipError_t launch_ckpt8_experts_wgrad(int format, const void* dy, const Experts& e, int64_t m, int64_t n, int64_t lddy,
+                                      const void* x_codes, const void* x_scales, int64_t k, const float* dw_in, float* dw,
+                                      int64_t lddw, void* ws, hipStream_t s) {
+  const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)x_codes, (const uint8_t*)x_scales, dw_in, dw, lddw, 0, 0, 1, 0, e};
+  const int tile = expert_wgrad_tile(m, n, k, e.count, dw_in != nullptr);
+  if (format == LQ_INT8) return grad_experts<kWgrad, LQ_INT8, LQ_F32>(g, tile, ws, s);
+  return grad_experts<kWgrad, LQ_E4M3, LQ_F32>(g, tile, ws, s);
 }
 
 }  // namespace lql

@@ -254,6 +254,82 @@ inline bool reads_in_place(int64_t m, int64_t n, int64_t lddy) {
 }
 inline int64_t padded_columns(int64_t n) { return (n + 63) / 64 * 64; }
 
+// ------------------------------------------------------------ rows by expert
+// Rows of x, y and dy lie expert by expert: offsets[e] .. offsets[e + 1] - 1 are
+// expert e's, on the device. Whatever they hold, the ranges taken from them ascend and
+// stay within the m rows.
+constexpr int kMostExperts = 512;
+struct Experts {
+  const int32_t* offsets;
+  int count;
+};
+// A wave's table of the experts' ranges, one expert in each lane of each register: the
+// tiles' LDS leaves no room for one (512 experts' 4 KB keep a second workgroup of 128 x
+// 128 off a compute unit).
+struct ExpertTable {
+  uint32_t end[kMostExperts / 64];     // of each expert's rows
+  uint32_t tiles[kMostExperts / 64];   // of `side` rows up to each expert's last
+  uint32_t first;                      // row of the first expert's
+
+  __device__ __forceinline__ void scan(const Experts& x, int64_t m, uint32_t side) {
+    const int lane = threadIdx.x & 63;
+    auto offset = [&](int i) {
+      const int32_t raw = x.offsets[i < x.count ? i : x.count];
+      return raw < 0 ? 0u : raw > m ? (uint32_t)m : (uint32_t)raw;
+    };
+    uint32_t top = first = __builtin_amdgcn_readfirstlane(offset(0)), sum = 0;
+#pragma unroll
+    for (int c = 0; c < kMostExperts / 64; c++) {
+      end[c] = tiles[c] = 0;
+      if (c * 64 >= x.count) continue;
+      uint32_t e = offset(c * 64 + lane + 1);   // (of lanes past the last expert, the last end again)
+      e = e > top ? e : top;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const uint32_t o = __shfl_up(e, d);
+        if (lane >= d) e = e > o ? e : o;
+      }
+      const uint32_t before = __shfl_up(e, 1);
+      uint32_t t = (e - (lane ? before : top) + side - 1) / side;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const uint32_t o = __shfl_up(t, d);
+        if (lane >= d) t += o;
+      }
+      end[c] = e;
+      tiles[c] = sum + t;
+      top = __builtin_amdgcn_readlane(e, 63);
+      sum = __builtin_amdgcn_readlane(tiles[c], 63);
+    }
+  }
+  // Of expert i (uniform).
+  static __device__ __forceinline__ uint32_t pick(const uint32_t (&v)[kMostExperts / 64], uint32_t i) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int c = 0; c < kMostExperts / 64; c++)
+      if (i / 64 == c) r = __builtin_amdgcn_readlane(v[c], i % 64);
+    return r;
+  }
+  __device__ __forceinline__ uint32_t row_end(uint32_t i) const { return pick(end, i); }
+  __device__ __forceinline__ uint32_t row_begin(uint32_t i) const { return i ? pick(end, i - 1) : first; }
+  __device__ __forceinline__ uint32_t tiles_to(uint32_t i) const { return pick(tiles, i); }
+  __device__ __forceinline__ uint32_t tiles_before(uint32_t i) const { return i ? pick(tiles, i - 1) : 0; }
+  // The expert of the t-th tile of rows (t below all of them).
+  __device__ __forceinline__ uint32_t at(uint32_t t, int count) const {
+    uint32_t n = 0;
+#pragma unroll
+    for (int c = 0; c < kMostExperts / 64; c++)
+      if (c * 64 < count) n += (uint32_t)__builtin_popcountll(__ballot(tiles[c] <= t && c * 64 + (int)(threadIdx.x & 63) < count));
+    return n;
+  }
+};
+// One expert's rows straight from memory.
+__device__ __forceinline__ void expert_rows(const Experts& x, int64_t m, int e, int64_t& begin, int64_t& end) {
+  const int32_t b = x.offsets[e], n = x.offsets[e + 1];
+  begin = b < 0 ? 0 : b > m ? m : b;
+  end = n < begin ? begin : n > m ? m : n;
+}
+
 // ------------------------------------------------------------ shapes of the products
 // Compute units of the current device (256 on MI355X, or with no device).
 inline int compute_units() {
@@ -278,6 +354,10 @@ __host__ __device__ inline int64_t plane_stride(int64_t cols) { return (cols + 3
 inline size_t planes_bytes(const Split& c, int64_t rows, int64_t cols) {
   return c.parts > 1 ? (size_t)c.parts * (size_t)(rows * plane_stride(cols)) * 4 : 0;
 }
+
+// The tile of a product over rows that lie by expert: rows / experts of them on the average (steps of 128, of 64, of 64).
+int expert_tile(int64_t m, int64_t n, int64_t k, int experts), expert_dgrad_tile(int64_t m, int64_t n, int64_t k, int experts);
+int expert_wgrad_tile(int64_t m, int64_t n, int64_t k, int experts, bool adds);
 
 // ------------------------------------------------------------ launchers
 // Instead of launching, the kernel's name and its template arguments for a plan being recorded (lq_plan.h).
@@ -339,5 +419,20 @@ hipError_t launch_int4_pack(const lq_int4_desc* d, const void* codes, const void
                             hipStream_t s);
 hipError_t launch_int4_linear(const lq_int4_desc* d, const void* x, const void* x_scales, const void* packed, void* y,
                               void* ws, hipStream_t s);
+
+// The layer of many experts (lq_mx4.hip, lq_grad.hip): W is an MX4 operand of experts * n rows.
+bool experts_few(int64_t m, int experts), experts_in_place(int64_t m, int64_t k, int experts);
+hipError_t launch_mx4_experts_few(int in_dtype, const void* x, int64_t ldx, const Experts& e, const void* w_codes,
+                                  const void* w_scales, int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy,
+                                  hipStream_t s);
+hipError_t launch_mx4_experts(const void* a_codes, const void* a_scales, const Experts& e, const void* w_codes,
+                              const void* w_scales, int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy,
+                              hipStream_t s);
+hipError_t launch_mx4_experts_dgrad(const void* dy, const Experts& e, int64_t m, int64_t n, int64_t lddy,
+                                    const void* w_codes, const void* w_scales, int64_t k, int out_dtype, void* dx,
+                                    int64_t lddx, void* ws, hipStream_t s);
+hipError_t launch_ckpt8_experts_wgrad(int format, const void* dy, const Experts& e, int64_t m, int64_t n, int64_t lddy,
+                                      const void* x_codes, const void* x_scales, int64_t k, const float* dw_in, float* dw,
+                                      int64_t lddw, void* ws, hipStream_t s);
 
 }  // namespace lql

@@ -73,14 +73,17 @@ constexpr TileCost kWgradTiles[] = {{2, 2, 6.0, 0.56, {0, 0.70, 1.17}, 8.0}, {4,
 // tiles over a long contraction gain from parts (512 x 1024 outputs over 16384:
 // 130 us in one part, 32 in eight); adding the parts up costs a launch and their
 // sums' way through memory and back.
+// Rows that lie by expert end in a tile of their own each, half of one on the
+// average, and are not cut into parts.
 template <size_t N>
-Split cheapest(const TileCost (&tiles)[N], int64_t rows, int64_t cols, int64_t steps, double further) {
+Split cheapest(const TileCost (&tiles)[N], int64_t rows, int64_t cols, int64_t steps, double further, int experts = 0) {
   const double cus = compute_units();
   Split best = {tiles[0].tile, 1, (int)steps};
   double least = 1e300;
   for (const TileCost& c : tiles) {
-    const int64_t side = 64 * c.tile, count = (rows + side - 1) / side * ((cols + side - 1) / side);
+    const int64_t side = 64 * c.tile, count = ((rows + side - 1) / side + experts / 2) * ((cols + side - 1) / side);
     for (int64_t wanted : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      if (experts && wanted > 1) break;
       const int64_t part = (steps + wanted - 1) / wanted, parts = part ? (steps + part - 1) / part : 1;
       if (wanted > 1 && (part < 4 || parts != wanted)) continue;
       const double wgs = (double)count * parts, planes = (double)parts * rows * cols * 4;
@@ -117,6 +120,16 @@ Split split_product(int64_t m, int64_t n, int64_t k, int out_dtype) {
 Split split_dgrad(int64_t m, int64_t n, int64_t k) { return cheapest(kDgradTiles, m, k, (n + 63) / 64, 0.0); }
 Split split_wgrad(int64_t m, int64_t n, int64_t k, bool adds) {
   return cheapest(kWgradTiles, n, k, (m + 63) / 64, adds ? (double)n * k * 4 : 0.0);
+}
+int expert_tile(int64_t m, int64_t n, int64_t k, int experts) {
+  return cheapest(kProductTiles, m, n, mx4_groups(k), 0.0, experts).tile;
+}
+int expert_dgrad_tile(int64_t m, int64_t n, int64_t k, int experts) {
+  return cheapest(kDgradTiles, m, k, (n + 63) / 64, 0.0, experts).tile;
+}
+// (the weights' rows are as many for each; they are contracted over an expert's share of the rows)
+int expert_wgrad_tile(int64_t m, int64_t n, int64_t k, int experts, bool adds) {
+  return cheapest(kWgradTiles, n * experts, k, (m + 63) / 64 / experts + 1, adds ? (double)n * k * experts * 4 : 0.0, 1).tile;
 }
 
 }  // namespace lql

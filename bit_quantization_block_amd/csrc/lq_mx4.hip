@@ -69,6 +69,7 @@ constexpr int kStages = 4;
 // 16 different units of 256 bytes.
 __device__ __forceinline__ int swizzled(int row, int unit) { return (unit ^ (row >> 2 & 3)) * 16; }
 
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 // A stretch of memory for buffer loads: what lies past its end reads as zero.
 __device__ __forceinline__ v4i stretch(const uint8_t* p, uint32_t bytes) {
   const uint64_t b = (uint64_t)(uintptr_t)p;
@@ -108,15 +109,22 @@ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t tm, uint32_t tn, ui
   col = __builtin_amdgcn_readfirstlane(in / high);
 }
 
-template <int OUT, int FM, int FN>
-__global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
-                                                        int64_t m, int64_t n, int64_t k, void* y, int64_t ldy,
-                                                        uint32_t tm, uint32_t tn, uint32_t parts, int part_groups) {
+// BY_EXPERT: the rows lie by expert, each multiplied by its own n rows of W; a tile
+// belongs to one of them.
+template <int OUT, int FM, int FN, bool BY_EXPERT>
+__device__ __forceinline__ void mx4_product(const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
+                                            int64_t m, int64_t n, int64_t k, void* y, int64_t ldy, uint32_t tm,
+                                            uint32_t tn, uint32_t parts, int part_groups, const Experts& experts) {
   typedef typename El<OUT>::T T;
   constexpr int BM = 64 * FM, BN = 64 * FN;
   __shared__ ProductLds<FM, FN> lds;
+  ExpertTable table;
+  if constexpr (BY_EXPERT) {
+    table.scan(experts, m, BM);
+    tm = table.tiles_to(experts.count - 1);
+  }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
+  const int r = lane & 31, h = lane >> 5, wm = wave >> 1, wc = wave & 1;
 
   // This workgroup's tiles: its XCD's share, every `slots`-th from its own on.
   // With the contraction in parts, part p of a tile is a tile of its own, whose
@@ -134,10 +142,32 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
     const uint8_t *x, *w, *xs, *ws;   // codes and scales of its first rows, in group 0
     uint32_t rows, cols;              // that exist, at most BM and BN; 0: no tile
     int deep;                         // groups of the contraction
+    uint32_t xsbytes, wsbytes, r0, last;   // by expert: of a group's scales; the first row, the expert's rows' end
   };
+  const int64_t wn = BY_EXPERT ? experts.count * n : n;   // rows of W as it is stored
+  // (by expert, `part` is the tile's expert and `row` its place among that one's)
   auto place = [&](uint32_t row, uint32_t col, uint32_t part, bool real) {
-    const int64_t r0 = (int64_t)row * BM, c0 = (int64_t)col * BN, g0 = (int64_t)part * part_groups;
     Tile t;
+    if constexpr (BY_EXPERT) {
+      const int64_t r0 = (int64_t)table.row_begin(part) + (int64_t)row * BM, last = table.row_end(part);
+      const int64_t c0 = (int64_t)col * BN, w0 = part * n + c0;
+      t.r0 = uniform((uint32_t)r0);
+      t.last = uniform((uint32_t)last);
+      t.x = x + r0 * 64;
+      t.w = w + w0 * 64;
+      t.xs = xs + r0 * 4;
+      t.ws = ws + w0 * 4;
+      t.deep = groups;
+      t.rows = real ? (uint32_t)(last - r0 < BM ? last - r0 : BM) : 0;
+      t.cols = real ? (uint32_t)(n - c0 < BN ? n - c0 : BN) : 0;
+      // (a transfer's 16 bytes start at any row: the last one of a group ends where its scales do)
+      const int64_t xleft = (mx4_scale_rows(m) - r0) * 4, wleft = (mx4_scale_rows(wn) - w0) * 4;
+      const uint32_t xb = (t.rows + 3) / 4 * 16, wb = (t.cols + 3) / 4 * 16;
+      t.xsbytes = xb < xleft ? xb : (uint32_t)xleft;
+      t.wsbytes = wb < wleft ? wb : (uint32_t)wleft;
+      return t;
+    }
+    const int64_t r0 = (int64_t)row * BM, c0 = (int64_t)col * BN, g0 = (int64_t)part * part_groups;
     t.x = x + (g0 * m + r0) * 64;
     t.w = w + (g0 * n + c0) * 64;
     t.xs = xs + (g0 * mx4_scale_rows(m) + r0) * 4;
@@ -149,6 +179,12 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
   };
   uint32_t trow, tcol, tpart, nrow, ncol, npart;
   auto tile_of = [&](uint32_t t, uint32_t& row, uint32_t& col, uint32_t& part) {
+    if constexpr (BY_EXPERT) {
+      part = uniform(table.at(t / tn, experts.count));
+      const uint32_t before = table.tiles_before(part), high = table.tiles_to(part) - before;
+      tile_at(t - before * tn, high, tn, row, col);
+      return;
+    }
     part = parts == 1 ? 0 : __builtin_amdgcn_readfirstlane(t / (tm * tn));
     tile_at(t - part * (tm * tn), tm, tn, row, col);
   };
@@ -178,13 +214,17 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
   }
   auto lds_at = [](const void* p) { return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p; };
   const uint32_t lx = lds_at(&lds.x[0][wave * FM * 16][0]), lw = lds_at(&lds.w[0][wave * FN * 16][0]), ls = lds_at(&lds.s[0][wave & 1][0][0]);
-  const int64_t xgroup = m * 64, wgroup = n * 64, sgroup = mx4_scale_rows(wave & 1 ? n : m) * 4;
+  const int64_t xgroup = m * 64, wgroup = wn * 64, sgroup = mx4_scale_rows(wave & 1 ? wn : m) * 4;
+  auto scale_bytes = [&](const Tile& t) {
+    if constexpr (BY_EXPERT) return wave & 1 ? t.wsbytes : t.xsbytes;
+    return ((wave & 1 ? t.cols : t.rows) + 3) / 4 * 16;
+  };
   // The step whose transfers come next: what is left of its rows in memory.
   struct Cursor {
     const uint8_t *x, *w, *s;
     int t, deep;
   } at = {now.x, now.w, wave & 1 ? now.ws : now.xs, 0, now.deep};
-  uint32_t xbytes = now.rows * 64, wbytes = now.cols * 64, sbytes = ((wave & 1 ? now.cols : now.rows) + 3) / 4 * 16;
+  uint32_t xbytes = now.rows * 64, wbytes = now.cols * 64, sbytes = scale_bytes(now);
   v4i fx, fw, fs;
   auto point_x = [&] { fx = stretch(at.x, at.t < at.deep ? xbytes : 0); };
   auto point_w = [&] { fw = stretch(at.w, at.t < at.deep ? wbytes : 0); };
@@ -197,7 +237,7 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
     at.s = wrap ? (wave & 1 ? next.ws : next.xs) : at.s + sgroup;
     xbytes = wrap ? next.rows * 64 : xbytes;
     wbytes = wrap ? next.cols * 64 : wbytes;
-    sbytes = wrap ? ((wave & 1 ? next.cols : next.rows) + 3) / 4 * 16 : sbytes;
+    sbytes = wrap ? scale_bytes(next) : sbytes;
     at.t = wrap ? 0 : at.t;
     at.deep = wrap ? next.deep : at.deep;
   };
@@ -216,11 +256,11 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
   auto read = [&](int st, int s, Operands& o, int f) {
     const int u = swizzled(r, 2 * h + s);
     if (f < FM) o.x[f] = *(const v4i*)&lds.x[st][wm * 32 * FM + f * 32 + r][u];
-    else o.w[f - FM] = *(const v4i*)&lds.w[st][wn * 32 * FN + (f - FM) * 32 + r][u];
+    else o.w[f - FM] = *(const v4i*)&lds.w[st][wc * 32 * FN + (f - FM) * 32 + r][u];
   };
   auto read_scale = [&](int st, Scales& e, int f) {
     if (f < FM) e.x[f] = *(const uint16_t*)&lds.s[st][0][wm * 32 * FM + f * 32 + r][2 * h];
-    else e.w[f - FM] = *(const uint16_t*)&lds.s[st][1][wn * 32 * FN + (f - FM) * 32 + r][2 * h];
+    else e.w[f - FM] = *(const uint16_t*)&lds.s[st][1][wc * 32 * FN + (f - FM) * 32 + r][2 * h];
   };
   v16f acc[FM][FN];
   // One half's products; `between` runs after each.
@@ -325,10 +365,17 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
     uint8_t* mine = lds.out[wave];
     uint8_t* const put = mine + (l & 31) * kRow;
     const int turn = (l & 31) >> 1, part = (l >> 5) * 4 * (int)sizeof(T);
-    const int64_t row0 = (int64_t)trow * BM + wm * 32 * FM, col0 = (int64_t)tcol * BN + wn * 32 * FN;
+    int64_t row0 = (int64_t)trow * BM + wm * 32 * FM, last_row = m, plane_row = 0;
+    if constexpr (BY_EXPERT) {
+      row0 = (int64_t)now.r0 + wm * 32 * FM;
+      last_row = now.last;
+    } else {
+      plane_row = tpart * m;
+    }
+    const int64_t col0 = (int64_t)tcol * BN + wc * 32 * FN;
     const int rr = l / units, cc = l % units;
-    T* const out = (T*)y + (tpart * m + row0 + rr) * ldy + col0 + cc * V;
-    const int rows_left = (int)(m - row0 < 32 * FM ? m - row0 : 32 * FM) - rr, cols_left = (int)(n - col0 < 32 * FN ? n - col0 : 32 * FN) - cc * V;
+    T* const out = (T*)y + (plane_row + row0 + rr) * ldy + col0 + cc * V;
+    const int rows_left = (int)(last_row - row0 < 32 * FM ? last_row - row0 : 32 * FM) - rr, cols_left = (int)(n - col0 < 32 * FN ? n - col0 : 32 * FN) - cc * V;
 #pragma unroll
     for (int i = 0; i < FM; i++)
 #pragma unroll
@@ -372,6 +419,18 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(cons
   }
   // (the transfers after the last step wrote zeros into LDS: they end before it is given away)
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+template <int OUT, int FM, int FN>
+__global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_product(const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
+                                                        int64_t m, int64_t n, int64_t k, void* y, int64_t ldy,
+                                                        uint32_t tm, uint32_t tn, uint32_t parts, int part_groups) {
+  mx4_product<OUT, FM, FN, false>(x, xs, w, ws, m, n, k, y, ldy, tm, tn, parts, part_groups, Experts());
+}
+template <int OUT, int FM, int FN>
+__global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_mx4_experts(const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
+                                                        int64_t m, int64_t n, int64_t k, void* y, int64_t ldy, uint32_t tn,
+                                                        Experts experts) {
+  mx4_product<OUT, FM, FN, true>(x, xs, w, ws, m, n, k, y, ldy, 0, tn, 1, (int)mx4_groups(k), experts);
 }
 
 // ---------------------------------------------------------------- a few rows
@@ -426,10 +485,11 @@ __device__ __forceinline__ v4i quantise_block(const Block<SRC>& block, uint32_t&
   return out;
 }
 
+// (wn and w0: rows of W as it is stored, and the one that these n begin at; xm and x0 likewise of an MX4 operand's m)
 template <int SRC, int OUT, int R, int CT>
-__global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64_t ldx, const uint8_t* xs, const uint8_t* w,
-                                                            const uint8_t* ws, int64_t m, int64_t n, int64_t k, void* y,
-                                                            int64_t ldy) {
+__device__ __forceinline__ void mx4_few(const void* x, int64_t ldx, const uint8_t* xs, int64_t xm, int64_t x0,
+                                        const uint8_t* w, const uint8_t* ws, int64_t wn, int64_t w0, int64_t m, int64_t n,
+                                        int64_t k, void* y, int64_t ldy) {
   typedef typename El<OUT>::T T;
   constexpr bool own = SRC != kOperand;
   __shared__ v4f sums[kFewWaves][R * CT][64];
@@ -440,10 +500,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64
   const int64_t row0 = (int64_t)blockIdx.x * 16 * R;
   const int groups = (int)mx4_groups(k), per = (groups + kFewWaves - 1) / kFewWaves;
   const int begin = wave * per, end = begin + per < groups ? begin + per : groups;
-  const int64_t wstep = mx4_scale_rows(n) * 4, xstep = mx4_scale_rows(m) * 4;
+  const int64_t wstep = mx4_scale_rows(wn) * 4, xstep = mx4_scale_rows(xm) * 4;
   int64_t wrow[R];   // rows past the last are the last again
 #pragma unroll
-  for (int i = 0; i < R; i++) wrow[i] = row0 + i * 16 + r < n ? row0 + i * 16 + r : n - 1;
+  for (int i = 0; i < R; i++) wrow[i] = row0 + i * 16 + r < n ? w0 + row0 + i * 16 + r : w0 + n - 1;
 
   constexpr int U = CT == 4 ? 2 : 4;   // groups whose reads are in flight together (4 of 64 rows' would leave one wave on a SIMD)
   struct Reads {
@@ -456,14 +516,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64
       const int g = g0 + u < groups ? g0 + u : groups - 1;
 #pragma unroll
       for (int i = 0; i < R; i++) {
-        a.wc[u][i] = *(const v4i*)(w + (g * n + wrow[i]) * 64 + q * 16);
+        a.wc[u][i] = *(const v4i*)(w + (g * wn + wrow[i]) * 64 + q * 16);
         a.we[u][i] = ws[g * wstep + wrow[i] * 4 + q];
       }
       if constexpr (!own) {
 #pragma unroll
         for (int c = 0; c < CT; c++) {
-          const int64_t at = c * 16 + r < m ? c * 16 + r : m - 1;
-          a.xc[u][c] = *(const v4i*)((const uint8_t*)x + (g * m + at) * 64 + q * 16);
+          const int64_t at = x0 + (c * 16 + r < m ? (int64_t)(c * 16 + r) : m - 1);
+          a.xc[u][c] = *(const v4i*)((const uint8_t*)x + (g * xm + at) * 64 + q * 16);
           a.xe[u][c] = xs[g * xstep + at * 4 + q];
         }
       }
@@ -547,6 +607,30 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64
       for (int e = 0; e < 4; e++)
         if (col + e < n) o[e] = narrow<OUT>(s[e]);
     }
+  }
+}
+
+template <int SRC, int OUT, int R, int CT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64_t ldx, const uint8_t* xs, const uint8_t* w,
+                                                            const uint8_t* ws, int64_t m, int64_t n, int64_t k, void* y,
+                                                            int64_t ldy) {
+  mx4_few<SRC, OUT, R, CT>(x, ldx, xs, m, 0, w, ws, n, 0, m, n, k, y, ldy);
+}
+// By expert, one a row of the grid: 16 rows at a time, or as many as fit in LDS.
+template <int SRC, int OUT, int R>
+__global__ __launch_bounds__(64 * kFewWaves) void k_mx4_experts_few(const void* x, int64_t ldx, const uint8_t* xs,
+                                                                    const uint8_t* w, const uint8_t* ws, int64_t m, int64_t n,
+                                                                    int64_t k, void* y, int64_t ldy, Experts experts) {
+  typedef typename El<OUT>::T T;
+  int64_t begin, end;
+  expert_rows(experts, m, blockIdx.y, begin, end);
+  const int64_t blocks = mx4_groups(k) * 4, fit = SRC == kOperand ? 16 : kFewBlocks / blocks, most = fit < 16 ? fit : 16;
+  for (int64_t row = begin; row < end; row += most) {
+    if (row > begin) __syncthreads();   // (the last rows' sums have been read)
+    const int64_t rows = end - row < most ? end - row : most;
+    const void* from = x;
+    if constexpr (SRC != kOperand) from = (const typename El<SRC>::T*)x + row * ldx;
+    mx4_few<SRC, OUT, R, 1>(from, ldx, xs, m, row, w, ws, experts.count * n, blockIdx.y * n, rows, n, k, (T*)y + row * ldy, ldy);
   }
 }
 
@@ -720,6 +804,84 @@ hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const v
     case LQ_F32: return product_dt<LQ_F32>(a_codes, a_scales, w_codes, w_scales, m, n, k, y, ldy, planes, s);
     case LQ_BF16: return product_dt<LQ_BF16>(a_codes, a_scales, w_codes, w_scales, m, n, k, y, ldy, planes, s);
     default: return product_dt<LQ_F16>(a_codes, a_scales, w_codes, w_scales, m, n, k, y, ldy, planes, s);
+  }
+}
+
+// Rows by expert: few of each are bound by reading W, which a row of workgroups reads
+// once for sixteen rows.
+bool experts_few(int64_t m, int experts) { return m <= 16 * (int64_t)experts; }
+// Few rows straight from x, at least one of them at a time in LDS (and not many more
+// than a launch of its own is worth).
+bool experts_in_place(int64_t m, int64_t k, int experts) {
+  return experts_few(m, experts) && mx4_groups(k) * 4 <= kFewBlocks;
+}
+
+namespace {
+
+template <int SRC, int OUT>
+hipError_t experts_few_out(const void* x, int64_t ldx, const void* xs, const Experts& e, const void* w, const void* ws,
+                           int64_t m, int64_t n, int64_t k, void* y, int64_t ldy, hipStream_t s) {
+  // 32 rows of W a workgroup where the experts with rows leave one of those for each compute unit, as above
+  const int r = n * (m < e.count ? m : e.count) >= 32 * (int64_t)compute_units() ? 2 : 1;
+  const dim3 grid((unsigned)((n + 16 * r - 1) / (16 * r)), (unsigned)e.count);
+  if (r == 2)
+    hipLaunchKernelGGL((k_mx4_experts_few<SRC, OUT, 2>), grid, dim3(64 * kFewWaves), 0, s, x, ldx, (const uint8_t*)xs,
+                       (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy, e);
+  else
+    hipLaunchKernelGGL((k_mx4_experts_few<SRC, OUT, 1>), grid, dim3(64 * kFewWaves), 0, s, x, ldx, (const uint8_t*)xs,
+                       (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy, e);
+  return hipGetLastError();
+}
+template <int SRC>
+hipError_t experts_few_src(const void* x, int64_t ldx, const void* xs, const Experts& e, const void* w, const void* ws,
+                           int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s) {
+  switch (out_dtype) {
+    case LQ_F32: return experts_few_out<SRC, LQ_F32>(x, ldx, xs, e, w, ws, m, n, k, y, ldy, s);
+    case LQ_BF16: return experts_few_out<SRC, LQ_BF16>(x, ldx, xs, e, w, ws, m, n, k, y, ldy, s);
+    default: return experts_few_out<SRC, LQ_F16>(x, ldx, xs, e, w, ws, m, n, k, y, ldy, s);
+  }
+}
+template <int OUT, int FM, int FN>
+hipError_t experts_tiled(const void* a, const void* as, const Experts& e, const void* w, const void* ws, int64_t m,
+                         int64_t n, int64_t k, void* y, int64_t ldy, hipStream_t s) {
+  // (at most one tile of rows an expert more than if the rows were one's)
+  const int64_t tn = (n + 64 * FN - 1) / (64 * FN), tiles = (m / (64 * FM) + e.count) * tn;
+  const int64_t most = (int64_t)compute_units() * (int)(163840 / sizeof(ProductLds<FM, FN>));
+  const dim3 grid((unsigned)(tiles < most ? tiles : most));
+  hipLaunchKernelGGL((k_mx4_experts<OUT, FM, FN>), grid, dim3(256), 0, s, (const uint8_t*)a, (const uint8_t*)as,
+                     (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy, (uint32_t)tn, e);
+  return hipGetLastError();
+}
+template <int OUT>
+hipError_t experts_out(const void* a, const void* as, const Experts& e, const void* w, const void* ws, int64_t m, int64_t n,
+                       int64_t k, void* y, int64_t ldy, hipStream_t s) {
+  const int tile = expert_tile(m, n, k, e.count);
+  if (tile == 4) return experts_tiled<OUT, 4, 4>(a, as, e, w, ws, m, n, k, y, ldy, s);
+  if (tile == 2) return experts_tiled<OUT, 2, 2>(a, as, e, w, ws, m, n, k, y, ldy, s);
+  return experts_tiled<OUT, 1, 1>(a, as, e, w, ws, m, n, k, y, ldy, s);
+}
+
+}  // namespace
+
+hipError_t launch_mx4_experts_few(int in_dtype, const void* x, int64_t ldx, const Experts& e, const void* w_codes,
+                                  const void* w_scales, int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy,
+                                  hipStream_t s) {
+  switch (in_dtype) {
+    case LQ_F32: return experts_few_src<LQ_F32>(x, ldx, nullptr, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
+    case LQ_BF16: return experts_few_src<LQ_BF16>(x, ldx, nullptr, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
+    default: return experts_few_src<LQ_F16>(x, ldx, nullptr, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
+  }
+}
+
+hipError_t launch_mx4_experts(const void* a_codes, const void* a_scales, const Experts& e, const void* w_codes,
+                              const void* w_scales, int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy,
+                              hipStream_t s) {
+  if (experts_few(m, e.count))
+    return experts_few_src<kOperand>(a_codes, 0, a_scales, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
+  switch (out_dtype) {
+    case LQ_F32: return experts_out<LQ_F32>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
+    case LQ_BF16: return experts_out<LQ_BF16>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
+    default: return experts_out<LQ_F16>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
   }
 }
 

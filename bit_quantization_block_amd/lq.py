@@ -31,7 +31,8 @@ EXPORTS = ("lq_quantize", "lq_dequantize", "lq_fake_quant_qsnr", "lq_hadamard_qu
            "lq_linear_workspace_bytes", "lq_mx4_quantize", "lq_mx4_product", "lq_mx4_linear", "lq_mx4_dgrad",
            "lq_ckpt8_wgrad", "lq_linear_kernels", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward",
            "lq_rmsnorm", "lq_rmsnorm_workspace_bytes", "lq_rmsnorm_backward", "lq_int4_packed_bytes",
-           "lq_int4_pack", "lq_int4_workspace_bytes", "lq_int4_linear")
+           "lq_int4_pack", "lq_int4_workspace_bytes", "lq_int4_linear", "lq_experts_workspace_bytes", "lq_mx4_experts",
+           "lq_mx4_experts_dgrad", "lq_ckpt8_experts_wgrad")
 LINEAR_CALL = {"quantize": 0, "product": 1, "linear": 2, "dgrad": 3, "wgrad": 4}
 # output bits of lq_call_kernels
 OUT = {"codes": 1, "scales": 2, "zeros": 4, "y": 8, "res": 16}
@@ -71,6 +72,11 @@ class NormDesc(ctypes.Structure):
 
 class Int4Desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("in_dtype", "x_format", "out_dtype", "group", "zero_points", "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("m", "n", "k", "ld_in", "ld_out")]
+
+
+class ExpertsDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_dtype", "out_dtype", "ckpt_format", "experts")] + \
                [(n, ctypes.c_int64) for n in ("m", "n", "k", "ld_in", "ld_out")]
 
 
@@ -133,6 +139,14 @@ def load(path: str | None = None):
     L.lq_int4_pack.argtypes = [ip, vp, vp, vp, vp, vp]
     L.lq_int4_linear.argtypes = [ip, vp, vp, vp, vp, vp, sz, vp]
     L.lq_int4_pack.restype = L.lq_int4_linear.restype = ctypes.c_int
+    ep = ctypes.POINTER(ExpertsDesc)
+    L.lq_experts_workspace_bytes.argtypes = [ep]
+    L.lq_experts_workspace_bytes.restype = sz
+    L.lq_mx4_experts.argtypes = [ep, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.lq_mx4_experts_dgrad.argtypes = [ep, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.lq_ckpt8_experts_wgrad.argtypes = [ep, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    for f in ("lq_mx4_experts", "lq_mx4_experts_dgrad", "lq_ckpt8_experts_wgrad"):
+        getattr(L, f).restype = ctypes.c_int
     L.lq_linear_kernels.argtypes = [lp, ctypes.c_int, ctypes.c_int, ctypes.c_char_p, sz]
     for f in ("lq_mx4_quantize", "lq_mx4_product", "lq_mx4_linear", "lq_mx4_dgrad", "lq_ckpt8_wgrad",
               "lq_linear_kernels", "lq_swiglu_ckpt8", "lq_swiglu_ckpt8_backward"):
@@ -1135,6 +1149,179 @@ class Int4Linear:
         if rc != LQ_OK:
             raise LQError("lq_int4_linear", rc)
         return y
+
+
+class Mx4Experts:
+    """A low-bit linear layer of many experts, and its gradients, as Mx4Linear's calls of their own: each row of x goes
+    through the weights of one expert. `w` [experts, n, k] is quantised once. Rows lie expert by expert: `offsets`
+    [experts + 1], int32 on the GPU, is where each one's rows begin and, at its end, where the last one's end (as a
+    router's counts add up to; nothing waits for their values). Rows behind the last expert's are not written. `rows` is
+    the most rows a call may have. Buffers, dtypes, streams, alignment and autograd: as Mx4Linear's."""
+
+    def __init__(self, w, rows: int, dtype: str = "bf16", out: str = "bf16", lib=None):
+        import torch
+
+        if w.dim() != 3:
+            raise ValueError(f"w has shape {tuple(w.shape)}, expected [experts, n, k]")
+        self.torch = torch
+        self._index = w.device.index
+        self.lib = _library(lib, self._index)
+        self.experts, self.n, self.k = w.shape
+        self.rows, self.dtype, self.out = rows, dtype, out
+        self.device = w.device
+        u8 = dict(dtype=torch.uint8, device=w.device)
+        self.codes = torch.empty(max(16, self.lib.lq_mx4_codes_bytes(self.experts * self.n, self.k)), **u8)
+        self.scales = torch.empty(max(16, self.lib.lq_mx4_scales_bytes(self.experts * self.n, self.k)), **u8)
+        self.load(w)
+        self._wc, self._ws = ctypes.c_void_p(self.codes.data_ptr()), ctypes.c_void_p(self.scales.data_ptr())
+        self._plans = {}
+        self._buffers = {}
+        self._workspaces = []
+
+    _workspace = Mx4Linear._workspace
+    _apart = Mx4Linear._apart
+    _check_ckpt = Mx4Linear._check_ckpt
+
+    def load(self, w, stream=None):
+        """Quantises w into the layer: its weights from the next call on, as after an optimizer's step."""
+        if w.dim() != 3 or tuple(w.shape) != (self.experts, self.n, self.k):
+            raise ValueError(f"w has shape {tuple(w.shape)}, expected {(self.experts, self.n, self.k)}")
+        if self.experts > 1 and self.n > 1 and w.stride(0) != self.n * w.stride(1):
+            raise ValueError(f"w's experts must lie one after the other (strides {w.stride()})")
+        flat = w.flatten(0, 1) if self.n > 1 or w.stride(0) == w.stride(1) else w[:, 0]
+        ld = _matrix(flat, self.experts * self.n, self.k, w.dtype, "w")
+        if w.device != self.device:
+            raise ValueError(f"w is on {w.device}, the layer on {self.device}")
+        d = LinearDesc(DTYPE[_dtype_name(w)], 0, 0, 0, self.experts * self.n, 0, self.k, ld, 0)
+        _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(flat), _ptr(self.codes),
+                                                           _ptr(self.scales), None, None,
+                                                           _stream_of(self._index, stream)))
+
+    def _cube(self, t, what):
+        """A float32 device tensor [experts, n, k], its experts one after the other; the stride of its rows."""
+        if tuple(t.shape) != (self.experts, self.n, self.k):
+            raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {(self.experts, self.n, self.k)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+        if t.dtype != self.torch.float32:
+            raise TypeError(f"{what} is {t.dtype}, expected torch.float32")
+        if not t.is_cuda or t.device != self.device:
+            raise ValueError(f"{what} is on {t.device}, the layer on {self.device}")
+
+    def _plan(self, key, kind, a, what, offsets, cols_in, cols_out, in_dtype, out_dtype, fmt, out, stream):
+        m = a.shape[0]
+        if m > self.rows:
+            raise ValueError(f"{m} rows in a layer planned for {self.rows}")
+        if offsets.dtype != self.torch.int32 or tuple(offsets.shape) != (self.experts + 1,) or not offsets.is_contiguous():
+            raise ValueError(f"offsets are {offsets.dtype} {tuple(offsets.shape)}, expected int32 {(self.experts + 1,)}, contiguous")
+        ld_in = _matrix(a, m, cols_in, _torch_dtype(in_dtype), what)
+        for t in (a, offsets, out):
+            if t is not None and t.device != self.device:
+                raise ValueError(f"a tensor is on {t.device}, the layer on {self.device}")
+        if kind == "dw":
+            shape, buffer, ld_out = (self.experts, self.n, self.k), None, self.k
+            if out is not None:
+                self._cube(out, "out")
+        else:
+            shape, buffer, ld_out = (self.rows, cols_out), None, cols_out
+            if out is not None:
+                ld_out = _matrix(out, m, cols_out, _torch_dtype(out_dtype), "out")
+        if out is None:
+            buffer = self._buffers.get(kind)
+            if buffer is None:
+                buffer = self._buffers[kind] = _empty_for(stream, *shape, dtype=_torch_dtype(out_dtype), device=self.device)
+            if kind != "dw":
+                buffer = buffer[:m]
+        d = ExpertsDesc(DTYPE[in_dtype], DTYPE[out_dtype], FORMAT[fmt], self.experts, m, self.n, self.k, ld_in, ld_out)
+        ref = ctypes.byref(d)
+        need = self.lib.lq_experts_workspace_bytes(ref)
+        if need == 0:   # the descriptor is refused: by this call too, with the status
+            _check("lq_mx4_experts", self.lib.lq_mx4_experts(ref, None, None, None, None, None, None, None, None, 0, None))
+        ws = self._workspace(need, stream)
+        if len(self._plans) >= 256:
+            self._plans.clear()
+        at = 0 if buffer is None else buffer.data_ptr()
+        rows_out = self.experts * self.n if kind == "dw" else m
+        plan = self._plans[key] = (ref, ctypes.c_void_p(ws.data_ptr()), ws.numel(), buffer, at,
+                                   at - _reach(m, ld_in, cols_in, _torch_dtype(in_dtype).itemsize),
+                                   at + _reach(rows_out, ld_out, cols_out, _torch_dtype(out_dtype).itemsize))
+        return plan
+
+    def forward(self, x, offsets, ckpt: Ckpt8 | None = None, out=None, stream=None):
+        """y_i = Q4(x_i) W_e^T for expert e's rows i; `ckpt` also receives x in 8 bits."""
+        if x.requires_grad:
+            _refuse_grad(x=x)
+        fmt = "int8" if ckpt is None else ckpt.fmt
+        key = ("y", fmt) + _layout(x, offsets, out)
+        plan = self._plans.get(key) or self._plan(key, "y", x, "x", offsets, self.k, self.n, self.dtype, self.out, fmt, out,
+                                                  stream)
+        cc = cs = None
+        if ckpt is not None:
+            self._check_ckpt(ckpt, x.shape[0])
+            cc, cs = ckpt.codes.data_ptr(), ckpt.scales.data_ptr()
+        ref, ws, ws_bytes, y, yp, low, high = plan
+        if out is not None:
+            y, yp = out, out.data_ptr()
+            low, high = low + yp, high + yp
+        xp = x.data_ptr()
+        if low < xp < high:
+            y = self._apart("y", "x", x, y, out, stream)
+            yp = y.data_ptr()
+        rc = self.lib.lq_mx4_experts(ref, xp, offsets.data_ptr(), self._wc, self._ws, yp, cc, cs, ws, ws_bytes,
+                                     _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_mx4_experts", rc)
+        return y
+
+    def dgrad(self, dy, offsets, out=None, stream=None):
+        """dx_i = dy_i W_e."""
+        if dy.requires_grad:
+            _refuse_grad(dy=dy)
+        key = ("dx",) + _layout(dy, offsets, out)
+        plan = self._plans.get(key) or self._plan(key, "dx", dy, "dy", offsets, self.n, self.k, "bf16", self.out, "int8", out,
+                                                  stream)
+        ref, ws, ws_bytes, dx, xp, low, high = plan
+        if out is not None:
+            dx, xp = out, out.data_ptr()
+            low, high = low + xp, high + xp
+        yp = dy.data_ptr()
+        if low < yp < high:
+            dx = self._apart("dx", "dy", dy, dx, out, stream)
+            xp = dx.data_ptr()
+        rc = self.lib.lq_mx4_experts_dgrad(ref, yp, offsets.data_ptr(), self._wc, self._ws, xp, ws, ws_bytes,
+                                           _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_mx4_experts_dgrad", rc)
+        return dx
+
+    def wgrad(self, dy, ckpt: Ckpt8, offsets, dw_in=None, out=None, stream=None):
+        """dw_e = dw_in_e + the sum over e's rows of dy_i^T x8_i, x8 the checkpoint that forward wrote; dw_in and `out` are
+        float32 [experts, n, k], contiguous, and may be the same."""
+        if dy.requires_grad:
+            _refuse_grad(dy=dy)
+        key = ("dw", ckpt.fmt) + _layout(dy, offsets, dw_in, out)
+        plan = self._plans.get(key)
+        if plan is None:
+            if dw_in is not None:
+                self._cube(dw_in, "dw_in")
+            plan = self._plan(key, "dw", dy, "dy", offsets, self.n, self.k, "bf16", "f32", ckpt.fmt, out, stream)
+        self._check_ckpt(ckpt, dy.shape[0])
+        ref, ws, ws_bytes, dw, wp, low, high = plan
+        if out is not None:
+            dw, wp = out, out.data_ptr()
+            low, high = low + wp, high + wp
+        yp, ap = dy.data_ptr(), None
+        if low < yp < high and _share(dy, dw.view(-1, self.k)):
+            raise ValueError("dy and the result share memory")
+        if dw_in is not None:
+            ap = dw_in.data_ptr()
+            if ap != wp and abs(ap - wp) < high - wp:
+                raise ValueError("dw_in and the result share memory, but are not the same")
+        rc = self.lib.lq_ckpt8_experts_wgrad(ref, yp, offsets.data_ptr(), ckpt.codes.data_ptr(), ckpt.scales.data_ptr(), ap,
+                                             wp, ws, ws_bytes, _stream_of(self._index, stream))
+        if rc != LQ_OK:
+            raise LQError("lq_ckpt8_experts_wgrad", rc)
+        return dw
 
 
 # ------------------------------------------------------------------ ceilings

@@ -45,7 +45,7 @@ def _header_types(text: str, path: str) -> str:
     text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
     out = re.findall(r"^#define LQ_\w+ .*$", text, flags=re.M)
     for body, name in re.findall(r"typedef (?:struct|enum)\s*\{([^}]*)\}\s*(\w+);", text):
-        if name.startswith(("lq_linear", "lq_swiglu", "lq_norm", "lq_int4")) <= (path == "linear"):
+        if name.startswith(("lq_linear", "lq_swiglu", "lq_norm", "lq_int4", "lq_experts")) <= (path == "linear"):
             out.append(name + " " + body)
     return _code_only("\n".join(out))
 

@@ -481,6 +481,47 @@ LQ_API size_t lq_int4_workspace_bytes(const lq_int4_desc* desc);
 LQ_API int lq_int4_linear(const lq_int4_desc* desc, const void* x, const void* x_scales, const void* packed, void* y,
                           void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A low-bit linear layer of many experts: each row of x belongs to one of them, and
+ * rows lie expert by expert. offsets [experts + 1] (int32, in DEVICE memory) tell
+ * where each one's begin, and the last where they end: rows offsets[e] ..
+ * offsets[e + 1] - 1 are expert e's, as many as there are, or none.
+ *
+ *   y_i = Q4(x_i) W_e^T     dx_i = dy_i W_e     dw_e = dw_in_e + sum over e's rows of dy_i^T x8_i
+ *
+ * Numerics, layouts and the forward call's checkpoint (of all m rows) are the linear
+ * layer's. W is one MX4 operand of experts * n rows, an expert's n after another's
+ * (lq_mx4_quantize with m = experts * n); dw likewise, fp32 [experts * n, k]. Of y and
+ * dx only the experts' rows are written: others, as those past offsets[experts], are
+ * left as they were; dw_e of an expert without rows is dw_in_e, or zeros.
+ * The offsets ascend from 0 or more to m at most. Whatever else they hold, a call reads
+ * and writes within its buffers only, but results are then unspecified.
+ *
+ * experts is 1 .. 512, n and k at least 1 and at most 2^21, experts * n at most 2^31-1.
+ * Streams, errors, alignment and workspaces (lq_experts_workspace_bytes(), 0 on a bad
+ * descriptor) as of the linear layer; dw may be dw_in. */
+typedef struct {
+  int32_t in_dtype;    /* lq_dtype of x (forward) or of dy (gradients: LQ_BF16, else LQ_ERR_UNSUPPORTED) */
+  int32_t out_dtype;   /* lq_dtype of y or dx; of dw: LQ_F32, else LQ_ERR_UNSUPPORTED */
+  int32_t ckpt_format; /* the checkpoint's elements: LQ_INT8 or LQ_E4M3 */
+  int32_t experts;
+  int64_t m, n, k;     /* rows of x, y and dy; columns of y; columns of x and W */
+  int64_t ld_in;       /* row stride of x (forward) or dy (gradients) */
+  int64_t ld_out;      /* row stride of y, dx, or dw and dw_in */
+} lq_experts_desc;
+
+LQ_API size_t lq_experts_workspace_bytes(const lq_experts_desc* desc);
+/* y, keeping x as a checkpoint unless ckpt_codes and ckpt_scales are NULL. */
+LQ_API int lq_mx4_experts(const lq_experts_desc* desc, const void* x, const void* offsets, const void* w_codes,
+                          const void* w_scales, void* y, void* ckpt_codes, void* ckpt_scales, void* ws, size_t ws_bytes,
+                          void* stream);
+LQ_API int lq_mx4_experts_dgrad(const lq_experts_desc* desc, const void* dy, const void* offsets, const void* w_codes,
+                                const void* w_scales, void* dx, void* ws, size_t ws_bytes, void* stream);
+/* dw_in NULL for zeros. */
+LQ_API int lq_ckpt8_experts_wgrad(const lq_experts_desc* desc, const void* dy, const void* offsets, const void* ckpt_codes,
+                                  const void* ckpt_scales, const void* dw_in, void* dw, void* ws, size_t ws_bytes,
+                                  void* stream);
+
 /* Text for a status code (static storage). */
 LQ_API const char* lq_status_string(int status);
 
