@@ -10,7 +10,10 @@
 //
 // Both passes read and write each matrix once and are bound by memory: a row stays
 // in the registers of T threads, V times eight elements each, from its load to its
-// last store, and the next row's loads are on their way meanwhile.
+// last store, and the next row's loads are on their way meanwhile. 8192 x 4096 bf16:
+// forward with the residual, h, y and the checkpoint 57 us (5.3 TB/s of what it reads and
+// writes), backward 55.5 us (4.8 TB/s; dw's planes are the rest); a copy of 1 GiB reaches
+// 5.2 TB/s.
 #include "lq_linear.h"
 
 namespace lql {
@@ -329,14 +332,25 @@ __global__ __launch_bounds__(Shape<T>::threads) void k_rmsnorm_backward(const No
       if (i < valid[c]) plane[(int64_t)(c * T + lane) * 8 + i] = share[c][i];
 }
 
-// dw = dw_in + the planes' sum: 32 columns a workgroup, 32 groups of planes side by side.
+// dw = dw_in + the planes' sum: 32 columns a workgroup, 32 groups of planes side by
+// side. What a thread reads does not depend on what it has read, so eight planes' loads
+// are on their way at a time.
 __global__ __launch_bounds__(1024) void k_norm_join(int64_t cols, int planes, const float* from, const float* in, float* dw) {
   __shared__ float part[32][33];
   const int c = threadIdx.x & 31, group = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + c, stride = plane_stride(cols);
   float s = 0.0f;
   if (col < cols)
-    for (int p = group; p < planes; p += 32) s += from[p * stride + col];
+    for (int p = group; p < planes; p += 256) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int at = p + 32 * j;
+        v[j] = from[(at < planes ? at : p) * stride + col];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++) s += p + 32 * j < planes ? v[j] : 0.0f;
+    }
   part[group][c] = s;
   __syncthreads();
   if (group != 0 || col >= cols) return;
@@ -345,55 +359,70 @@ __global__ __launch_bounds__(1024) void k_norm_join(int64_t cols, int planes, co
   dw[col] = in ? in[col] + s : s;
 }
 
-// Workgroups of a pass over the rows. Forward: enough to fill the chip several times
-// over; backward no more than run at once, since each leaves a plane of dw.
-inline int64_t forward_groups(int64_t rows, int each) {
-  const int64_t wanted = (rows + each - 1) / each, most = (int64_t)compute_units() * 8;
+// Workgroups of a pass over the rows. Forward: six for a compute unit where a thread has
+// one unit of eight elements of a 16-bit type, else four (16384 x 2048 bf16: 57 us by six,
+// 66 by four, 72 by seven; 8192 x 4096 bf16: 67 and 57; 8192 x 2048 f32: 69 and 66).
+inline int rows_at_once(int64_t cols) { return cols <= 1024 ? Shape<64>::rows : 1; }
+inline int64_t forward_groups(int64_t rows, int64_t cols, bool wide) {
+  const int each = rows_at_once(cols);
+  const int64_t wanted = (rows + each - 1) / each, most = (int64_t)compute_units() * (cols <= 2048 && !wide ? 6 : 4);
   return wanted < most ? wanted : most;
 }
-inline int64_t backward_groups(int64_t rows, int each) {
-  const int64_t wanted = (rows + each - 1) / each, most = (int64_t)compute_units() * 2;
+// Backward: as many as run at once, since each leaves a plane of dw (8192 x 4096 bf16, of 256
+// threads: 67 us by three for a compute unit, which fit, 83 by two, 88 by four; 16384 x 2048:
+// 56 by four, 61 by three); of few rows two rows for each where that leaves one for each
+// compute unit (1000 x 2048: 10.9 us, a row for each 14.5).
+inline int64_t backward_groups(int64_t rows, int64_t cols) {
+  const int each = rows_at_once(cols), fit = cols <= 512 ? 4 : cols <= 1024 ? 3 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
+  const int64_t units = compute_units(), most = units * fit;
+  int64_t wanted = (rows + each - 1) / each;
+  if (wanted > units) wanted = wanted / 2 > units ? wanted / 2 : units;
   return wanted < most ? wanted : most;
 }
-// Threads of a row, which hold two units of eight elements each at most, or four of the widest rows.
-inline int row_threads(int64_t cols) { return cols <= 512 ? 64 : cols <= 4096 ? 256 : 512; }
-
+// Threads of a row, and its units of eight elements for each. A wave alone up to 1024 columns:
+// it waits for no other (16384 x 1024 bf16: forward 27 us, by 256 threads 31; backward 36 and
+// 43). Then as few units as the threads of a workgroup allow in the backward pass, whose
+// units take most registers (8192 x 4096 bf16: 56 us by 512 threads, 67 by 256; 8192 x 8192:
+// 110 by 1024, 149 by 512); forward, more workgroups are worth more (8192 x 8192: 111 us by
+// 512 threads, 130 by 1024) up to 8192 columns (4096 x 16384: 119 us by 1024 threads, 160 by
+// 512; of binary32, and in the backward pass, two units' registers are too many for 1024).
 template <int DT, int F>
 hipError_t forward(const NormArgs& a, hipStream_t s) {
-  const int threads = row_threads(a.cols);
 #define LQ_NORM(T, V)                                                                                                  \
   {                                                                                                                    \
-    hipLaunchKernelGGL((k_rmsnorm<DT, F, T, V>), dim3((unsigned)forward_groups(a.rows, Shape<T>::rows)),               \
+    hipLaunchKernelGGL((k_rmsnorm<DT, F, T, V>), dim3((unsigned)forward_groups(a.rows, a.cols, DT == LQ_F32)),         \
                        dim3(Shape<T>::threads), 0, s, a);                                                              \
     return hipGetLastError();                                                                                          \
   }
-  if (threads == 64) LQ_NORM(64, 1)
-  if (threads == 256 && a.cols <= 2048) LQ_NORM(256, 1)
-  if (threads == 256) LQ_NORM(256, 2)
+  if (a.cols <= 512) LQ_NORM(64, 1)
+  if (a.cols <= 1024) LQ_NORM(64, 2)
+  if (a.cols <= 2048) LQ_NORM(256, 1)
+  if (a.cols <= 4096) LQ_NORM(256, 2)
   if (a.cols <= 8192) LQ_NORM(512, 2)
-  LQ_NORM(512, 4)
+  if constexpr (DT == LQ_F32) LQ_NORM(512, 4)
+  else LQ_NORM(1024, 2)
 #undef LQ_NORM
 }
 template <int DT>
 hipError_t backward(const NormArgs& a, hipStream_t s) {
-  const int threads = row_threads(a.cols);
 #define LQ_NORM(T, V)                                                                                                  \
   {                                                                                                                    \
-    hipLaunchKernelGGL((k_rmsnorm_backward<DT, T, V>), dim3((unsigned)backward_groups(a.rows, Shape<T>::rows)),        \
+    hipLaunchKernelGGL((k_rmsnorm_backward<DT, T, V>), dim3((unsigned)backward_groups(a.rows, a.cols)),                \
                        dim3(Shape<T>::threads), 0, s, a);                                                              \
     return hipGetLastError();                                                                                          \
   }
-  if (threads == 64) LQ_NORM(64, 1)
-  if (threads == 256 && a.cols <= 2048) LQ_NORM(256, 1)
-  if (threads == 256) LQ_NORM(256, 2)
-  if (a.cols <= 8192) LQ_NORM(512, 2)
+  if (a.cols <= 512) LQ_NORM(64, 1)
+  if (a.cols <= 1024) LQ_NORM(64, 2)
+  if (a.cols <= 2048) LQ_NORM(256, 1)
+  if (a.cols <= 4096) LQ_NORM(512, 1)
+  if (a.cols <= 8192) LQ_NORM(1024, 1)
   LQ_NORM(512, 4)
 #undef LQ_NORM
 }
 
 }  // namespace
 
-int64_t norm_planes(int64_t rows, int64_t cols) { return backward_groups(rows, row_threads(cols) == 64 ? 4 : 1); }
+int64_t norm_planes(int64_t rows, int64_t cols) { return backward_groups(rows, cols); }
 
 hipError_t launch_rmsnorm(int dtype, int format, const NormArgs& a, hipStream_t s) {
   if (format == LQ_INT8) {

@@ -536,7 +536,6 @@ class Ckpt8:
         _check("lq_mx4_quantize", self.lib.lq_mx4_quantize(ctypes.byref(d), _ptr(x), None, None, _ptr(self.codes),
                                                            _ptr(self.scales), _stream_of(self._index, stream)))
 
-
     def values(self, out=None, stream=None):
         """What the codes stand for, [rows, cols] in bfloat16 (exact but for E4M3 values of scales below 2^-124). The
         result is a view of the object's own buffer, which its next call overwrites, unless the caller passes its own."""
@@ -553,13 +552,14 @@ class Ckpt8:
         elif self._values is None:
             self._values = _empty_for(stream, self.rows, pitch, dtype=torch.bfloat16, device=self.codes.device)
         y = self._values if out is None else out
+        shown = y if pitch == self.cols else y[:, :self.cols]
         if self.rows == 0 or self.cols == 0:
-            return y[:, :self.cols]
+            return shown
         rc = self.lib.lq_dequantize(ctypes.byref(self._d), self.codes.data_ptr(), self.scales.data_ptr(), None, self.rows,
                                     pitch, y.data_ptr(), _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_dequantize", rc)
-        return y[:, :self.cols]
+        return shown
 
 
 def _layout(*tensors):
@@ -927,14 +927,11 @@ class RmsNormCkpt8:
         return plan
 
     @staticmethod
-    def _refuse(a, ra, b, rb, what, same=True):
-        """An element is read and written by the same lane: in place is as good as apart, but nothing between."""
-        if a is None or b is None:
-            return
-        pa, pb = a.data_ptr(), b.data_ptr()
-        if pa < pb + rb and pb < pa + ra and _share(a, b):
-            if not (same and pa == pb and (a.shape[0] == 1 or a.stride(0) == b.stride(0))):
-                raise ValueError(f"{what} share memory" + (", but are not the same" if same else ""))
+    def _refuse(a, b, what, same=True):
+        """An element is read and written by the same lane: in place is as good as apart, but nothing between. (Asked
+        only where the two's bytes from the first to the last overlap.)"""
+        if _share(a, b) and not (same and a.data_ptr() == b.data_ptr() and (a.shape[0] == 1 or a.stride(0) == b.stride(0))):
+            raise ValueError(f"{what} share memory" + (", but are not the same" if same else ""))
 
     def forward(self, x, weight, residual=None, y=True, out=None, h_out=None, stream=None):
         """(y, h): h is x itself without a residual; y is None if it is not asked for (`y` false), `kept` alone then
@@ -955,14 +952,24 @@ class RmsNormCkpt8:
         if not y and out is not None:
             raise ValueError("out is for y, which is not asked for")
         y = (out if out is not None else self._own("y", stream)) if y else None
-        self._refuse(x, rx, y, ry, "x and y")
+        px, pr, ph, py = x.data_ptr(), None, None, None
+        if y is not None:
+            py = y.data_ptr()
+            if px < py + ry and py < px + rx:
+                self._refuse(x, y, "x and y")
         if residual is not None:
-            self._refuse(residual, rr, y, ry, "the residual and y")
-            self._refuse(x, rx, h, rh, "x and h")
-            self._refuse(residual, rr, h, rh, "the residual and h")
-            self._refuse(h, rh, y, ry, "h and y", same=False)
-        rc = self.lib.lq_rmsnorm(ref, x.data_ptr(), _ptr(residual), weight.data_ptr(), None if residual is None else
-                                 h.data_ptr(), _ptr(y), *self._kept, _stream_of(self._index, stream))
+            pr, ph = residual.data_ptr(), h.data_ptr()
+            if px < ph + rh and ph < px + rx:
+                self._refuse(x, h, "x and h")
+            if pr < ph + rh and ph < pr + rr:
+                self._refuse(residual, h, "the residual and h")
+            if y is not None:
+                if pr < py + ry and py < pr + rr:
+                    self._refuse(residual, y, "the residual and y")
+                if ph < py + ry and py < ph + rh:
+                    self._refuse(h, y, "h and y", same=False)
+        rc = self.lib.lq_rmsnorm(ref, px, pr, weight.data_ptr(), ph, py, *self._kept,
+                                 _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_rmsnorm", rc)
         return y, h
@@ -985,9 +992,15 @@ class RmsNormCkpt8:
         ref, (ry, rd, rh, rx) = plan
         dx = out if out is not None else self._own("dx", stream)
         dw = dw_out if dw_out is not None else self._own("dw", stream, (max(4, self.cols),), self.torch.float32)[:self.cols]
-        self._refuse(dy, ry, dx, rx, "dy and dx")
-        self._refuse(dh, rd, dx, rx, "dh and dx")
-        self._refuse(h, rh, dx, rx, "h and dx")
+        pdy, pd, ph, px = dy.data_ptr(), None, h.data_ptr(), dx.data_ptr()
+        if pdy < px + rx and px < pdy + ry:
+            self._refuse(dy, dx, "dy and dx")
+        if ph < px + rx and px < ph + rh:
+            self._refuse(h, dx, "h and dx")
+        if dh is not None:
+            pd = dh.data_ptr()
+            if pd < px + rx and px < pd + rd:
+                self._refuse(dh, dx, "dh and dx")
         if dw_in is not None:
             far = abs(dw_in.data_ptr() - dw.data_ptr())
             if 0 < far < 4 * self.cols:
@@ -995,9 +1008,9 @@ class RmsNormCkpt8:
         if self._ws is None:
             self._ws = _empty_for(stream, max(16, self.lib.lq_rmsnorm_workspace_bytes(ref)), dtype=self.torch.uint8,
                                   device=self.device)
-        rc = self.lib.lq_rmsnorm_backward(ref, dy.data_ptr(), _ptr(dh), h.data_ptr(), weight.data_ptr(),
-                                          self.rs.data_ptr(), dx.data_ptr(), _ptr(dw_in), dw.data_ptr(),
-                                          self._ws.data_ptr(), self._ws.numel(), _stream_of(self._index, stream))
+        rc = self.lib.lq_rmsnorm_backward(ref, pdy, pd, ph, weight.data_ptr(), self._kept[2], px, _ptr(dw_in),
+                                          dw.data_ptr(), self._ws.data_ptr(), self._ws.numel(),
+                                          _stream_of(self._index, stream))
         if rc != LQ_OK:
             raise LQError("lq_rmsnorm_backward", rc)
         return dx, dw
