@@ -119,7 +119,8 @@ struct GradArgs {
 // rows end inside a unit of 8 elements, of whose last the rest is cut off.
 // BY_EXPERT: the rows of dy (and x8) lie by expert: a tile of dx is one expert's rows
 // times its n rows of W; a tile of dw, one expert's, is contracted over its rows alone.
-template <int KIND, int F, int OUT, int FM, int FN, bool RAGGED, bool BY_EXPERT>
+// RUNS (dw by expert, added to nothing): a workgroup makes many tiles, one after another.
+template <int KIND, int F, int OUT, int FM, int FN, bool RAGGED, bool BY_EXPERT, bool RUNS = false>
 __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
   typedef typename El<OUT>::T T;
   typedef GradLds<KIND, FM, FN> Lds;
@@ -130,7 +131,7 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
 
   // The XCD's share of the tiles is a contiguous run in bands of 4 rows of tiles (as in the 4-bit product). Of dw's by
   // expert, it is such a run of each expert's, whose tiles take as long as that one has rows.
-  uint32_t tm = g.tm, part = 0, expert = 0, t0;
+  uint32_t tm = g.tm, part = 0, expert = 0, t0 = 0;
   int64_t from = 0, until = KIND == kDgrad ? g.m : g.n;   // rows of A that the expert's are (dgrad); dw's rows
   int64_t depth0 = 0, depth = KIND == kDgrad ? g.n : g.m; // the contraction's: first, and how many
   const uint32_t xcd = blockIdx.x % 8;
@@ -146,6 +147,7 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
     tm = table.tiles_to(expert) - before;
     from = table.row_begin(expert);
     until = table.row_end(expert);
+  } else if constexpr (RUNS) {
   } else if constexpr (BY_EXPERT) {
     const uint32_t tiles = g.tm * g.tn, share = (tiles + 7) / 8, mine = blockIdx.x / 8;
     expert = uniform(mine / share);
@@ -160,13 +162,61 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
     part = __builtin_amdgcn_readfirstlane(mine8 / tiles);
     t0 = mine8 - part * tiles;
   }
-  const uint32_t band = t0 / (4 * g.tn), first = band * 4, high = tm - first < 4 ? tm - first : 4, in = t0 - band * 4 * g.tn;
-  const int64_t row0 = from + (int64_t)__builtin_amdgcn_readfirstlane(first + in % high) * BM;
-  const int64_t col0 = (int64_t)__builtin_amdgcn_readfirstlane(in / high) * BN;
+  int64_t row0, col0;
+  auto corner = [&]() __attribute__((always_inline)) {
+    const uint32_t band = t0 / (4 * g.tn), first = band * 4, high = tm - first < 4 ? tm - first : 4, in = t0 - band * 4 * g.tn;
+    row0 = from + (int64_t)__builtin_amdgcn_readfirstlane(first + in % high) * BM;
+    col0 = (int64_t)__builtin_amdgcn_readfirstlane(in / high) * BN;
+  };
+  // RUNS: a workgroup makes every so many-th of its XCD's tiles, one after another without a pause: what comes after a
+  // tile's last step is the next one's first, in the loads, in LDS and in the operands. (A tile has few steps: with a
+  // workgroup for each, 8192 rows over 16 experts of 2048 x 4096 took 236 us, of which 36 went by before the tiles' first
+  // products and 27 with the results' way through LDS; so it takes 186, and 179 with the experts in another order on each
+  // XCD, since then not all write at a time.) The loads are up to two tiles ahead of the products.
+  struct Made { uint32_t expert, row, col, steps; };
+  Made made0 = {}, made1 = {}, made2 = {};   // to come
+  int queued = 0, to_switch = 0;             // of those; steps until the loads go on to the next
+  uint32_t run = blockIdx.x / 8;             // its place among the XCD's tiles
+  auto next = [&]() __attribute__((always_inline)) {   // the tile at that place, or the next that there is
+    const uint32_t tiles = g.tm * g.tn, share = (tiles + 7) / 8;
+    for (; run < share * (uint32_t)g.experts.count; run += gridDim.x / 8) {
+      expert = uniform(run / share);
+      t0 = xcd * share + run - expert * share;
+      if (t0 >= tiles) continue;
+      expert = uniform((expert + xcd * g.experts.count / 8) % g.experts.count);
+      int64_t end;
+      expert_rows(g.experts, g.m, (int)expert, depth0, end);
+      depth = end - depth0;
+      corner();
+      const uint32_t pairs = uniform((uint32_t)((depth + 2 * kStep - 1) / (2 * kStep)));   // (without rows, a pair of zeros)
+      const Made m = {expert, uniform((uint32_t)row0), uniform((uint32_t)col0), pairs ? 2 * pairs : 2};
+      // (element by element: of assignments in branches the compiler makes one to a place in memory)
+      auto append = [&](int at, Made& to) __attribute__((always_inline)) {
+        to.expert = queued == at ? m.expert : to.expert;
+        to.row = queued == at ? m.row : to.row;
+        to.col = queued == at ? m.col : to.col;
+        to.steps = queued == at ? m.steps : to.steps;
+      };
+      append(0, made0);
+      append(1, made1);
+      append(2, made2);
+      queued++;
+      to_switch = (int)m.steps;
+      run += gridDim.x / 8;
+      return true;
+    }
+    to_switch = 0x7FFFFFFF;
+    return false;
+  };
+  if constexpr (RUNS) {
+    if (!next()) return;
+  } else {
+    corner();
+  }
 
   const int64_t rows = until;   // of A
   const int64_t w_rows = BY_EXPERT ? g.experts.count * g.n : g.n, w_first = expert * g.n;   // dgrad: rows of W as it is stored, and the expert's first
-  const int all = (int)((depth + kStep - 1) / kStep), begin = (int)part * g.part;
+  const int all = (int)((depth + kStep - 1) / kStep), begin = RUNS ? 0 : (int)part * g.part;
   const int steps = BY_EXPERT || begin + g.part >= all ? all : begin + g.part;
 
   // ---- A: 16 bytes a load, 2 FM loads a step
@@ -207,7 +257,8 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
   const uint8_t *pa8 = (const uint8_t*)(KIND == kDgrad ? g.dy + row0 * g.lddy + start : g.dy + (depth0 + start) * g.lddy + row0);
   const uint8_t *pc8 = g.b + (depth0 + start) * pitch + col0, *ps8 = g.bs + (depth0 + start) * spitch + col0 / 32;
   // (an expert's rows may begin in the middle of a word: the stretch begins with the word, and the places in it later)
-  const uint32_t shift = BY_EXPERT ? uniform((uint32_t)(uintptr_t)pa8 & 3u) : 0;
+  uint32_t shift = BY_EXPERT ? uniform((uint32_t)(uintptr_t)pa8 & 3u) : 0;
+  const uint32_t ao0 = ao;
   pa8 -= shift;
   ao += shift;
   const int64_t tail = end - start - (to_come - 1) * (int64_t)kStep;   // rows of the last step
@@ -217,7 +268,7 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
   auto size_a = [&](int64_t rows_left) { return (uint32_t)((rows_left - 1) * g.lddy * 2 + row_bytes - row0 * 2 + shift); };   // (below 2^31)
   auto size_c = [&](int64_t rows_left) { return (uint32_t)(rows_left * pitch - col0); };
   auto size_s = [&](int64_t rows_left) { return (uint32_t)(rows_left * spitch - col0 / 32); };
-  const uint32_t last_a = uniform(size_a(tail)), last_c = uniform(size_c(tail)), last_s = uniform(size_s(tail));
+  uint32_t last_a = uniform(size_a(tail)), last_c = uniform(size_c(tail)), last_s = uniform(size_s(tail));
   uint32_t bytes_a = uniform(KIND == kDgrad ? (uint32_t)((left - 1) * g.lddy * 2 + row_bytes - start * 2 + shift) : size_a(kStep));
   uint32_t bytes_c = uniform(size_c(kStep)), bytes_s = uniform(size_s(kStep));
   const uint32_t move_a = uniform((uint32_t)(KIND == kDgrad ? kStep * 2 : kStep * 2 * g.lddy)), move_c = uniform((uint32_t)(kStep * pitch)), move_s = uniform((uint32_t)(kStep * spitch));
@@ -231,7 +282,25 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
       ss[i] = stretch(g.bs + (panel * mx4_scale_rows(w_rows) + w_first) * 4, real ? end * 4 : 0);
     }
   }
-  auto point = [&] {
+  auto point = [&]() __attribute__((always_inline)) {
+    if constexpr (RUNS) {
+      if (to_switch == 0) {
+        to_come = 0;
+        if (next()) {
+          to_come = uniform((uint32_t)((depth + kStep - 1) / kStep));
+          pa8 = (const uint8_t*)(g.dy + depth0 * g.lddy + row0);
+          shift = uniform((uint32_t)(uintptr_t)pa8 & 3u);
+          pa8 -= shift;
+          ao = ao0 + shift;
+          pc8 = g.b + depth0 * pitch + col0;
+          ps8 = g.bs + depth0 * spitch + col0 / 32;
+          const int64_t left = depth - (to_come - 1) * (int64_t)kStep;
+          last_a = uniform(size_a(left)), last_c = uniform(size_c(left)), last_s = uniform(size_s(left));
+          bytes_a = uniform(size_a(kStep)), bytes_c = uniform(size_c(kStep)), bytes_s = uniform(size_s(kStep));
+        }
+      }
+      to_switch--;
+    }
     if (KIND == kWgrad) {
       if (to_come == 1) bytes_a = last_a, bytes_c = last_c, bytes_s = last_s;
       if (to_come <= 0) bytes_a = bytes_c = bytes_s = 0;
@@ -373,7 +442,8 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
     for (int i = 0; i < FM; i++)
 #pragma unroll
       for (int j = 0; j < FN; j++) {
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, o.b[j]), __builtin_bit_cast(v8bf, o.a[i]), acc[i][j], 0, 0, 0);
+        const v4i left = RUNS ? o.a[i] : o.b[j], right = RUNS ? o.b[j] : o.a[i];   // (RUNS: a lane has one column, see there)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, left), __builtin_bit_cast(v8bf, right), acc[i][j], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
         between(i * FN + j);
         __builtin_amdgcn_sched_barrier(0);
@@ -451,6 +521,55 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
       if (done == per / 2) point();
     });
   };
+  if constexpr (RUNS) {
+    // A lane holds column r of a 32 x 32 block, rows 8q + 4h .. + 3: a store is 128 bytes of two rows, and no LDS, whose
+    // next step is there already, is in between.
+    const uint32_t line = uniform((uint32_t)g.ldo * 4);
+    const uint32_t mine = 4 * h * line + (wn * 32 * FN + r) * 4;
+    for (;;) {
+      uint32_t t = 0;
+      do {
+        step(std::integral_constant<int, 0>(), (int)t);
+        step(std::integral_constant<int, 1>(), (int)t + 1);
+        t += 2;
+      } while (t < made0.steps);
+      // rows past the last are cut off, columns past the last sent out of the stretch
+      const int64_t at = (made0.expert * g.n + made0.row) * g.ldo + made0.col;
+      const int64_t high = rows - made0.row < BM ? rows - made0.row : BM, bytes = (high * g.ldo - made0.col) * 4;
+      const auto to = stretch((const float*)g.out + at, bytes);
+      uint32_t places[FN];
+#pragma unroll
+      for (int j = 0; j < FN; j++) places[j] = made0.col + wn * 32 * FN + j * 32 + r < g.k ? mine + j * 128 : 0x80000000u;
+      // (the sums are pinned to accumulation registers)
+#pragma unroll
+      for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++) asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+      for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const int there = (int)((wm * 32 * FM + i * 32 + 8 * q) * line);
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][4 * q + e]), to, (int)places[j], there + e * (int)line, 2);
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+      for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++) {
+          acc[i][j] = (v16f)(0.0f);
+          asm volatile("" : "+a"(acc[i][j]));
+        }
+      if (--queued == 0) return;
+      made0 = made1;
+      made1 = made2;
+    }
+  }
   // (of an odd number of steps, the last is followed by one of zeros)
   for (int t = begin; t < steps; t += 2) {
     step(std::integral_constant<int, 0>(), t);
@@ -535,6 +654,10 @@ __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad(const GradA
 template <int KIND, int F, int OUT, int FM, int FN, bool RAGGED>
 __global__ __launch_bounds__(256, FM * FN >= 16 ? 1 : 2) void k_grad_experts(const GradArgs g) {
   grad_tile_of<KIND, F, OUT, FM, FN, RAGGED, true>(g);
+}
+template <int F>
+__global__ __launch_bounds__(256, 1) void k_wgrad_experts(const GradArgs g) {
+  grad_tile_of<kWgrad, F, LQ_F32, 4, 4, false, true, true>(g);
 }
 
 // dy with rows of a multiple of 64 elements, zeros past n.
@@ -647,8 +770,23 @@ hipError_t grad_experts_tiled(GradArgs& g, hipStream_t s) {
   else hipLaunchKernelGGL((k_grad_experts<KIND, F, OUT, FM, FN, false>), grid, dim3(256), 0, s, g);
   return hipGetLastError();
 }
-template <int KIND, int F, int OUT>
-hipError_t grad_experts(GradArgs g, int tile, void* ws, hipStream_t s) {
+// dw: in 256 x 256 tiles, as many workgroups as run at once, which make one after another. Where it is added to dw_in, whose
+// elements have no registers there, in 128 x 128 tiles (8192 rows over 16 experts of 2048 x 4096 341 us, in 256 x 256 tiles
+// of a workgroup each 443), and so it is where a tile's rows pass 2^31 bytes.
+template <int F>
+hipError_t wgrad_experts(GradArgs g, void* ws, hipStream_t s) {
+  uint8_t* rest;
+  if (place_dy(g, ws, rest, s) != hipSuccess) return hipErrorLaunchFailure;
+  if (g.in || g.ldo >= (int64_t)1 << 21) return grad_experts_tiled<kWgrad, F, LQ_F32, 2, 2>(g, s);
+  g.tm = (uint32_t)((g.n + 255) / 256);
+  g.tn = (uint32_t)((g.k + 255) / 256);
+  const int64_t eighth = ((int64_t)g.tm * g.tn + 7) / 8 * g.experts.count, at_once = compute_units() / 8;
+  hipLaunchKernelGGL((k_wgrad_experts<F>), dim3((unsigned)((eighth < at_once ? eighth : at_once) * 8)), dim3(256), 0, s, g);
+  return hipGetLastError();
+}
+template <int OUT>
+hipError_t dgrad_experts(GradArgs g, int tile, void* ws, hipStream_t s) {
+  constexpr int KIND = kDgrad, F = LQ_E2M1;
   uint8_t* rest;
   if (place_dy(g, ws, rest, s) != hipSuccess) return hipErrorLaunchFailure;
   return tile == 4 ? grad_experts_tiled<KIND, F, OUT, 4, 4>(g, s) : grad_experts_tiled<KIND, F, OUT, 2, 2>(g, s);
@@ -662,9 +800,9 @@ hipError_t launch_mx4_experts_dgrad(const void* dy, const Experts& e, int64_t m,
   const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)w_codes, (const uint8_t*)w_scales, nullptr, dx, lddx, 0, 0, 1, 0, e};
   const int tile = expert_dgrad_tile(m, n, k, e.count);
   switch (out_dtype) {
-    case LQ_F32: return grad_experts<kDgrad, LQ_E2M1, LQ_F32>(g, tile, ws, s);
-    case LQ_BF16: return grad_experts<kDgrad, LQ_E2M1, LQ_BF16>(g, tile, ws, s);
-    default: return grad_experts<kDgrad, LQ_E2M1, LQ_F16>(g, tile, ws, s);
+    case LQ_F32: return dgrad_experts<LQ_F32>(g, tile, ws, s);
+    case LQ_BF16: return dgrad_experts<LQ_BF16>(g, tile, ws, s);
+    default: return dgrad_experts<LQ_F16>(g, tile, ws, s);
   }
 }
 
@@ -672,9 +810,8 @@ hipError_t launch_ckpt8_experts_wgrad(int format, const void* dy, const Experts&
                                       const void* x_codes, const void* x_scales, int64_t k, const float* dw_in, float* dw,
                                       int64_t lddw, void* ws, hipStream_t s) {
   const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)x_codes, (const uint8_t*)x_scales, dw_in, dw, lddw, 0, 0, 1, 0, e};
-  const int tile = expert_wgrad_tile(m, n, k, e.count, dw_in != nullptr);
-  if (format == LQ_INT8) return grad_experts<kWgrad, LQ_INT8, LQ_F32>(g, tile, ws, s);
-  return grad_experts<kWgrad, LQ_E4M3, LQ_F32>(g, tile, ws, s);
+  if (format == LQ_INT8) return wgrad_experts<LQ_INT8>(g, ws, s);
+  return wgrad_experts<LQ_E4M3>(g, ws, s);
 }
 
 }  // namespace lql

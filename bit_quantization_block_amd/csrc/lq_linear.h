@@ -323,9 +323,10 @@ struct ExpertTable {
     return n;
   }
 };
-// One expert's rows straight from memory.
+// One expert's rows straight from memory. (By scalar loads: a vector load's wait is one for all that is on its way.)
 __device__ __forceinline__ void expert_rows(const Experts& x, int64_t m, int e, int64_t& begin, int64_t& end) {
-  const int32_t b = x.offsets[e], n = x.offsets[e + 1];
+  const auto offsets = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)x.offsets;
+  const int32_t b = offsets[e], n = offsets[e + 1];
   begin = b < 0 ? 0 : b > m ? m : b;
   end = n < begin ? begin : n > m ? m : n;
 }
@@ -357,7 +358,6 @@ inline size_t planes_bytes(const Split& c, int64_t rows, int64_t cols) {
 
 // The tile of a product over rows that lie by expert: rows / experts of them on the average (steps of 128, of 64, of 64).
 int expert_tile(int64_t m, int64_t n, int64_t k, int experts), expert_dgrad_tile(int64_t m, int64_t n, int64_t k, int experts);
-int expert_wgrad_tile(int64_t m, int64_t n, int64_t k, int experts, bool adds);
 
 // ------------------------------------------------------------ launchers
 // Instead of launching, the kernel's name and its template arguments for a plan being recorded (lq_plan.h).

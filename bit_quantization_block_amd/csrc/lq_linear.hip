@@ -127,10 +127,6 @@ int expert_tile(int64_t m, int64_t n, int64_t k, int experts) {
 int expert_dgrad_tile(int64_t m, int64_t n, int64_t k, int experts) {
   return cheapest(kDgradTiles, m, k, (n + 63) / 64, 0.0, experts).tile;
 }
-// (the weights' rows are as many for each; they are contracted over an expert's share of the rows)
-int expert_wgrad_tile(int64_t m, int64_t n, int64_t k, int experts, bool adds) {
-  return cheapest(kWgradTiles, n * experts, k, (m + 63) / 64 / experts + 1, adds ? (double)n * k * experts * 4 : 0.0, 1).tile;
-}
 
 }  // namespace lql
 

@@ -123,6 +123,33 @@ def test_wgrad(m, experts, n, k, pad, before, behind, fmt):
         close(added[e], want + s, acc, "f32", f"expert {e} of {experts}, added")
 
 
+@pytest.mark.parametrize("m,experts,n,k,skew", [(2300, 40, 300, 600, 0), (700, 300, 40, 500, 0), (900, 96, 130, 257, 1),
+                                                (64, 512, 20, 30, 1), (5000, 33, 260, 513, 0), (0, 64, 40, 72, 0)])
+def test_wgrad_of_many_tiles(m, experts, n, k, skew):
+    """More tiles than run at a time, of one step and of many, and of experts without rows between them."""
+    say(f"[gpu] experts wgrad, tiles after one another, {m} rows, {experts} x {n} x {k}")
+    off = split(m, experts, m, 0, 0) if m else np.zeros(experts + 1, dtype=np.int64)
+    if skew:   # every second expert has the next one's rows too
+        off[1:-1:2] = off[2::2][:len(off[1:-1:2])]
+    dy, dv = matrix(m, n, "bf16", 1, 5)
+    x, xv = matrix(m, k, "bf16", 0, 6)
+    q = R.quantise(xv.astype(np.float32), "int8")[2] if m else xv
+    kept = lq.Ckpt8(m, k)
+    kept.save(x)
+    layer = lq.Mx4Experts(torch.zeros(experts, n, k, dtype=torch.bfloat16, device="cuda"), rows=m)
+    around = torch.full((experts * n * k + 64,), 7.0, device="cuda")
+    dw = around[32:-32].view(experts, n, k)
+    for _ in range(2):
+        layer.wgrad(dy, kept, on_gpu(off), out=dw)
+    for e in range(experts):
+        b, c = off[e], off[e + 1]
+        if b == c:
+            assert (dw[e] == 0).all()
+        else:
+            close(dw[e], dv[b:c].T @ q[b:c], accumulation(dv[b:c].T, q[b:c]), "f32", f"expert {e} of {experts}")
+    assert (around[:32] == 7).all() and (around[-32:] == 7).all()
+
+
 def test_spoiled_rows_stay_their_experts():
     """An infinity in one row: its row of y is NaN, and its expert's dw; nothing else changes. Rows of no expert are not read
     into any result."""
