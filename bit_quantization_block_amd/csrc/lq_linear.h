@@ -263,6 +263,17 @@ struct Experts {
   const int32_t* offsets;
   int count;
 };
+// Inclusive scan over a wave (0 changes nothing in `op`): within rows of 16, then the rows' last lanes on to the next rows.
+template <class OP>
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, OP op) {
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));   // row_shr 1
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // row_bcast 15, to rows 1 and 3
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));   // row_bcast 31, to rows 2 and 3
+  return v;
+}
 // A wave's table of the experts' ranges, one expert in each lane of each register: the
 // tiles' LDS leaves no room for one (512 experts' 4 KB keep a second workgroup of 128 x
 // 128 off a compute unit).
@@ -284,18 +295,9 @@ struct ExpertTable {
       if (c * 64 >= x.count) continue;
       uint32_t e = offset(c * 64 + lane + 1);   // (of lanes past the last expert, the last end again)
       e = e > top ? e : top;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const uint32_t o = __shfl_up(e, d);
-        if (lane >= d) e = e > o ? e : o;
-      }
-      const uint32_t before = __shfl_up(e, 1);
-      uint32_t t = (e - (lane ? before : top) + side - 1) / side;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const uint32_t o = __shfl_up(t, d);
-        if (lane >= d) t += o;
-      }
+      e = wave_scan(e, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+      const uint32_t before = (uint32_t)__builtin_amdgcn_update_dpp((int)top, (int)e, 0x138, 0xF, 0xF, false);   // wave_shr 1
+      const uint32_t t = wave_scan((e - before + side - 1) / side, [](uint32_t a, uint32_t b) { return a + b; });
       end[c] = e;
       tiles[c] = sum + t;
       top = __builtin_amdgcn_readlane(e, 63);

@@ -616,21 +616,170 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64
                                                             int64_t ldy) {
   mx4_few<SRC, OUT, R, CT>(x, ldx, xs, m, 0, w, ws, n, 0, m, n, k, y, ldy);
 }
-// By expert, one a row of the grid: 16 rows at a time, or as many as fit in LDS.
-template <int SRC, int OUT, int R>
-__global__ __launch_bounds__(64 * kFewWaves) void k_mx4_experts_few(const void* x, int64_t ldx, const uint8_t* xs,
-                                                                    const uint8_t* w, const uint8_t* ws, int64_t m, int64_t n,
-                                                                    int64_t k, void* y, int64_t ldy, Experts experts) {
-  typedef typename El<OUT>::T T;
+// By expert, of an MX4 operand: an expert a row of the grid, 16 rows at a time.
+template <int OUT, int R>
+__global__ __launch_bounds__(64 * kFewWaves) void k_mx4_experts_few(const void* x, const uint8_t* xs, const uint8_t* w,
+                                                                    const uint8_t* ws, int64_t m, int64_t n, int64_t k, void* y,
+                                                                    int64_t ldy, Experts experts) {
   int64_t begin, end;
   expert_rows(experts, m, blockIdx.y, begin, end);
-  const int64_t blocks = mx4_groups(k) * 4, fit = SRC == kOperand ? 16 : kFewBlocks / blocks, most = fit < 16 ? fit : 16;
-  for (int64_t row = begin; row < end; row += most) {
+  for (int64_t row = begin; row < end; row += 16) {
     if (row > begin) __syncthreads();   // (the last rows' sums have been read)
-    const int64_t rows = end - row < most ? end - row : most;
-    const void* from = x;
-    if constexpr (SRC != kOperand) from = (const typename El<SRC>::T*)x + row * ldx;
-    mx4_few<SRC, OUT, R, 1>(from, ldx, xs, m, row, w, ws, experts.count * n, blockIdx.y * n, rows, n, k, (T*)y + row * ldy, ldy);
+    const int64_t rows = end - row < 16 ? end - row : 16;
+    mx4_few<kOperand, OUT, R, 1>(x, 0, xs, m, row, w, ws, experts.count * n, blockIdx.y * n, rows, n, k,
+                                 (typename El<OUT>::T*)y + row * ldy, ldy);
+  }
+}
+
+// By expert, straight from x. The experts' rows in chunks of 16, or as many as fit in LDS;
+// a chunk times a strip of W's rows is a unit, and every workgroup of as many as run at
+// once takes a run of the units, so that W comes without a pause: its next groups are
+// asked for before the last ones' products, across units, and the chunk's x is
+// quantised into LDS once. 32 rows over 64 experts of 2048 x 4096 25 us, 4.6 TB/s of W,
+// 256 rows over 64 of 2048 x 2048 29 us (a workgroup for each unit, which waits out W's
+// way and quantises x for each: 30 and 56 us; where the units are few, 1 row of 2048 x
+// 4096, that took 4.8 us and this takes 5.9: finding the runs comes first).
+// Of a workgroup's eight waves, `splits` share 16 rows of W, a run of the contraction's
+// groups each: as many as leave a wave four groups, what it asks for at a time.
+template <int SRC, int OUT>
+__global__ __launch_bounds__(64 * kFewWaves, 4) void k_mx4_experts_rows(const void* x, int64_t ldx, const uint8_t* w,
+                                                                        const uint8_t* ws, int64_t m, int64_t n, int64_t k,
+                                                                        void* y, int64_t ldy, Experts experts, int splits) {
+  typedef typename El<OUT>::T T;
+  typedef typename El<SRC>::T E;
+  __shared__ v4f sums[2][kFewWaves][64];
+  __shared__ v4i xcodes[kFewBlocks];
+  __shared__ uint8_t xscales[kFewBlocks];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int groups = (int)mx4_groups(k), blocks = groups * 4, fit = (int)kFewBlocks / blocks, most = fit < 16 ? fit : 16;
+  ExpertTable table;
+  table.scan(experts, m, most);
+  const int tall = kFewWaves / splits, part = wave % splits, strip = wave / splits;   // strips of 16 rows of W
+  const uint32_t across = (uint32_t)((n + 16 * tall - 1) / (16 * tall));               // units of a chunk
+  const uint64_t total = (uint64_t)table.tiles_to(experts.count - 1) * across;
+  const int shift = 31 - __builtin_clz(gridDim.x);   // (a power of two)
+  const uint64_t first = total * blockIdx.x >> shift, last = total * (blockIdx.x + 1) >> shift;
+  if (first >= last) return;
+  const int each = (groups + splits - 1) / splits, from = part * each, to = from + each < groups ? from + each : groups;
+  constexpr int U = 4;   // groups asked for at a time
+  const int batches = (each + U - 1) / U;
+  const int64_t wn = experts.count * n, wstep = mx4_scale_rows(wn) * 4;
+
+  struct Reads { v4i c[U]; uint8_t e[U]; };
+  // Batch `batch` of the rows of W from w0 on, `high` of them left; of none, zeros that are not read: a load that some
+  // paths lack makes the compiler wait for all that is on its way.
+  auto load = [&](Reads& b, int64_t w0, int64_t high, int batch) __attribute__((always_inline)) {
+    const int tops = (int)(high < 0 ? 0 : high < 16 ? high : 16);
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int g = from + batch * U + u;
+      const int real = g < to ? tops : 0;
+      const int64_t at = real ? (int64_t)g : 0;
+      const auto codes = __builtin_amdgcn_make_buffer_rsrc((void*)(w + (at * wn + w0) * 64), 0, real * 64, 0x00020000);
+      const auto scales = __builtin_amdgcn_make_buffer_rsrc((void*)(ws + at * wstep + w0 * 4), 0, real * 4, 0x00020000);
+      b.c[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(codes, r * 64 + q * 16, 0, 0));
+      b.e[u] = __builtin_amdgcn_raw_buffer_load_b8(scales, r * 4 + q, 0, 0);
+    }
+  };
+
+  const uint32_t chunk = uniform((uint32_t)(first / across));
+  uint32_t strip0 = (uint32_t)(first - (uint64_t)chunk * across);
+  uint64_t left = last - first;   // units
+  int turn = 0;
+  uint32_t expert = uniform(table.at(chunk, experts.count));
+  uint32_t row0 = table.row_begin(expert) + (chunk - table.tiles_before(expert)) * most, end_of_rows = table.row_end(expert);
+  Reads a, b;
+  while (left > 0) {   // chunks
+    const int rows = end_of_rows - row0 < (uint32_t)most ? (int)(end_of_rows - row0) : most;
+    uint32_t units = across - strip0;
+    if (units > left) units = (uint32_t)left;
+    const int64_t w0 = expert * n + strip * 16;
+    auto high = [&](uint32_t at) { return n - ((int64_t)at * tall + strip) * 16; };   // rows of W from the strip's first on
+    // a thread's first two blocks of x, then W, whose way here hides the rest
+    const int all = rows * blocks;
+    auto block = [&](int i) {
+      const int row = i / blocks, col = (i - row * blocks) * 32;
+      return load_block<SRC>((const E*)x + (int64_t)(row0 + row) * ldx + col, k - col < 32 ? (int)(k - col) : 32);
+    };
+    auto keep = [&](int i, const Block<SRC>& v) {
+      uint32_t e;
+      xcodes[i] = quantise_block<SRC>(v, e);
+      xscales[i] = (uint8_t)e;
+    };
+    constexpr int kThreads = 64 * kFewWaves;
+    {
+      int i = threadIdx.x;
+      Block<SRC> mine;
+      if (i < all) mine = block(i);
+      asm volatile("" ::: "memory");
+      load(a, w0 + (int64_t)strip0 * tall * 16, high(strip0), 0);
+      if (i < all) keep(i, mine);
+      for (i += kThreads; i < all; i += kThreads) keep(i, block(i));
+    }
+    __syncthreads();
+
+    uint32_t at = strip0, end = strip0 + units;   // strips of W
+    int batch = 0;
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    // The products of `now`'s groups, with what comes next on its way to `then`.
+    auto go = [&](const Reads& now, Reads& then) __attribute__((always_inline)) {
+      const bool ends = batch + 1 == batches;
+      const uint32_t next = ends ? at + 1 : at;
+      load(then, w0 + (int64_t)next * tall * 16, next < end ? high(next) : 0, ends ? 0 : batch + 1);
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const int g = from + batch * U + u;
+        v4i xc = {0, 0, 0, 0};
+        uint32_t xe = 0;
+        if (r < rows && g < to) {
+          const int place = (r * groups + g) * 4 + q;
+          xc = xcodes[place];
+          xe = xscales[place];
+        }
+        const v8i A = {now.c[u][0], now.c[u][1], now.c[u][2], now.c[u][3], 0, 0, 0, 0};
+        const v8i B = {xc[0], xc[1], xc[2], xc[3], 0, 0, 0, 0};
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc, 4, 4, 0, (int)now.e[u], 0, (int)xe);
+      }
+      batch++;
+      if (!ends) return;
+      sums[turn][wave][lane] = acc;
+      // (LDS only: W's next groups stay on their way)
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      // One wave of a strip's adds them up: a lane's four sums are columns 4q .. 4q + 3 of one row of y. (Who is a unit
+      // ahead writes the other sums, and with that unit's barrier everyone has read these.)
+      if (part == (int)(at % (uint32_t)splits)) {
+        v4f s = sums[turn][strip * splits][lane];
+        for (int v = 1; v < splits; v++) s += sums[turn][strip * splits + v][lane];
+        const int64_t col = ((int64_t)at * tall + strip) * 16 + 4 * q;
+        if (r < rows) {
+          T* o = (T*)y + (int64_t)(row0 + r) * ldy + col;
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            if (col + e < n) o[e] = narrow<OUT>(s[e]);
+        }
+      }
+      turn ^= 1;
+      batch = 0;
+      at++;
+      acc = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    while (at < end) {
+      go(a, b);
+      if (at < end) go(b, a);
+    }
+    left -= units;
+    strip0 = 0;
+    // the expert's next rows, or the next one's that has any (as in the table, but without its registers)
+    row0 += most;
+    while (left > 0 && row0 >= end_of_rows) {
+      expert++;
+      row0 = end_of_rows;
+      const int32_t raw = ((const __attribute__((address_space(4))) int32_t*)(uintptr_t)experts.offsets)[expert + 1];
+      const uint32_t end = raw < 0 ? 0u : raw > m ? (uint32_t)m : (uint32_t)raw;
+      end_of_rows = end > end_of_rows ? end : end_of_rows;
+    }
+    // (x is written anew after the last unit's barrier, behind which no one reads it)
   }
 }
 
@@ -818,27 +967,40 @@ bool experts_in_place(int64_t m, int64_t k, int experts) {
 
 namespace {
 
-template <int SRC, int OUT>
-hipError_t experts_few_out(const void* x, int64_t ldx, const void* xs, const Experts& e, const void* w, const void* ws,
-                           int64_t m, int64_t n, int64_t k, void* y, int64_t ldy, hipStream_t s) {
+template <int OUT>
+hipError_t experts_few_out(const void* x, const void* xs, const Experts& e, const void* w, const void* ws, int64_t m, int64_t n,
+                           int64_t k, void* y, int64_t ldy, hipStream_t s) {
   // 32 rows of W a workgroup where the experts with rows leave one of those for each compute unit, as above
   const int r = n * (m < e.count ? m : e.count) >= 32 * (int64_t)compute_units() ? 2 : 1;
   const dim3 grid((unsigned)((n + 16 * r - 1) / (16 * r)), (unsigned)e.count);
   if (r == 2)
-    hipLaunchKernelGGL((k_mx4_experts_few<SRC, OUT, 2>), grid, dim3(64 * kFewWaves), 0, s, x, ldx, (const uint8_t*)xs,
-                       (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy, e);
+    hipLaunchKernelGGL((k_mx4_experts_few<OUT, 2>), grid, dim3(64 * kFewWaves), 0, s, x, (const uint8_t*)xs, (const uint8_t*)w,
+                       (const uint8_t*)ws, m, n, k, y, ldy, e);
   else
-    hipLaunchKernelGGL((k_mx4_experts_few<SRC, OUT, 1>), grid, dim3(64 * kFewWaves), 0, s, x, ldx, (const uint8_t*)xs,
-                       (const uint8_t*)w, (const uint8_t*)ws, m, n, k, y, ldy, e);
+    hipLaunchKernelGGL((k_mx4_experts_few<OUT, 1>), grid, dim3(64 * kFewWaves), 0, s, x, (const uint8_t*)xs, (const uint8_t*)w,
+                       (const uint8_t*)ws, m, n, k, y, ldy, e);
+  return hipGetLastError();
+}
+template <int SRC, int OUT>
+hipError_t experts_rows_out(const void* x, int64_t ldx, const Experts& e, const void* w, const void* ws, int64_t m, int64_t n,
+                            int64_t k, void* y, int64_t ldy, hipStream_t s) {
+  int splits = 1;
+  while (splits < kFewWaves && splits * 8 <= mx4_groups(k)) splits *= 2;
+  // two workgroups for a compute unit, or one for each unit if there are fewer, rounded down to a power of two
+  const int64_t tall = kFewWaves / splits, units = m * ((n + 16 * tall - 1) / (16 * tall));
+  unsigned grid = 1;
+  while (grid * 2 <= units && grid * 2 <= 2 * (unsigned)compute_units()) grid *= 2;
+  hipLaunchKernelGGL((k_mx4_experts_rows<SRC, OUT>), dim3(grid), dim3(64 * kFewWaves), 0, s, x, ldx, (const uint8_t*)w,
+                     (const uint8_t*)ws, m, n, k, y, ldy, e, splits);
   return hipGetLastError();
 }
 template <int SRC>
-hipError_t experts_few_src(const void* x, int64_t ldx, const void* xs, const Experts& e, const void* w, const void* ws,
-                           int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s) {
+hipError_t experts_rows(const void* x, int64_t ldx, const Experts& e, const void* w, const void* ws, int64_t m, int64_t n,
+                        int64_t k, int out_dtype, void* y, int64_t ldy, hipStream_t s) {
   switch (out_dtype) {
-    case LQ_F32: return experts_few_out<SRC, LQ_F32>(x, ldx, xs, e, w, ws, m, n, k, y, ldy, s);
-    case LQ_BF16: return experts_few_out<SRC, LQ_BF16>(x, ldx, xs, e, w, ws, m, n, k, y, ldy, s);
-    default: return experts_few_out<SRC, LQ_F16>(x, ldx, xs, e, w, ws, m, n, k, y, ldy, s);
+    case LQ_F32: return experts_rows_out<SRC, LQ_F32>(x, ldx, e, w, ws, m, n, k, y, ldy, s);
+    case LQ_BF16: return experts_rows_out<SRC, LQ_BF16>(x, ldx, e, w, ws, m, n, k, y, ldy, s);
+    default: return experts_rows_out<SRC, LQ_F16>(x, ldx, e, w, ws, m, n, k, y, ldy, s);
   }
 }
 template <int OUT, int FM, int FN>
@@ -867,17 +1029,20 @@ hipError_t launch_mx4_experts_few(int in_dtype, const void* x, int64_t ldx, cons
                                   const void* w_scales, int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy,
                                   hipStream_t s) {
   switch (in_dtype) {
-    case LQ_F32: return experts_few_src<LQ_F32>(x, ldx, nullptr, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
-    case LQ_BF16: return experts_few_src<LQ_BF16>(x, ldx, nullptr, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
-    default: return experts_few_src<LQ_F16>(x, ldx, nullptr, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
+    case LQ_F32: return experts_rows<LQ_F32>(x, ldx, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
+    case LQ_BF16: return experts_rows<LQ_BF16>(x, ldx, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
+    default: return experts_rows<LQ_F16>(x, ldx, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
   }
 }
 
 hipError_t launch_mx4_experts(const void* a_codes, const void* a_scales, const Experts& e, const void* w_codes,
                               const void* w_scales, int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy,
                               hipStream_t s) {
-  if (experts_few(m, e.count))
-    return experts_few_src<kOperand>(a_codes, 0, a_scales, e, w_codes, w_scales, m, n, k, out_dtype, y, ldy, s);
+  if (experts_few(m, e.count)) switch (out_dtype) {
+    case LQ_F32: return experts_few_out<LQ_F32>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
+    case LQ_BF16: return experts_few_out<LQ_BF16>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
+    default: return experts_few_out<LQ_F16>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
+  }
   switch (out_dtype) {
     case LQ_F32: return experts_out<LQ_F32>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
     case LQ_BF16: return experts_out<LQ_BF16>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
