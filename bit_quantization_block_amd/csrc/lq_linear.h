@@ -290,9 +290,10 @@ struct ExpertTable {
     };
     uint32_t top = first = __builtin_amdgcn_readfirstlane(offset(0)), sum = 0;
 #pragma unroll
+    for (int c = 0; c < kMostExperts / 64; c++) end[c] = tiles[c] = 0;
+#pragma unroll
     for (int c = 0; c < kMostExperts / 64; c++) {
-      end[c] = tiles[c] = 0;
-      if (c * 64 >= x.count) continue;
+      if (c * 64 >= x.count) break;   // (one branch for up to 64 experts, here and below)
       uint32_t e = offset(c * 64 + lane + 1);   // (of lanes past the last expert, the last end again)
       e = e > top ? e : top;
       e = wave_scan(e, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
@@ -306,10 +307,12 @@ struct ExpertTable {
   }
   // Of expert i (uniform).
   static __device__ __forceinline__ uint32_t pick(const uint32_t (&v)[kMostExperts / 64], uint32_t i) {
-    uint32_t r = 0;
+    uint32_t r = __builtin_amdgcn_readlane(v[0], i % 64);
+    if (i >= 64) {
 #pragma unroll
-    for (int c = 0; c < kMostExperts / 64; c++)
-      if (i / 64 == c) r = __builtin_amdgcn_readlane(v[c], i % 64);
+      for (int c = 1; c < kMostExperts / 64; c++)
+        if (i / 64 == c) r = __builtin_amdgcn_readlane(v[c], i % 64);
+    }
     return r;
   }
   __device__ __forceinline__ uint32_t row_end(uint32_t i) const { return pick(end, i); }
@@ -320,8 +323,10 @@ struct ExpertTable {
   __device__ __forceinline__ uint32_t at(uint32_t t, int count) const {
     uint32_t n = 0;
 #pragma unroll
-    for (int c = 0; c < kMostExperts / 64; c++)
-      if (c * 64 < count) n += (uint32_t)__builtin_popcountll(__ballot(tiles[c] <= t && c * 64 + (int)(threadIdx.x & 63) < count));
+    for (int c = 0; c < kMostExperts / 64; c++) {
+      if (c * 64 >= count) break;
+      n += (uint32_t)__builtin_popcountll(__ballot(tiles[c] <= t && c * 64 + (int)(threadIdx.x & 63) < count));
+    }
     return n;
   }
 };

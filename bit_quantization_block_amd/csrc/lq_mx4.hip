@@ -635,10 +635,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_experts_few(const void* 
 // a chunk times a strip of W's rows is a unit, and every workgroup of as many as run at
 // once takes a run of the units, so that W comes without a pause: its next groups are
 // asked for before the last ones' products, across units, and the chunk's x is
-// quantised into LDS once. 32 rows over 64 experts of 2048 x 4096 25 us, 4.6 TB/s of W,
-// 256 rows over 64 of 2048 x 2048 29 us (a workgroup for each unit, which waits out W's
+// quantised into LDS once. 32 rows over 64 experts of 2048 x 4096 23.5 us, 4.8 TB/s of W,
+// 256 rows over 64 of 2048 x 2048 28 us (a workgroup for each unit, which waits out W's
 // way and quantises x for each: 30 and 56 us; where the units are few, 1 row of 2048 x
-// 4096, that took 4.8 us and this takes 5.9: finding the runs comes first).
+// 4096, that took 4.8 us and this takes 5.6: finding the runs comes first).
 // Of a workgroup's eight waves, `splits` share 16 rows of W, a run of the contraction's
 // groups each: as many as leave a wave four groups, what it asks for at a time.
 template <int SRC, int OUT>
@@ -667,23 +667,24 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void k_mx4_experts_rows(const vo
   const int64_t wn = experts.count * n, wstep = mx4_scale_rows(wn) * 4;
 
   struct Reads { v4i c[U]; uint8_t e[U]; };
-  // Batch `batch` of the rows of W from w0 on, `high` of them left; of none, zeros that are not read: a load that some
-  // paths lack makes the compiler wait for all that is on its way.
-  auto load = [&](Reads& b, int64_t w0, int64_t high, int batch) __attribute__((always_inline)) {
-    const int tops = (int)(high < 0 ? 0 : high < 16 ? high : 16);
+  // The batch at codes, scales, with `high` rows of W left and `deep` groups of the wave's; of none, zeros that are not read:
+  // a load that some paths lack makes the compiler wait for all that is on its way.
+  const int64_t cgroup = wn * 64, sgroup = wstep;
+  auto load = [&](Reads& b, const uint8_t* codes, const uint8_t* scales, int high, int deep) __attribute__((always_inline)) {
+    const int tops = high < 0 ? 0 : high < 16 ? high : 16;
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const int g = from + batch * U + u;
-      const int real = g < to ? tops : 0;
-      const int64_t at = real ? (int64_t)g : 0;
-      const auto codes = __builtin_amdgcn_make_buffer_rsrc((void*)(w + (at * wn + w0) * 64), 0, real * 64, 0x00020000);
-      const auto scales = __builtin_amdgcn_make_buffer_rsrc((void*)(ws + at * wstep + w0 * 4), 0, real * 4, 0x00020000);
-      b.c[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(codes, r * 64 + q * 16, 0, 0));
-      b.e[u] = __builtin_amdgcn_raw_buffer_load_b8(scales, r * 4 + q, 0, 0);
+      const int real = u < deep ? tops : 0;
+      const auto c = __builtin_amdgcn_make_buffer_rsrc((void*)codes, 0, real * 64, 0x00020000);
+      const auto e = __builtin_amdgcn_make_buffer_rsrc((void*)scales, 0, real * 4, 0x00020000);
+      b.c[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(c, r * 64 + q * 16, 0, 0));
+      b.e[u] = __builtin_amdgcn_raw_buffer_load_b8(e, r * 4 + q, 0, 0);
+      codes += cgroup;
+      scales += sgroup;
     }
   };
 
-  const uint32_t chunk = uniform((uint32_t)(first / across));
+  const uint32_t chunk = uniform(total >> 32 ? (uint32_t)(first / across) : (uint32_t)first / across);
   uint32_t strip0 = (uint32_t)(first - (uint64_t)chunk * across);
   uint64_t left = last - first;   // units
   int turn = 0;
@@ -694,8 +695,11 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void k_mx4_experts_rows(const vo
     const int rows = end_of_rows - row0 < (uint32_t)most ? (int)(end_of_rows - row0) : most;
     uint32_t units = across - strip0;
     if (units > left) units = (uint32_t)left;
-    const int64_t w0 = expert * n + strip * 16;
-    auto high = [&](uint32_t at) { return n - ((int64_t)at * tall + strip) * 16; };   // rows of W from the strip's first on
+    auto high = [&](uint32_t at) { return (int)n - (int)(at * tall + strip) * 16; };   // rows of W from the strip's first on
+    // W's next batch, and of the strip of the unit that it is of (by additions: a batch's products of 64 bits would take as
+    // long as its matrix instructions)
+    const int64_t w0 = from * wn + expert * n + ((int64_t)strip0 * tall + strip) * 16;
+    const uint8_t *codes0 = w + w0 * 64, *scales0 = ws + from * wstep + (w0 - from * wn) * 4, *codes = codes0, *scales = scales0;
     // a thread's first two blocks of x, then W, whose way here hides the rest
     const int all = rows * blocks;
     auto block = [&](int i) {
@@ -713,11 +717,11 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void k_mx4_experts_rows(const vo
       Block<SRC> mine;
       if (i < all) mine = block(i);
       asm volatile("" ::: "memory");
-      load(a, w0 + (int64_t)strip0 * tall * 16, high(strip0), 0);
+      load(a, codes, scales, high(strip0), to - from);
       if (i < all) keep(i, mine);
       for (i += kThreads; i < all; i += kThreads) keep(i, block(i));
     }
-    __syncthreads();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // (W stays on its way)
 
     uint32_t at = strip0, end = strip0 + units;   // strips of W
     int batch = 0;
@@ -726,7 +730,13 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void k_mx4_experts_rows(const vo
     auto go = [&](const Reads& now, Reads& then) __attribute__((always_inline)) {
       const bool ends = batch + 1 == batches;
       const uint32_t next = ends ? at + 1 : at;
-      load(then, w0 + (int64_t)next * tall * 16, next < end ? high(next) : 0, ends ? 0 : batch + 1);
+      if (ends) {
+        codes0 += tall * 1024;
+        scales0 += tall * 64;
+      }
+      codes = ends ? codes0 : codes + U * cgroup;
+      scales = ends ? scales0 : scales + U * sgroup;
+      load(then, codes, scales, next < end ? high(next) : 0, to - from - (ends ? 0 : (batch + 1) * U));
 #pragma unroll
       for (int u = 0; u < U; u++) {
         const int g = from + batch * U + u;

@@ -938,7 +938,12 @@ class RmsNormCkpt8:
         holds it. `out`: a tensor for y, `h_out`: for h."""
         if x.requires_grad or weight.requires_grad or (residual is not None and residual.requires_grad):
             _refuse_grad(x=x, weight=weight, **({} if residual is None else {"residual": residual}))
-        key = ("y",) + _layout(x, weight, residual, out, h_out)
+        key = ("y", x.shape, x.stride(), x.dtype, x.get_device(), weight.shape, weight.stride(), weight.dtype,
+               weight.get_device())
+        if residual is not None:
+            key += (residual.shape, residual.stride(), residual.dtype, residual.get_device())
+        if out is not None or h_out is not None:
+            key += _layout(out, h_out)
         plan = self._plans.get(key)
         if plan is None:
             if h_out is not None and residual is None:
