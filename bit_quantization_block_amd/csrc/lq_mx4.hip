@@ -783,7 +783,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void k_mx4_experts_rows(const vo
     // the expert's next rows, or the next one's that has any (as in the table, but without its registers)
     row0 += most;
     while (left > 0 && row0 >= end_of_rows) {
-      expert++;
+      if (++expert >= (uint32_t)experts.count) return;   // (not with the offsets that the units were counted by)
       row0 = end_of_rows;
       const int32_t raw = ((const __attribute__((address_space(4))) int32_t*)(uintptr_t)experts.offsets)[expert + 1];
       const uint32_t end = raw < 0 ? 0u : raw > m ? (uint32_t)m : (uint32_t)raw;
