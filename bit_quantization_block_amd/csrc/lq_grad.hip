@@ -138,12 +138,14 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
   if constexpr (BY_EXPERT && KIND == kDgrad) {
     ExpertTable table;
     table.scan(g.experts, g.m, BM);
-    const uint32_t total = table.tiles_to(g.experts.count - 1) * g.tn, per8 = total / 8, more = total % 8;
+    const uint32_t tiles = table.tiles_to(g.experts.count - 1) * g.tn, total = tiles * g.parts, per8 = total / 8, more = total % 8;
     if (blockIdx.x / 8 >= per8 + (xcd < more ? 1 : 0)) return;
     const uint32_t mine8 = xcd * per8 + (xcd < more ? xcd : more) + blockIdx.x / 8;
-    expert = uniform(table.at(mine8 / g.tn, g.experts.count));
+    part = uniform(mine8 / tiles);
+    const uint32_t t = mine8 - part * tiles;
+    expert = uniform(table.at(t / g.tn, g.experts.count));
     const uint32_t before = table.tiles_before(expert);
-    t0 = mine8 - before * g.tn;
+    t0 = t - before * g.tn;
     tm = table.tiles_to(expert) - before;
     from = table.row_begin(expert);
     until = table.row_end(expert);
@@ -217,7 +219,7 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
   const int64_t rows = until;   // of A
   const int64_t w_rows = BY_EXPERT ? g.experts.count * g.n : g.n, w_first = expert * g.n;   // dgrad: rows of W as it is stored, and the expert's first
   const int all = (int)((depth + kStep - 1) / kStep), begin = RUNS ? 0 : (int)part * g.part;
-  const int steps = BY_EXPERT || begin + g.part >= all ? all : begin + g.part;
+  const int steps = (BY_EXPERT && KIND == kWgrad) || begin + g.part >= all ? all : begin + g.part;
 
   // ---- A: 16 bytes a load, 2 FM loads a step
   constexpr int kLoadsA = 2 * FM;
@@ -591,7 +593,7 @@ __device__ __forceinline__ void grad_tile_of(const GradArgs& g) {
   // What dw is added to, of 32 rows: asked for a block of rows ahead (a load may not pass a store that might be to the
   // same place: one by one, 154 x 11008 x 4096 took 123 us, and with 8 at a time 20 us more in 256 x 256 tiles).
   constexpr int kStores = units / 2;
-  const int64_t dw0 = BY_EXPERT && KIND == kWgrad ? expert * g.n : part * rows;   // of out: the expert's, or the plane's
+  const int64_t dw0 = BY_EXPERT && KIND == kWgrad ? expert * g.n : part * (BY_EXPERT ? g.m : rows);   // of out: the expert's, or the plane's
   v4f base[2][kStores];
   auto load_base = [&](int i) {
     if (KIND == kWgrad && g.in) {
@@ -764,7 +766,7 @@ hipError_t grad_experts_tiled(GradArgs& g, hipStream_t s) {
   // dgrad: at most one tile of rows an expert more than if the rows were one's, and an eighth of them for an XCD;
   // wgrad: an eighth of each expert's
   const int64_t tiles = KIND == kDgrad ? ((int64_t)g.m / (64 * FM) + g.experts.count) * g.tn : (int64_t)g.tm * g.tn;
-  const int64_t eighth = (tiles + 7) / 8 * (KIND == kDgrad ? 1 : g.experts.count);
+  const int64_t eighth = KIND == kDgrad ? (tiles * g.parts + 7) / 8 : (tiles + 7) / 8 * g.experts.count;
   const dim3 grid((unsigned)(eighth * 8));
   if (kMayBe && g.row % 8 != 0) hipLaunchKernelGGL((k_grad_experts<KIND, F, OUT, FM, FN, kMayBe>), grid, dim3(256), 0, s, g);
   else hipLaunchKernelGGL((k_grad_experts<KIND, F, OUT, FM, FN, false>), grid, dim3(256), 0, s, g);
@@ -784,12 +786,26 @@ hipError_t wgrad_experts(GradArgs g, void* ws, hipStream_t s) {
   hipLaunchKernelGGL((k_wgrad_experts<F>), dim3((unsigned)((eighth < at_once ? eighth : at_once) * 8)), dim3(256), 0, s, g);
   return hipGetLastError();
 }
+// dx: few tiles over a long contraction in parts, whose sums a launch of its own adds (2 rows over 2 experts of 4096 x 512
+// 11.7 us, in one part 32).
 template <int OUT>
-hipError_t dgrad_experts(GradArgs g, int tile, void* ws, hipStream_t s) {
-  constexpr int KIND = kDgrad, F = LQ_E2M1;
-  uint8_t* rest;
-  if (place_dy(g, ws, rest, s) != hipSuccess) return hipErrorLaunchFailure;
-  return tile == 4 ? grad_experts_tiled<KIND, F, OUT, 4, 4>(g, s) : grad_experts_tiled<KIND, F, OUT, 2, 2>(g, s);
+hipError_t dgrad_experts(GradArgs g, void* ws, hipStream_t s) {
+  uint8_t* planes;
+  if (place_dy(g, ws, planes, s) != hipSuccess) return hipErrorLaunchFailure;
+  const Split c = split_experts_dgrad(g.m, g.n, g.k, g.experts.count);
+  g.parts = c.parts;
+  g.part = c.part;
+  auto tiled = [&](auto out) {
+    constexpr int T = decltype(out)::value;
+    return c.tile == 4 ? grad_experts_tiled<kDgrad, LQ_E2M1, T, 4, 4>(g, s) : grad_experts_tiled<kDgrad, LQ_E2M1, T, 2, 2>(g, s);
+  };
+  if (c.parts == 1) return tiled(std::integral_constant<int, OUT>());
+  void* const out = g.out;
+  const int64_t ldo = g.ldo;
+  g.out = planes;
+  g.ldo = plane_stride(g.k);
+  const hipError_t e = tiled(std::integral_constant<int, LQ_F32>());
+  return e != hipSuccess ? e : launch_join_experts(g.experts, g.m, g.k, OUT, c.parts, (const float*)planes, out, ldo, s);
 }
 
 }  // namespace
@@ -798,11 +814,10 @@ hipError_t launch_mx4_experts_dgrad(const void* dy, const Experts& e, int64_t m,
                                     const void* w_codes, const void* w_scales, int64_t k, int out_dtype, void* dx,
                                     int64_t lddx, void* ws, hipStream_t s) {
   const GradArgs g = {(const uint16_t*)dy, m, n, k, lddy, n, (const uint8_t*)w_codes, (const uint8_t*)w_scales, nullptr, dx, lddx, 0, 0, 1, 0, e};
-  const int tile = expert_dgrad_tile(m, n, k, e.count);
   switch (out_dtype) {
-    case LQ_F32: return dgrad_experts<LQ_F32>(g, tile, ws, s);
-    case LQ_BF16: return dgrad_experts<LQ_BF16>(g, tile, ws, s);
-    default: return dgrad_experts<LQ_F16>(g, tile, ws, s);
+    case LQ_F32: return dgrad_experts<LQ_F32>(g, ws, s);
+    case LQ_BF16: return dgrad_experts<LQ_BF16>(g, ws, s);
+    default: return dgrad_experts<LQ_F16>(g, ws, s);
   }
 }
 

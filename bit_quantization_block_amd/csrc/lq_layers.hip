@@ -169,8 +169,10 @@ int lq_int4_linear(const lq_int4_desc* d, const void* x, const void* x_scales, c
 
 size_t lq_experts_workspace_bytes(const lq_experts_desc* d) {
   if (check_experts(d)) return 0;
-  const size_t dy = reads_in_place(d->m, d->n, d->ld_in) ? 0 : (size_t)(d->m * padded_columns(d->n)) * 2;
-  const size_t b = experts_operand(d) > dy ? experts_operand(d) : dy;
+  // the most of: the forward call's operand; a gradient's padded dy, and dx's parts' sums
+  const size_t dy = reads_in_place(d->m, d->n, d->ld_in) ? 0 : round256((size_t)(d->m * padded_columns(d->n)) * 2);
+  const size_t back = d->m ? dy + planes_bytes(split_experts_dgrad(d->m, d->n, d->k, d->experts), d->m, d->k) : 0;
+  const size_t b = experts_operand(d) > back ? experts_operand(d) : back;
   return b ? b : 256;
 }
 

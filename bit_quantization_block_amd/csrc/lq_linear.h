@@ -364,7 +364,8 @@ inline size_t planes_bytes(const Split& c, int64_t rows, int64_t cols) {
 }
 
 // The tile of a product over rows that lie by expert: rows / experts of them on the average (steps of 128, of 64, of 64).
-int expert_tile(int64_t m, int64_t n, int64_t k, int experts), expert_dgrad_tile(int64_t m, int64_t n, int64_t k, int experts);
+int expert_tile(int64_t m, int64_t n, int64_t k, int experts);
+Split split_experts_dgrad(int64_t m, int64_t n, int64_t k, int experts);
 
 // ------------------------------------------------------------ launchers
 // Instead of launching, the kernel's name and its template arguments for a plan being recorded (lq_plan.h).
@@ -373,6 +374,9 @@ int expert_tile(int64_t m, int64_t n, int64_t k, int experts), expert_dgrad_tile
 hipError_t launch_mx4_quantize(int in_dtype, int ckpt_format, const void* x, int64_t m, int64_t k, int64_t ldx,
                                void* codes, void* scales, void* ckpt_codes, void* ckpt_scales, hipStream_t s);
 hipError_t launch_constant(int64_t rows, int64_t cols, int dtype, const void* in, void* y, int64_t ldy, hipStream_t s);
+// (of the experts' rows only)
+hipError_t launch_join_experts(const Experts& e, int64_t rows, int64_t cols, int dtype, int parts, const float* planes, void* y,
+                               int64_t ldy, hipStream_t s);
 hipError_t launch_join(int64_t rows, int64_t cols, int dtype, int parts, const float* planes, const float* in, void* y,
                        int64_t ldy, hipStream_t s);
 hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,

@@ -74,16 +74,17 @@ constexpr TileCost kWgradTiles[] = {{2, 2, 6.0, 0.56, {0, 0.70, 1.17}, 8.0}, {4,
 // 130 us in one part, 32 in eight); adding the parts up costs a launch and their
 // sums' way through memory and back.
 // Rows that lie by expert end in a tile of their own each, half of one on the
-// average, and are not cut into parts.
+// average.
 template <size_t N>
-Split cheapest(const TileCost (&tiles)[N], int64_t rows, int64_t cols, int64_t steps, double further, int experts = 0) {
+Split cheapest(const TileCost (&tiles)[N], int64_t rows, int64_t cols, int64_t steps, double further, int experts = 0, int most = 32) {
   const double cus = compute_units();
   Split best = {tiles[0].tile, 1, (int)steps};
   double least = 1e300;
+  const int64_t ends = rows < experts ? rows : experts;
   for (const TileCost& c : tiles) {
-    const int64_t side = 64 * c.tile, count = ((rows + side - 1) / side + experts / 2) * ((cols + side - 1) / side);
+    const int64_t side = 64 * c.tile, count = ((rows + side - 1) / side + ends / 2) * ((cols + side - 1) / side);
     for (int64_t wanted : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
-      if (experts && wanted > 1) break;
+      if (wanted > most) break;
       const int64_t part = (steps + wanted - 1) / wanted, parts = part ? (steps + part - 1) / part : 1;
       if (wanted > 1 && (part < 4 || parts != wanted)) continue;
       const double wgs = (double)count * parts, planes = (double)parts * rows * cols * 4;
@@ -122,10 +123,10 @@ Split split_wgrad(int64_t m, int64_t n, int64_t k, bool adds) {
   return cheapest(kWgradTiles, n, k, (m + 63) / 64, adds ? (double)n * k * 4 : 0.0);
 }
 int expert_tile(int64_t m, int64_t n, int64_t k, int experts) {
-  return cheapest(kProductTiles, m, n, mx4_groups(k), 0.0, experts).tile;
+  return cheapest(kProductTiles, m, n, mx4_groups(k), 0.0, experts, 1).tile;
 }
-int expert_dgrad_tile(int64_t m, int64_t n, int64_t k, int experts) {
-  return cheapest(kDgradTiles, m, k, (n + 63) / 64, 0.0, experts).tile;
+Split split_experts_dgrad(int64_t m, int64_t n, int64_t k, int experts) {
+  return cheapest(kDgradTiles, m, k, (n + 63) / 64, 0.0, experts);
 }
 
 }  // namespace lql

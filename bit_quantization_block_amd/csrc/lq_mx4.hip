@@ -885,12 +885,12 @@ __global__ __launch_bounds__(256) void k_constant(int64_t rows, int64_t cols, co
 // y = in + the planes' sum, in the planes' order: four columns a lane, a wave's
 // on one row.
 template <int OUT>
-__global__ __launch_bounds__(256) void k_join(int64_t rows, int64_t cols, int parts, const float* planes,
-                                              const float* in, void* y, int64_t ldy) {
+__device__ __forceinline__ void join_rows(int64_t first, int64_t last, int64_t rows, int64_t cols, int parts, const float* planes,
+                                          const float* in, void* y, int64_t ldy) {
   const int64_t stride = plane_stride(cols), plane = rows * stride;
   const int64_t col = (int64_t)blockIdx.x * 256 + (threadIdx.x & 63) * 4;
   if (col >= cols) return;
-  for (int64_t row = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); row < rows; row += (int64_t)gridDim.y * 4) {
+  for (int64_t row = first + (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); row < last; row += (int64_t)gridDim.y * 4) {
     const float* p = planes + row * stride + col;
     float4 s = *(const float4*)p;
 #pragma unroll 4
@@ -915,8 +915,31 @@ __global__ __launch_bounds__(256) void k_join(int64_t rows, int64_t cols, int pa
     }
   }
 }
+template <int OUT>
+__global__ __launch_bounds__(256) void k_join(int64_t rows, int64_t cols, int parts, const float* planes,
+                                              const float* in, void* y, int64_t ldy) {
+  join_rows<OUT>(0, rows, rows, cols, parts, planes, in, y, ldy);
+}
+// Of the experts' rows, which follow one another.
+template <int OUT>
+__global__ __launch_bounds__(256) void k_join_experts(Experts e, int64_t rows, int64_t cols, int parts, const float* planes,
+                                                      void* y, int64_t ldy) {
+  int64_t first, last, end;
+  expert_rows(e, rows, 0, first, end);
+  expert_rows(e, rows, e.count - 1, end, last);
+  join_rows<OUT>(first, last, rows, cols, parts, planes, nullptr, y, ldy);
+}
 
 }  // namespace
+
+hipError_t launch_join_experts(const Experts& e, int64_t rows, int64_t cols, int dtype, int parts, const float* planes, void* y,
+                               int64_t ldy, hipStream_t s) {
+  const dim3 g = matrix_grid((cols + 255) / 256, rows);
+  if (dtype == LQ_F32) hipLaunchKernelGGL((k_join_experts<LQ_F32>), g, dim3(256), 0, s, e, rows, cols, parts, planes, y, ldy);
+  else if (dtype == LQ_BF16) hipLaunchKernelGGL((k_join_experts<LQ_BF16>), g, dim3(256), 0, s, e, rows, cols, parts, planes, y, ldy);
+  else hipLaunchKernelGGL((k_join_experts<LQ_F16>), g, dim3(256), 0, s, e, rows, cols, parts, planes, y, ldy);
+  return hipGetLastError();
+}
 
 hipError_t launch_join(int64_t rows, int64_t cols, int dtype, int parts, const float* planes, const float* in, void* y,
                        int64_t ldy, hipStream_t s) {

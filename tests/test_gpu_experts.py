@@ -98,6 +98,24 @@ def test_dgrad(m, experts, n, k, pad, before, behind, out):
     assert (dx[:off[0]] == 3).all() and (dx[off[-1]:] == 3).all() and (buffer[:, k:] == 3).all()
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32", "f16"])
+@pytest.mark.parametrize("m,experts,n,k,pad,before,behind", [(2, 2, 4096, 512, 0, 0, 0), (6, 40, 2001, 130, 1, 1, 2),
+                                                             (70, 3, 3001, 257, 3, 5, 0), (140, 1, 1500, 40, 0, 0, 9)])
+def test_dgrad_in_parts(m, experts, n, k, pad, before, behind, out):
+    """Few tiles over a long contraction are cut along it, and their sums added: of the experts' rows only, and the same
+    in every call."""
+    say(f"[gpu] experts dgrad {out} in parts, {m} rows, {experts} x {n} x {k} + {pad}, {before}, {behind}")
+    test_dgrad(m, experts, n, k, pad, before, behind, out)
+    off = on_gpu(split(m, experts, m, before, behind))
+    w, _ = weights(experts, n, k, 3)
+    dy, _ = matrix(m, n, "bf16", pad, 4)
+    layer = lq.Mx4Experts(w, rows=m, out=out)
+    first = layer.dgrad(dy, off)[before:m - behind].clone()
+    layer._workspaces[0].fill_(255)
+    assert torch.equal(layer.dgrad(dy, off)[before:m - behind], first)
+    assert not layer.dgrad(dy, torch.full_like(off, before), out=torch.zeros(m, k, dtype=T[out], device="cuda")).any()
+
+
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("m,experts,n,k,pad,before,behind", GRADS)
 def test_wgrad(m, experts, n, k, pad, before, behind, fmt):
