@@ -878,6 +878,8 @@ class RmsNormCkpt8:
     dh or h (the same rows), but no other part of them. Calls of one object share its buffers: on two streams at a time,
     use two objects. As the linear layer's, its calls are no part of autograd's graph."""
 
+    _dw = None   # dw, if it is the object's own
+
     def __init__(self, rows: int, cols: int, dtype: str = "bf16", fmt: str = "int8", eps: float = 1e-6, device="cuda",
                  lib=None):
         import torch
@@ -984,7 +986,12 @@ class RmsNormCkpt8:
         alike; dw = dw_in + the rows' sum, in float32. `out`: a tensor for dx, `dw_out`: for dw (it may be dw_in)."""
         if dy.requires_grad or h.requires_grad or weight.requires_grad or (dh is not None and dh.requires_grad):
             _refuse_grad(dy=dy, h=h, weight=weight, **({} if dh is None else {"dh": dh}))
-        key = ("dx",) + _layout(dy, h, weight, dh, dw_in, out, dw_out)
+        key = ("dx", dy.shape, dy.stride(), dy.dtype, dy.get_device(), h.shape, h.stride(), h.dtype, h.get_device(),
+               weight.shape, weight.stride(), weight.dtype, weight.get_device())
+        if dh is not None:
+            key += (dh.shape, dh.stride(), dh.dtype, dh.get_device())
+        if dw_in is not None or out is not None or dw_out is not None:
+            key += _layout(dw_in, out, dw_out)
         plan = self._plans.get(key)
         if plan is None:
             self._weight(weight)
@@ -996,7 +1003,11 @@ class RmsNormCkpt8:
                                   self._stride(out, "out"))
         ref, (ry, rd, rh, rx) = plan
         dx = out if out is not None else self._own("dx", stream)
-        dw = dw_out if dw_out is not None else self._own("dw", stream, (max(4, self.cols),), self.torch.float32)[:self.cols]
+        dw = dw_out
+        if dw is None:
+            dw = self._dw
+            if dw is None:
+                dw = self._dw = self._own("dw", stream, (max(4, self.cols),), self.torch.float32)[:self.cols]
         pdy, pd, ph, px = dy.data_ptr(), None, h.data_ptr(), dx.data_ptr()
         if pdy < px + rx and px < pdy + ry:
             self._refuse(dy, dx, "dy and dx")
