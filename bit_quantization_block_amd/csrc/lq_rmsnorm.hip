@@ -6,7 +6,8 @@
 //
 // h is the rounded sum, as the residual stream keeps it, in both passes; the
 // checkpoint is of the rounded y, whether y is written or not: it holds what the
-// checkpoint of a layer called on y would. Sums are in binary32.
+// checkpoint of a layer called on y would. Sums are in binary32, of a row whose squares
+// leave its range times a power of two.
 //
 // Both passes read and write each matrix once and are bound by memory: a row stays
 // in the registers of T threads, V times eight elements each, from its load to its
@@ -120,10 +121,39 @@ __device__ __forceinline__ void hide(Words<DT>& r) {
   for (int i = 0; i < (int)(sizeof(r.w) / 4); i++) asm volatile("" : "+v"(r.w[i]));
 }
 
+// The sum of a row's squares where binary32 cannot hold it as it is: infinite, as of finite
+// values from about 2^57 on, or so small (without an eps beside it) that squares get lost
+// below the subnormal numbers. Taken anew of the row times a power of two, which is
+// returned: 2^-72 leaves the largest values' squares below 2^112, 2^96 the smallest ones'
+// above 2^-106. A row that holds an infinity or a NaN gets a NaN, and is NaN throughout.
+// (The sum is the same in all of a row's threads, and so is the way that they take. `slots`
+// is this call's alone: the next row's first sum, whose barrier everyone has to pass, is
+// between its reads and the next call's writes.)
+template <int DT, int T, int V>
+__device__ __forceinline__ float sum_in_range(const Raw8<DT> (&h)[V], float& sum, float eps, float (*slots)[16]) {
+  const bool low = sum < 0x1p-100f && eps < 0x1p-90f, high = !(sum + eps < __builtin_inff());
+  if (!low && !high) return 1.0f;
+  const float scale = low ? 0x1p96f : 0x1p-72f;
+  float again = 0.0f;
+#pragma unroll
+  for (int c = 0; c < V; c++) {
+    float v[8];
+    widen8<DT>(h[c], v);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const float s = v[i] * scale;
+      again = __builtin_fmaf(s, s, again);
+    }
+  }
+  sum = row_sum<T>(again, slots, 0);
+  if (!(sum < __builtin_inff())) sum = __builtin_nanf("");
+  return scale;
+}
+
 template <int DT, int F, int T, int V>
 __global__ __launch_bounds__(Shape<T>::threads) void k_rmsnorm(const NormArgs a) {
   typedef typename El<DT>::T E;
-  __shared__ float slots[2][16];
+  __shared__ float slots[2][16], more_slots[1][16];
   const int lane = T == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int cols = (int)a.cols;
   int valid[V];
@@ -173,7 +203,9 @@ __global__ __launch_bounds__(Shape<T>::threads) void k_rmsnorm(const NormArgs a)
         store8<DT>((E*)a.h + row * a.ldh, (int64_t)(c * T + lane) * 8, valid[c], v);
       }
     }
-    const float rs = 1.0f / sqrtf(row_sum<T>(sum, slots, turn) / (float)a.cols + a.eps);
+    sum = row_sum<T>(sum, slots, turn);
+    const float power = sum_in_range<DT, T, V>(h, sum, a.eps, more_slots);
+    const float rs = power / sqrtf(sum / (float)a.cols + a.eps * power * power);
     if (a.rs && lane == 0) a.rs[row] = rs;
 #pragma unroll
     for (int c = 0; c < V; c++) {

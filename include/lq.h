@@ -409,10 +409,12 @@ LQ_API int lq_swiglu_ckpt8_backward(const lq_swiglu_desc* desc, const void* dh, 
  * backward, from h and rs, with g = dy weight and n = h rs:
  *   dx = dh + rs (g - n mean(g n)), the gradient of x and of the residual alike
  *   dw = dw_in + sum over the rows of dy n
- * Additions, squares and sums are in binary32 (|h| up to 2^63); a repeated call
- * gives the same bits. A row that holds an infinity or a NaN is NaN, and so is a
- * row of zeros with eps 0. Rows are of at most 16384 elements
- * (LQ_ERR_UNSUPPORTED beyond). Matrices have a row stride each and start at a
+ * Additions, squares and sums are in binary32, of rows whose squares leave its range
+ * after a multiplication by a power of two (|h| up to 2^127; with eps 0, rows of a root
+ * mean square of 2^-126 or more); a repeated call gives the same bits. A row whose h
+ * holds an infinity or a NaN is NaN in all of y, of the checkpoint and of dx, and its
+ * rs, and with it all of dw, too; so is a row of zeros with eps 0. Rows are of at most
+ * 16384 elements (LQ_ERR_UNSUPPORTED beyond). Matrices have a row stride each and start at a
  * multiple of 16 bytes; layouts, ownership, streams and errors as above. Buffers
  * of one call must not overlap, except that h or y may be x or the residual, and
  * dx may be dy, dh or h, with the same row stride, and dw may be dw_in. */
