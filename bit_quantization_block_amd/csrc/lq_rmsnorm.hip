@@ -4,6 +4,9 @@
 //   h = x + r    rs = 1 / sqrt(mean(h^2) + eps)    n = h rs    y = n w
 //   g = dy w     dx = dh + rs (g - n mean(g n))    dw = dw_in + sum over rows of dy n
 //
+// (forward, n is the quotient to the nearest; backward, the product with the rounded rs
+// that the forward pass keeps)
+//
 // h is the rounded sum, as the residual stream keeps it, in both passes; the
 // checkpoint is of the rounded y, whether y is written or not: it holds what the
 // checkpoint of a layer called on y would. Sums are in binary32, of a row whose squares
@@ -205,7 +208,8 @@ __global__ __launch_bounds__(Shape<T>::threads) void k_rmsnorm(const NormArgs a)
     }
     sum = row_sum<T>(sum, slots, turn);
     const float power = sum_in_range<DT, T, V>(h, sum, a.eps, more_slots);
-    const float rs = power / sqrtf(sum / (float)a.cols + a.eps * power * power);
+    const float root = sqrtf(sum / (float)a.cols + a.eps * power * power), rs = power / root;
+    const float natural = root * (1.0f / power);   // (exact, as 1 / power is)
     if (a.rs && lane == 0) a.rs[row] = rs;
 #pragma unroll
     for (int c = 0; c < V; c++) {
@@ -215,7 +219,10 @@ __global__ __launch_bounds__(Shape<T>::threads) void k_rmsnorm(const NormArgs a)
       Raw8<DT> y;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        y.t[i] = narrow<DT>(v[i] * rs * w[c][i]);
+        // h / root to the nearest: the product with rs, whose own rounding it has, and what that leaves of h times rs
+        float n = v[i] * rs;
+        n = __builtin_fmaf(__builtin_fmaf(-n, natural, v[i]), rs, n);
+        y.t[i] = narrow<DT>(n * w[c][i]);
         if (i >= valid[c]) y.t[i] = (E)0;   // (0 times an infinite rs is no zero)
       }
       widen8<DT>(y, v);

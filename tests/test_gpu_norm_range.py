@@ -98,3 +98,36 @@ def test_rows_of_either_kind_beside_others():
         keep[11::97] = False
         assert y[~keep].isnan().all() and torch.equal(y[keep], want[keep])
         assert torch.equal(norm.rs[:rows][keep], (plain.rs[:rows] * torch.exp2(-power[:, 0]))[keep])
+
+
+# three whole numbers of a mean square that is a square
+THREES = {3: [(1, 1, 5)], 7: [(1, 5, 11)], 11: [(5, 7, 17), (5, 13, 13)], 13: [(5, 11, 19), (7, 13, 17)],
+          15: [(1, 7, 25), (3, 15, 21), (5, 5, 25), (5, 11, 23)], 21: [(3, 15, 33), (7, 7, 35)], 25: [(1, 5, 43), (5, 13, 41), (11, 23, 35)]}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("cols", [3, 33, 510, 1002, 2046, 4095, 8190, 16383])
+def test_a_quotient_is_rounded_once(cols, dtype):
+    """Rows whose root mean square is a whole number, so that all before the quotient is exact: h / root is the nearest number
+    to it, and no product with a rounded 1 / root; then one rounding for the weight's product, and the result's."""
+    say(f"[gpu] norm quotient {dtype} {cols}")
+    g = torch.Generator().manual_seed(cols)
+    rows, roots = [], []
+    for root, threes in THREES.items():
+        for t in threes:
+            # (sums of squares up to 16383 * 25^2 < 2^24; powers of two change nothing)
+            for power in (1.0, 2.0 ** -3):
+                sign = torch.randint(0, 2, (cols,), generator=g) * 2.0 - 1
+                rows.append(torch.tensor(t, dtype=torch.float32).repeat(cols // 3)[torch.randperm(cols, generator=g)] * sign * power)
+                roots.append(root * power)
+    x, root = torch.stack(rows).to(T[dtype]).cuda(), torch.tensor(roots, device="cuda")[:, None]
+    n = (x.double() / root.double()).float()
+    for w in (torch.ones(cols, device="cuda"), weights(cols, "f32", 1)):
+        norm = lq.RmsNormCkpt8(len(rows), cols, dtype, eps=0.0)
+        y, _ = norm.forward(x, w)
+        # the product with the weight goes to its type by way of binary32, or, where an instruction of the card multiplies and
+        # converts, straight: on what binary32 rounds to a tie of binary16 the two differ by one step, and either is right
+        straight = (n.double() * w.double()).cpu()   # exact: 24 bits times 24
+        straight = torch.from_numpy(straight.numpy().astype("float16")).cuda() if dtype == "f16" else straight.to(T[dtype]).cuda()
+        assert ((y == (n * w).to(T[dtype])) | ((y == straight) if dtype == "f16" else False)).all()
+        assert torch.equal(norm.rs[:len(rows), None], (1 / root.double()).float())
