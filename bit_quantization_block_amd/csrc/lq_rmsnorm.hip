@@ -15,7 +15,7 @@
 // Both passes read and write each matrix once and are bound by memory: a row stays
 // in the registers of T threads, V times eight elements each, from its load to its
 // last store, and the next row's loads are on their way meanwhile. 8192 x 4096 bf16:
-// forward with the residual, h, y and the checkpoint 57 us (5.3 TB/s of what it reads and
+// forward with the residual, h, y and the checkpoint 58 us (5.2 TB/s of what it reads and
 // writes), backward 55.5 us (4.8 TB/s; dw's planes are the rest); a copy of 1 GiB reaches
 // 5.2 TB/s.
 #include "lq_linear.h"
@@ -124,19 +124,24 @@ __device__ __forceinline__ void hide(Words<DT>& r) {
   for (int i = 0; i < (int)(sizeof(r.w) / 4); i++) asm volatile("" : "+v"(r.w[i]));
 }
 
-// The sum of a row's squares where binary32 cannot hold it as it is: infinite, as of finite
-// values from about 2^57 on, or so small (without an eps beside it) that squares get lost
-// below the subnormal numbers. Taken anew of the row times a power of two, which is
-// returned: 2^-72 leaves the largest values' squares below 2^112, 2^96 the smallest ones'
-// above 2^-106. A row that holds an infinity or a NaN gets a NaN, and is NaN throughout.
+// The root of a row's mean square (with eps), and its reciprocal, from the sum of the squares.
+// Where binary32 cannot hold that sum as it is, infinite, as of finite values from about
+// 2^57 on, or so small (without an eps beside it) that squares get lost below the subnormal
+// numbers, it is taken anew of the row times a power of two: 2^-72 leaves the largest
+// values' squares below 2^112, 2^96 the smallest ones' above 2^-106. A row that holds an
+// infinity or a NaN gets a NaN, and is NaN throughout.
 // (The sum is the same in all of a row's threads, and so is the way that they take. `slots`
 // is this call's alone: the next row's first sum, whose barrier everyone has to pass, is
 // between its reads and the next call's writes.)
+struct Root { float root, rs; };
 template <int DT, int T, int V>
-__device__ __forceinline__ float sum_in_range(const Raw8<DT> (&h)[V], float& sum, float eps, float (*slots)[16]) {
+__device__ __forceinline__ Root root_of(const Raw8<DT> (&h)[V], float sum, float cols, float eps, float (*slots)[16]) {
   const bool low = sum < 0x1p-100f && eps < 0x1p-90f, high = !(sum + eps < __builtin_inff());
-  if (!low && !high) return 1.0f;
-  const float scale = low ? 0x1p96f : 0x1p-72f;
+  if (__builtin_expect(!low && !high, 1)) {
+    const float root = sqrtf(sum / cols + eps);
+    return {root, 1.0f / root};
+  }
+  const float power = low ? 0x1p96f : 0x1p-72f;
   float again = 0.0f;
 #pragma unroll
   for (int c = 0; c < V; c++) {
@@ -144,13 +149,14 @@ __device__ __forceinline__ float sum_in_range(const Raw8<DT> (&h)[V], float& sum
     widen8<DT>(h[c], v);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const float s = v[i] * scale;
+      const float s = v[i] * power;
       again = __builtin_fmaf(s, s, again);
     }
   }
-  sum = row_sum<T>(again, slots, 0);
-  if (!(sum < __builtin_inff())) sum = __builtin_nanf("");
-  return scale;
+  again = row_sum<T>(again, slots, 0);
+  if (!(again < __builtin_inff())) again = __builtin_nanf("");
+  const float root = sqrtf(again / cols + eps * power * power);
+  return {root * (low ? 0x1p-96f : 0x1p72f), power / root};
 }
 
 template <int DT, int F, int T, int V>
@@ -206,10 +212,7 @@ __global__ __launch_bounds__(Shape<T>::threads) void k_rmsnorm(const NormArgs a)
         store8<DT>((E*)a.h + row * a.ldh, (int64_t)(c * T + lane) * 8, valid[c], v);
       }
     }
-    sum = row_sum<T>(sum, slots, turn);
-    const float power = sum_in_range<DT, T, V>(h, sum, a.eps, more_slots);
-    const float root = sqrtf(sum / (float)a.cols + a.eps * power * power), rs = power / root;
-    const float natural = root * (1.0f / power);   // (exact, as 1 / power is)
+    const auto [root, rs] = root_of<DT, T, V>(h, row_sum<T>(sum, slots, turn), (float)a.cols, a.eps, more_slots);
     if (a.rs && lane == 0) a.rs[row] = rs;
 #pragma unroll
     for (int c = 0; c < V; c++) {
@@ -221,7 +224,7 @@ __global__ __launch_bounds__(Shape<T>::threads) void k_rmsnorm(const NormArgs a)
       for (int i = 0; i < 8; i++) {
         // h / root to the nearest: the product with rs, whose own rounding it has, and what that leaves of h times rs
         float n = v[i] * rs;
-        n = __builtin_fmaf(__builtin_fmaf(-n, natural, v[i]), rs, n);
+        n = __builtin_fmaf(__builtin_fmaf(-n, root, v[i]), rs, n);
         y.t[i] = narrow<DT>(n * w[c][i]);
         if (i >= valid[c]) y.t[i] = (E)0;   // (0 times an infinite rs is no zero)
       }
