@@ -122,14 +122,21 @@ struct Int4Args {
   int out, turns;          // y's type; times that the contraction runs through W (the parts of binary32 x, one after another)
 };
 
-// Eight codes of W as 16 + u in the operand's type: j = 0..3 picks nibbles j and j + 4.
-// binary16: exponent of 16, a step of 2^-6; bfloat16: a step of 2^-3. (The two constants
+// What the matrix cores multiply by, 16 + u and one, is held times a power of two where x
+// has binary32's range: a group's (16 + u) x, and (24 + z) times its sum of x, are up to
+// 2^12 times an element (2^14.3 for zero points of 128), and 2^120 of that would be an
+// infinity. The scale, times 2^8, makes up for it; every step is exact.
+template <int SRC> struct Held { static constexpr float up = 256.0f, down = 1.0f / up; };
+template <> struct Held<LQ_F16> { static constexpr float up = 1.0f, down = 1.0f; };   // (x up to 65504)
+
+// Eight codes of W as 16 + u in the operand's type, times Held's 2^-8: j = 0..3 picks nibbles j and j + 4.
+// binary16: exponent of 16, a step of 2^-6; bfloat16: of 2^-4, a step of 2^-3 times 2^-8. (The two constants
 // are in registers of either kind: an instruction takes one from a scalar one, and no
 // literal besides.)
 template <int SRC>
 struct Widen {
   uint32_t mask, magic;
-  __device__ __forceinline__ Widen() : mask(SRC == LQ_F16 ? 0x03C003C0u : 0x00780078u), magic(SRC == LQ_F16 ? 0x4C004C00u : 0x41804180u) {
+  __device__ __forceinline__ Widen() : mask(SRC == LQ_F16 ? 0x03C003C0u : 0x00780078u), magic(SRC == LQ_F16 ? 0x4C004C00u : 0x3D803D80u) {
     asm volatile("" : "+s"(mask));
     asm volatile("" : "+v"(magic));
   }
@@ -219,14 +226,14 @@ __global__ __launch_bounds__(64 * kWaves, STAGED ? 4 : 2) void k_int4(const Int4
     for (int k = 0; k < kUnits; k++) {
       const int i = k * 64 + lane;
       if (i < both) {
-        const float more = i < units ? 0.0f : 24.0f;
+        const float more = i < units ? 0.0f : 24.0f, times = i < units ? Held<SRC>::up : 1.0f;
         uint16_t h[8];
         __builtin_memcpy(h, &b.v[k], 16);
 #pragma unroll
         for (int f = 0; f < 2; f++) {
           v4f v;
 #pragma unroll
-          for (int e = 0; e < 4; e++) v[e] = widen<LQ_F16>(h[4 * f + e]) + more;
+          for (int e = 0; e < 4; e++) v[e] = __builtin_fmaf(widen<LQ_F16>(h[4 * f + e]), times, more);
           *(v4f*)(bank + i * 32 + f * 16) = v;
         }
       }
@@ -270,7 +277,8 @@ __global__ __launch_bounds__(64 * kWaves, STAGED ? 4 : 2) void k_int4(const Int4
   v4f y[CT];
 #pragma unroll
   for (int c = 0; c < CT; c++) y[c] = none;
-  constexpr int one2 = SRC == LQ_F16 ? 0x3C003C00 : 0x3F803F80;
+  constexpr int one2 = SRC == LQ_F16 ? 0x3C003C00 : 0x3B803B80;   // (bfloat16: 2^-8, as the codes)
+  static_assert(Held<SRC>::down == (SRC == LQ_F16 ? 1.0f : 0x1p-8f), "the constants here and in Widen");
   const v4i ones = {one2, one2, one2, one2};
   const uint8_t* const xrow = xlds + (r < rows ? r : 0) * staged_pitch(a.k) + q * 16;
   const int64_t plane = rows * staged_pitch(a.k);

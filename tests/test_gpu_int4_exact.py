@@ -116,6 +116,37 @@ def test_all_parts_of_binary32(m, n, k128):
             check(x, "f32", stored, w, "f32", 1)
 
 
+@gpu
+@pytest.mark.parametrize("source,power", [("bf16", 118), ("int8", 118), ("e4m3", 118), ("f32", 118), ("f16", 13), ("bf16", -90), ("f32", -90),
+                                          ("int8", -90), ("e4m3", -90), ("f16", -20)])
+@pytest.mark.parametrize("m,n,k128", [(1, 40, 3), (3, 70, 8), (2, 8200, 2), (16, 33, 33), (40, 50, 5), (64, 40, 8)])
+def test_the_largest_and_smallest_elements(m, n, k128, source, power):
+    """Elements up to 2^120 in magnitude, all of one sign in some rows, with zero points up to 128: what is added up before the
+    zero point is taken off, 32 and more times as large as what is left, stays in binary32's range."""
+    for group in (32, 64, 128):
+        k = k128 * 128
+        say(f"[gpu] int4 {source} 2^{power} group {group} {m}x{n}x{k}")
+        x = whole(m, k, m + k)
+        x[0] = 3.0
+        x[m - 1] = x[m - 1].abs()
+        for most, zeros in ((8, False), (8, True), (128, True)):
+            stored, w = weights(n, k, group, zeros, n + k, most=most, scales=(2.0 ** -14, 2.0 ** -13))
+            # |q - z| <= 136
+            assert (x.abs() @ w.abs().t()).max() * 2.0 ** 14 < 2.0 ** 24
+            check(x * 2.0 ** power, source, stored, w, "f32", 2)
+
+
+@gpu
+@pytest.mark.parametrize("m,n,k128", [(1, 40, 32), (3, 70, 9), (1, 8200, 8), (40, 100, 12), (64, 64, 8)])
+def test_all_parts_of_the_largest_and_smallest(m, n, k128):
+    for group in (32, 64, 128):
+        for power in (99, -90):
+            say(f"[gpu] int4 parts 2^{power} group {group} {m}x{n}x{k128 * 128}")
+            x = parts(m, k128 * 128, group, m + k128) * 2.0 ** power
+            stored, w = weights(n, k128 * 128, group, True, n, codes=(-8, -4, 0, 4), scales=(2.0 ** -14,))
+            check(x, "f32", stored, w, "f32", 1)
+
+
 def test_the_parts_are_there_and_matter():
     """Without any one of an element's parts, results of the test above are others."""
     k, group = 1152, 64
