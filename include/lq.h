@@ -454,7 +454,9 @@ LQ_API int lq_rmsnorm_backward(const lq_norm_desc* desc, const void* dy, const v
  * the gated unit or lq_mx4_quantize leave it, taken at the values it holds. Products
  * are exact and added in binary32 (values of x up to 2^120 in magnitude, zero points up
  * to 128; of binary32 elements, bits below 2^-133 are rounded away), groups are scaled
- * and added in binary32, and y is rounded once, to nearest even. A repeated call
+ * and added in binary32, and y is rounded once, to nearest even. What is added up before
+ * the zero point is taken off is up to 31 |x| an element: the sums' rounding goes with the
+ * row's sum of s |x|, also where q - z is small or zero. A repeated call
  * gives the same bits. An infinity or a NaN in a row of x makes the row of y NaN.
  *
  * W is laid out once for the kernels by lq_int4_pack, into lq_int4_packed_bytes() (0 on
