@@ -432,7 +432,7 @@ hipError_t launch_int4_linear(const lq_int4_desc* d, const void* x, const void* 
                               void* ws, hipStream_t s);
 
 // The layer of many experts (lq_mx4.hip, lq_grad.hip): W is an MX4 operand of experts * n rows.
-bool experts_few(int64_t m, int experts), experts_in_place(int64_t m, int64_t k, int experts);
+bool experts_in_place(int64_t m, int64_t k, int experts);
 hipError_t launch_mx4_experts_few(int in_dtype, const void* x, int64_t ldx, const Experts& e, const void* w_codes,
                                   const void* w_scales, int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy,
                                   hipStream_t s);

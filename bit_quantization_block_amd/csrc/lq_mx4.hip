@@ -616,15 +616,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(const void* x, int64
                                                             int64_t ldy) {
   mx4_few<SRC, OUT, R, CT>(x, ldx, xs, m, 0, w, ws, n, 0, m, n, k, y, ldy);
 }
-// By expert, of an MX4 operand: an expert a row of the grid, 16 rows at a time.
+// By expert, of an MX4 operand: an expert a row of the grid, 16 rows at a time, every gridDim.z-th of these chunks.
 template <int OUT, int R>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_experts_few(const void* x, const uint8_t* xs, const uint8_t* w,
                                                                     const uint8_t* ws, int64_t m, int64_t n, int64_t k, void* y,
                                                                     int64_t ldy, Experts experts) {
   int64_t begin, end;
   expert_rows(experts, m, blockIdx.y, begin, end);
-  for (int64_t row = begin; row < end; row += 16) {
-    if (row > begin) __syncthreads();   // (the last rows' sums have been read)
+  const int64_t first = begin + 16 * (int64_t)blockIdx.z;
+  for (int64_t row = first; row < end; row += 16 * (int64_t)gridDim.z) {
+    if (row > first) __syncthreads();   // (the last rows' sums have been read)
     const int64_t rows = end - row < 16 ? end - row : 16;
     mx4_few<kOperand, OUT, R, 1>(x, 0, xs, m, row, w, ws, experts.count * n, blockIdx.y * n, rows, n, k,
                                  (typename El<OUT>::T*)y + row * ldy, ldy);
@@ -989,13 +990,38 @@ hipError_t launch_mx4_product(const void* a_codes, const void* a_scales, const v
   }
 }
 
-// Rows by expert: few of each are bound by reading W, which a row of workgroups reads
-// once for sixteen rows.
-bool experts_few(int64_t m, int experts) { return m <= 16 * (int64_t)experts; }
-// Few rows straight from x, at least one of them at a time in LDS (and not many more
-// than a launch of its own is worth).
+// Rows by expert, few of each. The counts are on the device: these rules know the rows that
+// an expert has on the average, and have to do well where most go to one. W in memory, in a
+// graph; rows spread evenly / half of them to one expert / all to one:
+//
+// Straight from x, where an expert's rows, up to 16, take up to a quarter of LDS on the average. A chunk
+// is quantised by every workgroup that has a strip of W for it, and of long rows it is short,
+// so that W is read for few rows at a time. In place, or x to 4 bits in a launch of its own
+// and then the better of the kernels below:
+//   128 rows over 64 of 1024 x 2048   20.5 / 23.3 / 10.6 us   22.4 / 23.6 / 9.3
+//   32 over 8 of 2048 x 4096          14.7 / 17.7 / 14.8      14.8 / 14.9 / 8.3
+//   1024 over 64 of 2048 x 4096       78.6 / 83.7 / 52.8      69.4 / 73.9 / 23.1
+//   128 over 8 of 512 x 16384         25.7 / 25.0 / 22.6      16.4 / 20.7 / 17.4
 bool experts_in_place(int64_t m, int64_t k, int experts) {
-  return experts_few(m, experts) && mx4_groups(k) * 4 <= kFewBlocks;
+  return m <= 16 * (int64_t)experts && mx4_groups(k) * 4 <= kFewBlocks && m * mx4_groups(k) * 4 <= kFewBlocks / 4 * experts;
+}
+// Of an operand: a row of workgroups for each expert, which reads W once for sixteen rows,
+// where these are one for each compute unit at most, of up to four rows an expert two; there
+// they finish a long contraction sooner than tiles, whose steps follow one another. More of
+// them take their turns, and all rows at one expert are theirs alone. By rows, or in tiles:
+//   32 over 2 of 1024 x 4096       7.1 / 7.1 / 6.9 us     12.0 / 12.1 / 12.2
+//   8 over 8 of 512 x 16384        13.8 / 11.9 / 10.8     34.1 / 32.8 / 28.3
+//   32 over 8 of 2048 x 4096       14.8 / 16.7 / 8.3      15.5 / 14.9 / 12.0
+//   64 over 4 of 4096 x 4096       16.2 / 18.5 / 12.7     15.7 / 15.2 / 12.1
+//   1024 over 64 of 2048 x 2048    75 / 126 / 178         37.6 / 40.3 / 14.4
+// `r`: 16 or 32 rows of W a workgroup, 32 where the experts with rows leave one of those for
+// each compute unit, as above.
+static int experts_few_strips(int64_t m, int64_t n, int experts) {
+  return n * (m < experts ? m : experts) >= 32 * (int64_t)compute_units() ? 2 : 1;
+}
+static bool experts_few(int64_t m, int64_t n, int experts) {
+  const int64_t wide = 16 * experts_few_strips(m, n, experts);
+  return m <= 16 * (int64_t)experts && (n + wide - 1) / wide * experts <= compute_units() * (m <= 4 * (int64_t)experts ? 2 : 1);
 }
 
 namespace {
@@ -1003,9 +1029,11 @@ namespace {
 template <int OUT>
 hipError_t experts_few_out(const void* x, const void* xs, const Experts& e, const void* w, const void* ws, int64_t m, int64_t n,
                            int64_t k, void* y, int64_t ldy, hipStream_t s) {
-  // 32 rows of W a workgroup where the experts with rows leave one of those for each compute unit, as above
-  const int r = n * (m < e.count ? m : e.count) >= 32 * (int64_t)compute_units() ? 2 : 1;
-  const dim3 grid((unsigned)((n + 16 * r - 1) / (16 * r)), (unsigned)e.count);
+  const int r = experts_few_strips(m, n, e.count);
+  const int64_t strips = (n + 16 * r - 1) / (16 * r);
+  // the chunks that one expert may have at most, side by side as far as eight workgroups a compute unit allow it
+  const int64_t chunks = (m + 15) / 16, beside = 8 * (int64_t)compute_units() / (strips * e.count);
+  const dim3 grid((unsigned)strips, (unsigned)e.count, (unsigned)(chunks < beside ? chunks : beside));
   if (r == 2)
     hipLaunchKernelGGL((k_mx4_experts_few<OUT, 2>), grid, dim3(64 * kFewWaves), 0, s, x, (const uint8_t*)xs, (const uint8_t*)w,
                        (const uint8_t*)ws, m, n, k, y, ldy, e);
@@ -1071,7 +1099,7 @@ hipError_t launch_mx4_experts_few(int in_dtype, const void* x, int64_t ldx, cons
 hipError_t launch_mx4_experts(const void* a_codes, const void* a_scales, const Experts& e, const void* w_codes,
                               const void* w_scales, int64_t m, int64_t n, int64_t k, int out_dtype, void* y, int64_t ldy,
                               hipStream_t s) {
-  if (experts_few(m, e.count)) switch (out_dtype) {
+  if (experts_few(m, n, e.count)) switch (out_dtype) {
     case LQ_F32: return experts_few_out<LQ_F32>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
     case LQ_BF16: return experts_few_out<LQ_BF16>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
     default: return experts_few_out<LQ_F16>(a_codes, a_scales, e, w_codes, w_scales, m, n, k, y, ldy, s);
