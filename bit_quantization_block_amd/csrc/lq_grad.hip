@@ -773,7 +773,7 @@ hipError_t grad_experts_tiled(GradArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 // dw: in 256 x 256 tiles, as many workgroups as run at once, which make one after another. Where it is added to dw_in, whose
-// elements have no registers there, in 128 x 128 tiles (8192 rows over 16 experts of 2048 x 4096 341 us, in 256 x 256 tiles
+// elements have no registers there, in 128 x 128 tiles (8192 rows over 16 experts of 2048 x 4096 311 to 341 us, in 256 x 256 tiles
 // of a workgroup each 443), and so it is where a tile's rows pass 2^31 bytes.
 template <int F>
 hipError_t wgrad_experts(GradArgs g, void* ws, hipStream_t s) {

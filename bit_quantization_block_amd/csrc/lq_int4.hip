@@ -174,7 +174,7 @@ __device__ __forceinline__ v4f multiply(v4i a, v4i b, v4f c) {
 // as fit in its bank, and the next page is on its way meanwhile: converted there, each
 // is converted once instead of by the sixteen lanes that multiply by it.
 // Measured, W in memory, within a graph: one row of 11008 x 4096 9.5 us, 16 rows of 4096 x
-// 11008 from an 8-bit checkpoint 15.5 us (12.3 with W in the last-level cache), 64 rows of
+// 11008 from an 8-bit checkpoint 15.4 us (11.9 with W in the last-level cache), 64 rows of
 // 4096 x 4096 15 us, 8 rows of 16384 x 16384 55 us. One row reads W at 2.5 TB/s, which its
 // start and end bound (the large W streams no faster for eight rows: there the sums of a
 // step's groups and the widening of its codes do); many rows are bound by x's operands,

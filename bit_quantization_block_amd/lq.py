@@ -936,8 +936,9 @@ class RmsNormCkpt8:
             raise ValueError(f"{what} share memory" + (", but are not the same" if same else ""))
 
     def forward(self, x, weight, residual=None, y=True, out=None, h_out=None, stream=None):
-        """(y, h): h is x itself without a residual; y is None if it is not asked for (`y` false), `kept` alone then
-        holds it. `out`: a tensor for y, `h_out`: for h."""
+        """(y, h): h is x itself without a residual (which is gone if y takes its place, and with it the backward call's h);
+        y is None if it is not asked for (`y` false), `kept` alone then holds it. `out`: a tensor for y, `h_out`: for h. A
+        row whose h holds an infinity or a NaN is NaN throughout."""
         if x.requires_grad or weight.requires_grad or (residual is not None and residual.requires_grad):
             _refuse_grad(x=x, weight=weight, **({} if residual is None else {"residual": residual}))
         key = ("y", x.shape, x.stride(), x.dtype, x.get_device(), weight.shape, weight.stride(), weight.dtype,

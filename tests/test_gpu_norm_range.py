@@ -45,7 +45,7 @@ def scaled(cols, dtype, power):
 
 @pytest.mark.parametrize("dtype,power,eps", [("bf16", 57, 1e-6), ("bf16", 63, 1e-6), ("bf16", 90, 1.0), ("bf16", 127, 1e-6), ("f32", 60, 1e-6),
                                              ("f32", 63, 0.0), ("f32", 64, 1e-6), ("f32", 126, 1e30), ("f32", 64, 3e38), ("f32", 63, 3e38),
-                                             ("bf16", -52, 0.0), ("bf16", -70, 0.0), ("f32", -60, 0.0), ("f32", -110, 0.0),
+                                             ("bf16", -52, 0.0), ("bf16", -70, 0.0), ("f32", -60, 0.0), ("f32", -110, 0.0), ("f32", -119, 0.0),
                                              ("f32", -60, 1e-35), ("f32", -20, 1e-12), ("f32", -45, 1e-27)])
 @pytest.mark.parametrize("cols", WIDTHS)
 def test_large_and_small_rows(cols, dtype, power, eps):
